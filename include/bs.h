@@ -466,6 +466,83 @@ bs_status bs_fw_gemv(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, ui
  * last bits. Enqueued on stream. */
 bs_status bs_fw_gemm(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, uint32_t* d_err, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * AdamW over many tensors at once: the step that trains adapters beside a coded projection, or a
+ * whole layer whose BF16 words bs_encoder_* then codes. The cards have no counterpart; this is
+ * this library's design. All device memory belongs to the caller.
+ *   g = clip * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g g
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * The moments m and v are held in 32 bits, or in 8 bits with a FP32 scale for each block of
+ * BS_ADAMW_BLOCK elements of a tensor (the last block may be short):
+ *   m: e4m3 (sign, 4 exponent bits of bias 7, 3 fraction bits), value code * scale; the scale is
+ *      the block's largest |m| / 448;
+ *   v: 5 exponent bits of bias 15 and 3 fraction bits (no sign; code << 7 is the half-precision
+ *      number), value code * scale; the scale is the block's largest v / 61440. A v above zero
+ *      keeps a code above zero.
+ *   A block whose largest magnitude is below 2^-100 is held as zero. A block with a NaN or an
+ *   infinity in it becomes NaN.
+ * A value y between two codes is rounded up where floor(fraction left * 2^16) + u reaches 2^16,
+ * with u 16 random bits: for step t of tensor k (its place in the call) and its element e, of
+ * z = mix(key + 0x9E3779B97F4A7C15 (e / 2 + 1)), key = mix(mix(seed + 2654435769 t) + k) with
+ * mix the output function of splitmix64, the low 32 bits for even e and the high ones for odd e;
+ * their low half rounds m and their high half v. So a step repeats bit for bit.
+ * ------------------------------------------------------------------------------------ */
+#define BS_TYPE_F32 0u
+#define BS_TYPE_BF16 1u
+#define BS_ADAMW_BLOCK 256
+
+typedef struct {
+    void* d_param;       /* n elements of param_type; updated */
+    const void* d_grad;  /* n elements of grad_type */
+    float* d_master;     /* NULL, or n FP32 elements: the step is taken from and kept in them, and
+                          * d_param receives them rounded to nearest */
+    void* d_m;           /* n FP32 elements, or n 8-bit codes; zero before the first step */
+    void* d_v;           /* the same */
+    float* d_m_scale;    /* 8 bits: ceil(n / BS_ADAMW_BLOCK) scales; 32 bits: NULL */
+    float* d_v_scale;
+    uint64_t n;          /* elements, at most 2^38 */
+    uint32_t param_type; /* BS_TYPE_* */
+    uint32_t grad_type;
+    float weight_decay;
+    uint32_t reserved;
+} bs_adamw_item;
+
+/* Device memory, 16-byte aligned: what a step reads on the device, so that a captured graph sees
+ * new values. The caller sets lr, and clip = 1 and the rest 0 before the first use. */
+typedef struct {
+    float lr;
+    float clip;        /* factor on every gradient; bs_grad_norm writes it */
+    int32_t step;      /* completed steps; bs_adamw counts on */
+    uint32_t skip;     /* nonzero: bs_adamw changes nothing, the step count included */
+    float norm;        /* of the last bs_grad_norm */
+    uint32_t arrived;  /* internal, 0 between calls */
+    uint32_t reserved[2];
+} bs_adamw_ctl;
+
+typedef struct {
+    double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0 */
+    uint32_t bits;            /* 32 or 8: how d_m and d_v are held */
+    uint32_t reserved;        /* 0 */
+    uint64_t seed;            /* of the 8-bit rounding */
+} bs_adamw_params;
+
+/* Scratch bytes of bs_grad_norm for these items; 0 if an item is invalid. */
+size_t bs_grad_norm_scratch_bytes(int32_t n, const bs_adamw_item* items);
+/* The 2-norm of all the items' gradients (only d_grad, n and grad_type are used), summed in a fixed
+ * order: d_ctl->norm = norm, d_ctl->clip = min(1, max_norm / (norm + 1e-6)) (max_norm above 0, may be
+ * infinite), d_ctl->skip = 0. A norm that is not finite (a NaN or infinity in a gradient, or
+ * gradients whose squares leave the FP32 range) sets clip = 0 and skip = 1 instead, so that the step
+ * that follows is left out. d_scratch: 8-byte aligned. Enqueued on stream. */
+bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs_adamw_ctl* d_ctl, void* d_scratch,
+                       size_t scratch_bytes, void* stream);
+/* One step over every item. Pointers need their type's alignment (16 bytes, 8 for codes, are faster).
+ * The items' buffers must not overlap, but for empty items (n = 0). Two calls that share d_ctl must
+ * be ordered (one stream, or events). Enqueued on stream: one launch for 384 tensors. */
+bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_params* params, bs_adamw_ctl* d_ctl, void* stream);
+/* The values that 8-bit moments stand for, as FP32: d_m[k] and d_v[k] receive items[k].n values each
+ * (only d_m, d_v, their scales and n of an item are used). Enqueued on stream. */
+bs_status bs_adamw_read_states(int32_t n, const bs_adamw_item* items, float* const* d_m, float* const* d_v, void* stream);
+
 /* Diagnostics (this library's design). */
 const char* bs_status_str(bs_status s);
 int bs_last_cuda_error(void); /* the cudaError_t behind the last BS_E_CUDA on this thread */

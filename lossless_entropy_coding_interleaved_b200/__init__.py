@@ -15,6 +15,7 @@ The byte layout is the BF16RANS container, version 2.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 
@@ -81,6 +82,18 @@ class FwGemvItem(ctypes.Structure):
                 ("d_x", ctypes.c_void_p), ("d_y", ctypes.c_void_p)]
 
 
+class AdamWItem(ctypes.Structure):
+    """bs_adamw_item: one tensor of an AdamW step."""
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("d_param", "d_grad", "d_master", "d_m", "d_v", "d_m_scale", "d_v_scale")] +
+                [("n", ctypes.c_uint64), ("param_type", ctypes.c_uint32), ("grad_type", ctypes.c_uint32),
+                 ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_uint32)])
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("bits", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libbs.so is not built ({LIB_PATH}); run "
@@ -137,6 +150,14 @@ def _load():
     L.bs_fw_decode.argtypes = [i32, P, P, P, P, P, P]
     L.bs_fw_gemv.argtypes = [i32, ctypes.POINTER(FwGemvItem), ctypes.c_uint32, ctypes.c_uint32, P, P]
     L.bs_fw_gemm.argtypes = [i32, ctypes.POINTER(FwGemvItem), ctypes.c_uint32, P, P]
+    IT = ctypes.POINTER(AdamWItem)
+    L.bs_grad_norm_scratch_bytes.argtypes = [i32, IT]
+    L.bs_grad_norm_scratch_bytes.restype = sz
+    L.bs_grad_norm.argtypes = [i32, IT, ctypes.c_float, P, P, sz, P]
+    L.bs_adamw.argtypes = [i32, IT, ctypes.POINTER(AdamWParams), P, P]
+    L.bs_adamw_read_states.argtypes = [i32, IT, P, P, P]
+    for fn in ("bs_grad_norm", "bs_adamw", "bs_adamw_read_states"):
+        getattr(L, fn).restype = ctypes.c_int
     for fn in ("bs_fw_measure", "bs_fw_write", "bs_fw_parse", "bs_fw_decode", "bs_fw_gemv", "bs_fw_gemm"):
         getattr(L, fn).restype = ctypes.c_int
     for fn in ("bs_streamer_create", "bs_streamer_group_count", "bs_streamer_tensor_info_get", "bs_streamer_prefetch", "bs_streamer_acquire",
@@ -163,7 +184,7 @@ EXPORTS = ("bs_plan_workspace_bytes", "bs_plan_workspace_bytes_device", "bs_plan
            "bs_streamer_acquire",
            "bs_streamer_release", "bs_streamer_get_stats", "bs_streamer_check", "bs_streamer_destroy",
            "bs_fw_scratch_bytes", "bs_fw_measure", "bs_fw_write", "bs_fw_parse", "bs_fw_decode", "bs_fw_gemv",
-           "bs_fw_gemm")
+           "bs_fw_gemm", "bs_grad_norm_scratch_bytes", "bs_grad_norm", "bs_adamw", "bs_adamw_read_states")
 
 
 def decode_noalloc(container, d_container: torch.Tensor, idx: int, out: torch.Tensor, stream=None) -> torch.Tensor:
@@ -657,3 +678,143 @@ def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = F
         _check(lib.bs_fw_gemv(n, arr, batch or 1, FW_LAYOUTS_RESIDENT if layouts_resident else 0, err.data_ptr(),
                               _stream(stream)), "fw_gemv")
     return [p[5] for p in products]
+
+
+# ------------------------------------------------------------ AdamW over many tensors
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+ADAMW_BLOCK = 256  # elements that share a scale of the 8-bit moments
+
+
+def _flat_list(ts, what: str, n: int, sizes=None, dtypes=None, device=None) -> list:
+    """The list of n contiguous CUDA tensors on one device, checked."""
+    ts = list(ts)
+    if len(ts) != n:
+        raise BsError(E_ARG, "adamw", f"{what}: one tensor for each parameter")
+    for k, t in enumerate(ts):
+        if not t.is_cuda or not t.is_contiguous() or (device is not None and t.device != device):
+            raise BsError(E_ARG, "adamw", f"{what}[{k}]: a contiguous tensor on the parameters' device")
+        if dtypes is not None and t.dtype not in dtypes:
+            raise BsError(E_ARG, "adamw", f"{what}[{k}]: dtype {t.dtype}")
+        if sizes is not None and t.numel() != sizes[k]:
+            raise BsError(E_ARG, "adamw", f"{what}[{k}]: {t.numel()} elements, not {sizes[k]}")
+    return ts
+
+
+class AdamW:
+    """AdamW over many tensors in one launch (bs_adamw), with the moments in 32 or in 8 bits.
+
+    params and grads: lists of contiguous CUDA tensors (float32 or bfloat16, mixed as they come);
+    the handle keeps both, and step() reads the gradients that stand in the grads' buffers then.
+    masters: float32 copies of the parameters, in which the step is taken (else a bfloat16 parameter
+    is rounded to nearest each step). weight_decay: a number, or one for each tensor.
+    states: existing moments to go on with, (exp_avgs, exp_avg_sqs) in 32 bits, or
+    ((codes, scales), (codes, scales)) in 8 bits, each a list; they are updated in place. step: the
+    steps already done. clip: the factor on gradients where step() computes no norm.
+
+    The learning rate, the factor, the step count and the norm live on the device (``ctl``): set
+    ``lr`` and ``clip`` by attribute, read ``norm`` and ``steps`` as device tensors; a captured step
+    sees new values.
+    """
+
+    def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
+                 bits: int = 32, masters=None, seed: int = 0, step: int = 0, clip: float = 1.0, states=None):
+        params = list(params)
+        if not torch.cuda.is_available():
+            raise BsError(E_UNSUPPORTED, "adamw", "no CUDA device")
+        if not params:
+            raise BsError(E_ARG, "adamw", "no parameters")
+        if bits not in (8, 32):
+            raise BsError(E_ARG, "adamw", "bits: 8 or 32")
+        n, dev = len(params), params[0].device
+        sizes = [p.numel() for p in params]
+        both = (torch.float32, torch.bfloat16)
+        self.params = _flat_list(params, "params", n, None, both, dev)
+        self.grads = _flat_list(grads, "grads", n, sizes, both, dev)
+        self.masters = None if masters is None else _flat_list(masters, "masters", n, sizes, (torch.float32,), dev)
+        self.device, self.bits = dev, bits
+        blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if len(decay) != n:
+            raise BsError(E_ARG, "adamw", "weight_decay: one for each parameter")
+        if states is None:
+            z = lambda dt, of: [torch.zeros(k, dtype=dt, device=dev) for k in of]  # noqa: E731
+            states = ((z(torch.float32, sizes), z(torch.float32, sizes)) if bits == 32 else
+                      tuple((z(torch.uint8, sizes), z(torch.float32, blocks)) for _ in range(2)))
+        if bits == 32:
+            self.exp_avg, self.exp_avg_sq = (_flat_list(v, "states", n, sizes, (torch.float32,), dev) for v in states)
+            self.exp_avg_scale = self.exp_avg_sq_scale = None
+        else:
+            (m, ms), (v, vs) = states
+            self.exp_avg, self.exp_avg_sq = (_flat_list(c, "states", n, sizes, (torch.uint8,), dev) for c in (m, v))
+            self.exp_avg_scale, self.exp_avg_sq_scale = (_flat_list(c, "states", n, blocks, (torch.float32,), dev) for c in (ms, vs))
+        written = [t for ts in (self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+                   if ts is not None for t in ts]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise BsError(E_ARG, "adamw", "parameters, masters and moments must not overlap")
+        for g in self.grads:  # a gradient may be read by several items, but not written by any
+            lo, hi = g.data_ptr(), g.data_ptr() + g.numel() * g.element_size()
+            at = bisect.bisect_left(spans, (hi,))
+            if g.numel() and at and spans[at - 1][1] > lo:
+                raise BsError(E_ARG, "adamw", "gradients must not overlap what the step writes")
+        self._items = (AdamWItem * n)()
+        ptr = lambda ts, k: ts[k].data_ptr() if ts is not None and sizes[k] else None  # noqa: E731
+        for k in range(n):
+            it = self._items[k]
+            it.d_param, it.d_grad, it.d_master = ptr(self.params, k), ptr(self.grads, k), ptr(self.masters, k)
+            it.d_m, it.d_v = ptr(self.exp_avg, k), ptr(self.exp_avg_sq, k)
+            it.d_m_scale, it.d_v_scale = ptr(self.exp_avg_scale, k), ptr(self.exp_avg_sq_scale, k)
+            it.n, it.param_type, it.grad_type = sizes[k], _TYPES[self.params[k].dtype], _TYPES[self.grads[k].dtype]
+            it.weight_decay = decay[k]
+        self._n = n
+        self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
+        self.ctl = torch.zeros(8, dtype=torch.int32, device=dev)
+        f = self.ctl.view(torch.float32)
+        self._lr, self._clip, self.norm, self.steps = f[0], f[1], f[4], self.ctl[2]
+        self.lr, self.clip = lr, clip
+        self.steps.fill_(step)
+        self._scratch = torch.empty(max(8, lib.bs_grad_norm_scratch_bytes(n, self._items)), dtype=torch.uint8, device=dev)
+
+    @property
+    def lr(self):
+        return self._lr
+
+    @lr.setter
+    def lr(self, v):
+        self._lr.fill_(v)
+
+    @property
+    def clip(self):
+        return self._clip
+
+    @clip.setter
+    def clip(self, v):
+        self._clip.fill_(v)
+
+    def grad_norm(self, max_norm: float = float("inf"), stream=None) -> torch.Tensor:
+        """bs_grad_norm: the norm of all gradients as a device scalar; sets the factor of the next
+        step to min(1, max_norm / (norm + 1e-6)), or marks it to be left out if the norm is not finite."""
+        with torch.cuda.device(self.device):
+            _check(lib.bs_grad_norm(self._n, self._items, max_norm, self.ctl.data_ptr(), self._scratch.data_ptr(),
+                                    self._scratch.numel(), _stream(stream)), "grad_norm")
+        return self.norm
+
+    def step(self, max_norm: float | None = None, stream=None):
+        """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first."""
+        if max_norm is not None:
+            self.grad_norm(max_norm, stream)
+        with torch.cuda.device(self.device):
+            _check(lib.bs_adamw(self._n, self._items, ctypes.byref(self._prm), self.ctl.data_ptr(), _stream(stream)), "adamw")
+
+    def read_states(self, ms=None, vs=None, stream=None):
+        """The moments as float32 lists, (exp_avgs, exp_avg_sqs). 32-bit moments are returned as they
+        stand; 8-bit ones are decoded (bs_adamw_read_states) into ms and vs, or into new tensors."""
+        if self.bits == 32:
+            return self.exp_avg, self.exp_avg_sq
+        sizes = [p.numel() for p in self.params]
+        ms, vs = ([torch.empty(k, dtype=torch.float32, device=self.device) for k in sizes] if t is None else
+                  _flat_list(t, "read_states", self._n, sizes, (torch.float32,), self.device) for t in (ms, vs))
+        pm, pv = ((ctypes.c_void_p * self._n)(*[t.data_ptr() if t.numel() else None for t in ts]) for ts in (ms, vs))
+        with torch.cuda.device(self.device):
+            _check(lib.bs_adamw_read_states(self._n, self._items, pm, pv, _stream(stream)), "adamw_read_states")
+        return ms, vs
