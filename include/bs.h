@@ -467,6 +467,81 @@ bs_status bs_fw_gemv(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, ui
 bs_status bs_fw_gemm(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, uint32_t* d_err, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once beside a shared projection: every token of a batch
+ * may use an adapter of its own, while the projection itself stays coded (bs_fw_gemv, bs_fw_gemm).
+ * The cards have no counterpart; this is this library's design. With a = idx[t]:
+ *   forward:   h[t] = scale[a] A_a x[t],   y[t] = base[t] + B_a h[t]
+ *   backward:  g[t] = scale[a] B_a^T dy[t],   dx[t] = dx_base[t] + A_a^T g[t],
+ *              dA_a = sum_t g[t] x[t]^T,   dB_a = sum_t dy[t] h[t]^T
+ * base is the projection's own product, dx_base its own gradient; both may be the output itself.
+ * A token without an adapter keeps base (dx_base). An adapter uses the first ranks[a] of its
+ * rank_max rank rows: the rest of A and B is never read, and their gradients are 0.
+ * x, dy, A and B are BF16; y, dx and their bases FP32 or BF16; sums, h, g, dA and dB FP32 (h and g
+ * are kept in 24 bits). Sums are in a fixed order: the same call gives the same bits.
+ * All device memory belongs to the caller. Calls are enqueued on stream, launch nothing that
+ * depends on host-side values of the routing, and can be captured.
+ * ------------------------------------------------------------------------------------ */
+#define BS_TYPE_F32 0u
+#define BS_TYPE_BF16 1u
+/* Device bytes of the plan of a batch, and of h or g for one projection; 0 for bad arguments
+ * (tokens above 2^20, n_adapters outside 1..8192, rank_max not a multiple of 8 in 8..128). */
+size_t bs_lora_plan_bytes(uint32_t tokens, uint32_t n_adapters);
+size_t bs_lora_state_bytes(uint32_t tokens, uint32_t rank_max);
+/* The routing of a batch, once for all its projections: groups the tokens by adapter.
+ *   d_idx: an adapter per token; negative: none. An index past the adapters counts as none and
+ *          sets bit 2 (value 4) of *d_err (d_err may be NULL).
+ *   d_plan: 16-byte aligned. The plan holds no pointers; it stays valid until it is rewritten. */
+bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_t n_adapters, void* d_plan, size_t plan_bytes,
+                       uint32_t* d_err, void* stream);
+
+typedef struct {
+    uint32_t tokens, n_adapters; /* those of the plan */
+    uint32_t rank_max;           /* rank rows of the pools */
+    uint32_t reserved;           /* 0 */
+    const int32_t* d_ranks;      /* NULL (rank_max for all), or one for each adapter, 0..rank_max */
+    const float* d_scales;       /* NULL (1 for all), or one for each adapter */
+    const void* d_plan;
+} bs_lora_batch;
+
+/* One projection. Strides are in elements from one token to the next, at least the row's length.
+ * BF16 rows start on 16 bytes (strides a multiple of 8), FP32 rows too (a multiple of 4). */
+typedef struct {
+    const void* d_a;       /* [n_adapters][rank_max][cols], 16-byte aligned */
+    const void* d_b;       /* [n_adapters][rows][rank_max], 16-byte aligned */
+    uint32_t rows, cols;   /* multiples of 8, at most 2^24 */
+    uint32_t type;         /* BS_TYPE_* of base and y, or of dx_base and dx */
+    uint32_t reserved;     /* 0 */
+    const void* d_x;       /* [tokens][cols] */
+    uint64_t x_stride;
+    void* d_h;             /* bs_lora_state_bytes, 16-byte aligned: bs_lora_forward writes h,
+                            * bs_lora_backward of the same batch and plan reads it */
+    const void* d_base;    /* forward: NULL (0), or [tokens][rows], which may be d_y itself */
+    uint64_t base_stride;
+    void* d_y;             /* forward: [tokens][rows], or NULL: h only */
+    uint64_t y_stride;
+    const void* d_dy;      /* backward: [tokens][rows] */
+    uint64_t dy_stride;
+    void* d_g;             /* backward: bs_lora_state_bytes of workspace, as d_h */
+    const void* d_dx_base; /* backward: NULL (0), or [tokens][cols], which may be d_dx itself */
+    uint64_t dx_base_stride;
+    void* d_dx;            /* backward: [tokens][cols], or NULL: not wanted */
+    uint64_t dx_stride;
+    float* d_da;           /* backward: [n_adapters][rank_max][cols] */
+    float* d_db;           /* backward: [n_adapters][rows][rank_max] */
+} bs_lora_item;
+
+/* Every item's h and y. Outputs and states of one call must not overlap, nor an output its inputs
+ * (but for d_base == d_y with equal strides). */
+bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, void* stream);
+/* Every item's dx, dA and dB. Items that read the same x (q, k and v) may name the same d_dx, with
+ * the same base, strides, cols and type, within one run of 16 items: dx then receives base plus all
+ * their parts, rounded once.
+ * flags: 0: dA and dB are written whole, adapters without tokens as 0. BS_LORA_ACCUMULATE: they are
+ * added to, and those of adapters without tokens are left alone. */
+#define BS_LORA_ACCUMULATE 1u
+bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * AdamW over many tensors at once: the step that trains adapters beside a coded projection, or a
  * whole layer whose BF16 words bs_encoder_* then codes. The cards have no counterpart; this is
  * this library's design. All device memory belongs to the caller.
@@ -487,8 +562,6 @@ bs_status bs_fw_gemm(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, ui
  * mix the output function of splitmix64, the low 32 bits for even e and the high ones for odd e;
  * their low half rounds m and their high half v. So a step repeats bit for bit.
  * ------------------------------------------------------------------------------------ */
-#define BS_TYPE_F32 0u
-#define BS_TYPE_BF16 1u
 #define BS_ADAMW_BLOCK 256
 
 typedef struct {

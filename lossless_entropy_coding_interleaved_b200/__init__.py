@@ -82,6 +82,23 @@ class FwGemvItem(ctypes.Structure):
                 ("d_x", ctypes.c_void_p), ("d_y", ctypes.c_void_p)]
 
 
+class LoraItem(ctypes.Structure):
+    """bs_lora_item: one projection's adapters, inputs and outputs."""
+    _fields_ = [("d_a", ctypes.c_void_p), ("d_b", ctypes.c_void_p), ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("d_x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64),
+                ("d_h", ctypes.c_void_p), ("d_base", ctypes.c_void_p), ("base_stride", ctypes.c_uint64),
+                ("d_y", ctypes.c_void_p), ("y_stride", ctypes.c_uint64), ("d_dy", ctypes.c_void_p), ("dy_stride", ctypes.c_uint64),
+                ("d_g", ctypes.c_void_p), ("d_dx_base", ctypes.c_void_p), ("dx_base_stride", ctypes.c_uint64),
+                ("d_dx", ctypes.c_void_p), ("dx_stride", ctypes.c_uint64), ("d_da", ctypes.c_void_p), ("d_db", ctypes.c_void_p)]
+
+
+class LoraBatch(ctypes.Structure):
+    """bs_lora_batch: the batch that the items of one call share."""
+    _fields_ = [("tokens", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32), ("rank_max", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("d_ranks", ctypes.c_void_p), ("d_scales", ctypes.c_void_p),
+                ("d_plan", ctypes.c_void_p)]
+
+
 class AdamWItem(ctypes.Structure):
     """bs_adamw_item: one tensor of an AdamW step."""
     _fields_ = ([(k, ctypes.c_void_p) for k in ("d_param", "d_grad", "d_master", "d_m", "d_v", "d_m_scale", "d_v_scale")] +
@@ -150,6 +167,17 @@ def _load():
     L.bs_fw_decode.argtypes = [i32, P, P, P, P, P, P]
     L.bs_fw_gemv.argtypes = [i32, ctypes.POINTER(FwGemvItem), ctypes.c_uint32, ctypes.c_uint32, P, P]
     L.bs_fw_gemm.argtypes = [i32, ctypes.POINTER(FwGemvItem), ctypes.c_uint32, P, P]
+    LI, LB = ctypes.POINTER(LoraItem), ctypes.POINTER(LoraBatch)
+    u32 = ctypes.c_uint32
+    L.bs_lora_plan_bytes.argtypes = [u32, u32]
+    L.bs_lora_plan_bytes.restype = sz
+    L.bs_lora_state_bytes.argtypes = [u32, u32]
+    L.bs_lora_state_bytes.restype = sz
+    L.bs_lora_plan.argtypes = [P, u32, u32, P, sz, P, P]
+    L.bs_lora_forward.argtypes = [i32, LI, LB, P]
+    L.bs_lora_backward.argtypes = [i32, LI, LB, u32, P]
+    for fn in ("bs_lora_plan", "bs_lora_forward", "bs_lora_backward"):
+        getattr(L, fn).restype = ctypes.c_int
     IT = ctypes.POINTER(AdamWItem)
     L.bs_grad_norm_scratch_bytes.argtypes = [i32, IT]
     L.bs_grad_norm_scratch_bytes.restype = sz
@@ -184,7 +212,8 @@ EXPORTS = ("bs_plan_workspace_bytes", "bs_plan_workspace_bytes_device", "bs_plan
            "bs_streamer_acquire",
            "bs_streamer_release", "bs_streamer_get_stats", "bs_streamer_check", "bs_streamer_destroy",
            "bs_fw_scratch_bytes", "bs_fw_measure", "bs_fw_write", "bs_fw_parse", "bs_fw_decode", "bs_fw_gemv",
-           "bs_fw_gemm", "bs_grad_norm_scratch_bytes", "bs_grad_norm", "bs_adamw", "bs_adamw_read_states")
+           "bs_fw_gemm", "bs_lora_plan_bytes", "bs_lora_state_bytes", "bs_lora_plan", "bs_lora_forward", "bs_lora_backward",
+           "bs_grad_norm_scratch_bytes", "bs_grad_norm", "bs_adamw", "bs_adamw_read_states")
 
 
 def decode_noalloc(container, d_container: torch.Tensor, idx: int, out: torch.Tensor, stream=None) -> torch.Tensor:
@@ -680,8 +709,149 @@ def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = F
     return [p[5] for p in products]
 
 
-# ------------------------------------------------------------ AdamW over many tensors
+# ------------------------------------------------------------ low-rank adapters
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
+LORA_ACCUMULATE = 1
+
+
+class LoraPlan:
+    """The routing of a batch of ``tokens`` tokens to ``n_adapters`` adapters (bs_lora_plan), in
+    device memory. update(idx) sets it from an int32 CUDA tensor, an adapter per token (negative:
+    none); one plan serves every projection of the batch, and may be updated for the next batch."""
+
+    def __init__(self, tokens: int, n_adapters: int, device="cuda"):
+        if not torch.cuda.is_available():
+            raise BsError(E_UNSUPPORTED, "lora_plan", "no CUDA device")
+        nb = lib.bs_lora_plan_bytes(tokens, n_adapters) if 0 <= tokens < 2 ** 32 and 0 <= n_adapters < 2 ** 32 else 0
+        if nb == 0:
+            raise BsError(E_ARG, "lora_plan", "tokens up to 2^20, adapters 1..8192")
+        self.tokens, self.n_adapters = tokens, n_adapters
+        self.data = torch.zeros(nb, dtype=torch.uint8, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = self.data.device
+
+    def update(self, idx: torch.Tensor, stream=None) -> "LoraPlan":
+        """Enqueued on the stream. An index past the adapters counts as none and sets bit 2 of ``err``."""
+        if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.numel() != self.tokens or idx.device != self.device:
+            raise BsError(E_ARG, "lora_plan", "idx: one int32 for each token, contiguous, on the plan's device")
+        with torch.cuda.device(self.device):
+            _check(lib.bs_lora_plan(idx.data_ptr() if self.tokens else None, self.tokens, self.n_adapters, self.data.data_ptr(),
+                                    self.data.numel(), self.err.data_ptr(), _stream(stream)), "lora_plan")
+        return self
+
+
+class LoraAdapters:
+    """The adapters of one or more projections, each a pool over ``n`` adapters:
+
+    a[k]: bfloat16 [n, rank_max, cols_k] and b[k]: bfloat16 [n, rows_k, rank_max], contiguous; scales:
+    float32 [n] or None (1); ranks: int32 [n] or None (rank_max), the rank rows that each adapter
+    uses. The handle keeps the tensors and reads what stands in them at each call.
+
+    forward(plan, xs, ys, bases, state): ys[k][t] = bases[k][t] + B_a (scale_a A_a xs[k][t]); bases
+    None adds to ys in place, a None among them stands for 0; ys None leaves only the state behind.
+    backward(plan, xs, dys, state, das, dbs, dxs, dx_bases, work): das and dbs (float32, as the
+    pools) are written, or added to with accumulate; dxs[k] = dx_bases[k] + the adapters' part,
+    where entries of dxs that are the same tensor receive the sum of their parts. dx_bases None: 0.
+    xs and dys are bfloat16 [tokens, width], ys and dxs float32 or bfloat16, their bases of the same
+    type; rows may be strided. Beside fw_gemv and fw_gemm the outputs of those are the bases.
+    """
+
+    def __init__(self, a, b, scales: torch.Tensor | None = None, ranks: torch.Tensor | None = None):
+        a, b = list(a), list(b)
+        bad = lambda msg: BsError(E_ARG, "lora", msg)  # noqa: E731
+        if not a or len(a) != len(b):
+            raise bad("one a and one b for each projection")
+        self.n, self.rank_max = (a[0].shape[0], a[0].shape[1]) if a[0].dim() == 3 else (0, 0)
+        self.device = a[0].device
+        for x, y in zip(a, b):
+            if x.dim() != 3 or y.dim() != 3 or x.shape[:2] != (self.n, self.rank_max) or y.shape[::2] != (self.n, self.rank_max):
+                raise bad("a: [n, rank_max, cols], b: [n, rows, rank_max]")
+            if any(t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda or t.device != self.device for t in (x, y)):
+                raise bad("pools: contiguous bfloat16 CUDA tensors on one device")
+        for t, dt in ((scales, torch.float32), (ranks, torch.int32)):
+            if t is not None and (t.dtype != dt or t.numel() != self.n or not t.is_contiguous() or t.device != self.device):
+                raise bad(f"scales float32 and ranks int32: one for each of {self.n} adapters")
+        self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
+        self._n = len(a)
+        self._items = (LoraItem * self._n)()
+        for it, x, y in zip(self._items, a, b):
+            it.d_a, it.d_b, it.rows, it.cols = x.data_ptr(), y.data_ptr(), y.shape[1], x.shape[2]
+        self._batch = LoraBatch(0, self.n, self.rank_max, 0, ranks.data_ptr() if ranks is not None else None,
+                                scales.data_ptr() if scales is not None else None, None)
+
+    def state(self, tokens: int) -> list:
+        """Buffers for one batch: what forward leaves for backward, or backward's own workspace."""
+        nb = lib.bs_lora_state_bytes(tokens, self.rank_max) if 0 <= tokens < 2 ** 32 else 0
+        if nb == 0:
+            raise BsError(E_ARG, "lora", "tokens up to 2^20, rank_max a multiple of 8 in 8..128")
+        return [torch.empty(nb, dtype=torch.uint8, device=self.device) for _ in range(self._n)]
+
+    def _rows(self, t, width, dtypes, what, tokens):
+        if t.dim() != 2 or t.shape[0] != tokens or t.shape[1] != width or t.dtype not in dtypes or t.device != self.device or (
+                tokens and t.stride(1) != 1):
+            raise BsError(E_ARG, "lora", f"{what}: [{tokens}, {width}] of {dtypes}, rows contiguous, on the adapters' device")
+        return t.data_ptr(), width if tokens <= 1 else t.stride(0)
+
+    def _begin(self, plan, lists, states):
+        if plan.n_adapters != self.n or plan.device != self.device:
+            raise BsError(E_ARG, "lora", "the plan is of another set of adapters")
+        if any(len(v) != self._n for v in lists + states):
+            raise BsError(E_ARG, "lora", "one entry for each projection")
+        need = lib.bs_lora_state_bytes(plan.tokens, self.rank_max)
+        for v in states:
+            for t in v:
+                if t.dtype != torch.uint8 or t.device != self.device or t.numel() < need:
+                    raise BsError(E_SIZE, "lora", "a state is of another batch")
+        self._batch.tokens, self._batch.d_plan = plan.tokens, plan.data.data_ptr()
+
+    def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
+        xs = list(xs)
+        state = self.state(plan.tokens) if state is None else list(state)
+        ys = [None] * self._n if ys is None else list(ys)
+        bases = ys if bases is None else list(bases)
+        self._begin(plan, [xs, ys, bases], [state])
+        T, both = plan.tokens, (torch.float32, torch.bfloat16)
+        for it, x, y, base, h in zip(self._items, xs, ys, bases, state):
+            it.d_x, it.x_stride = self._rows(x, it.cols, (torch.bfloat16,), "x", T)
+            it.d_h, it.d_y, it.d_base, it.type = h.data_ptr(), None, None, 0
+            if y is not None:
+                it.d_y, it.y_stride = self._rows(y, it.rows, both, "y", T)
+                it.type = _TYPES[y.dtype]
+                if base is not None:
+                    it.d_base, it.base_stride = self._rows(base, it.rows, (y.dtype,), "base", T)
+        with torch.cuda.device(self.device):
+            _check(lib.bs_lora_forward(self._n, self._items, ctypes.byref(self._batch), _stream(stream)), "lora_forward")
+        return ys
+
+    def backward(self, plan: LoraPlan, xs, dys, state, das, dbs, dxs=None, dx_bases=None, work=None, accumulate: bool = False,
+                 stream=None):
+        xs, dys, das, dbs, state = list(xs), list(dys), list(das), list(dbs), list(state)
+        work = self.state(plan.tokens) if work is None else list(work)
+        dxs = [None] * self._n if dxs is None else list(dxs)
+        dx_bases = [None] * self._n if dx_bases is None else list(dx_bases)
+        self._begin(plan, [xs, dys, das, dbs, dxs, dx_bases], [state, work])
+        T, both = plan.tokens, (torch.float32, torch.bfloat16)
+        for it, a, b, x, dy, h, g, da, db, dx, base in zip(self._items, self.a, self.b, xs, dys, state, work, das, dbs, dxs, dx_bases):
+            it.d_x, it.x_stride = self._rows(x, it.cols, (torch.bfloat16,), "x", T)
+            it.d_dy, it.dy_stride = self._rows(dy, it.rows, (torch.bfloat16,), "dy", T)
+            for t, like in ((da, a), (db, b)):
+                if t.dtype != torch.float32 or t.shape != like.shape or not t.is_contiguous() or t.device != self.device:
+                    raise BsError(E_ARG, "lora", "das and dbs: contiguous float32, of the pools' shapes")
+            it.d_h, it.d_g, it.d_da, it.d_db = h.data_ptr(), g.data_ptr(), da.data_ptr(), db.data_ptr()
+            it.d_dx, it.d_dx_base, it.type = None, None, 0
+            it.dx_stride = it.dx_base_stride = 0
+            if dx is not None:
+                it.d_dx, it.dx_stride = self._rows(dx, it.cols, both, "dx", T)
+                it.type = _TYPES[dx.dtype]
+                if base is not None:
+                    it.d_dx_base, it.dx_base_stride = self._rows(base, it.cols, (dx.dtype,), "dx_base", T)
+        with torch.cuda.device(self.device):
+            _check(lib.bs_lora_backward(self._n, self._items, ctypes.byref(self._batch), LORA_ACCUMULATE if accumulate else 0,
+                                        _stream(stream)), "lora_backward")
+        return das, dbs, dxs
+
+
+# ------------------------------------------------------------ AdamW over many tensors
 ADAMW_BLOCK = 256  # elements that share a scale of the 8-bit moments
 
 

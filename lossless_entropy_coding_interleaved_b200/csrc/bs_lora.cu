@@ -1,0 +1,875 @@
+// bs_lora.cu -- low-rank adapters of many requests at once beside a shared projection, and their
+// gradients.
+//
+//   forward:  h[t] = s_a A_a x[t],  y[t] = base[t] + B_a h[t]           with a = idx[t]
+//   backward: g[t] = s_a B_a^T dy[t],  dx[t] = A_a^T g[t],
+//             dA_a = sum_t g[t] x[t]^T,  dB_a = sum_t dy[t] h[t]^T
+//
+// Every product has one side of the adapter's rank (8 to 128) and is bound by the bytes of its wide
+// side (x, y, dy, dx). lora_plan_kernel groups the tokens by adapter once a batch; the kernels
+// below take tiles of up to 128 tokens of one adapter, gathered through the plan:
+//   shrink: [128 tokens x K] times [K x rank] -> h or g. The K range is split over a cluster of
+//           CTAs, whose parts are added through distributed shared memory in a fixed order.
+//   expand: [128 tokens x rank] times [rank x 128 columns], added to base on the way to y or dx.
+//   outer:  [rank x tokens of an adapter] times [tokens x 128 columns] -> dA or dB; the tokens are
+//           split over a cluster in the same way.
+// x, dy and the weights are BF16, so their products are exact in FP32. h and g, FP32 sums, enter
+// the next product as three BF16 numbers each (24 bits, see split3): three small matrix
+// instructions in place of one lossy one, on a side where the tensor cores wait for memory.
+// The tensor cores' accumulation rounds towards zero, so chains of matrix instructions are kept
+// to 16 to 24 links and their sums added in FP32 outside.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "bs_lora.cuh"
+
+namespace bs {
+namespace {
+using namespace lora;
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------- plan
+// A stable counting sort by one CTA: W warps each take a contiguous run of tokens, count them per
+// bucket, and after a scan over buckets and warps put them in their places, 32 at a time; lanes of
+// the same bucket are ranked by their lane. No order depends on timing.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restrict__ idx, uint32_t tokens, uint32_t n,
+                                                         uint32_t* __restrict__ plan, uint32_t warps, uint32_t* err) {
+    extern __shared__ uint32_t sm[];
+    __shared__ uint32_t s_scan[3][32], s_carry[3];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, nb = n + 1; // buckets
+    uint32_t* hist = sm;                    // [warps][nb]
+    uint32_t* first = hist + warps * nb;    // [nb + 1] first place of each bucket
+    uint32_t* t128 = first + nb + 1;        // [nb + 1] first tile of each bucket
+    uint32_t* t8 = t128 + nb + 1;           // [nb + 1]
+    for (uint32_t i = tid; i < warps * nb; i += blockDim.x) hist[i] = 0;
+    if (tid < 3) s_carry[tid] = 0;
+    __syncthreads();
+    const uint32_t per = ((tokens + warps - 1) / warps + 31u) & ~31u;
+    const uint32_t b0 = min(warp * per, tokens), b1 = min(b0 + per, tokens);
+    bool bad = false;
+    auto bucket = [&](uint32_t t) {
+        const int32_t a = __ldg(idx + t);
+        bad |= a >= static_cast<int32_t>(n);
+        return a < 0 || a >= static_cast<int32_t>(n) ? n : static_cast<uint32_t>(a);
+    };
+    if (warp < warps)
+        for (uint32_t t = b0; t < b1; t += 32) {
+            const uint32_t a = t + lane < b1 ? bucket(t + lane) : nb;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+            if (a < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a] += __popc(same);
+            __syncwarp();
+        }
+    if (bad && err) atomicOr(err, 4u);
+    __syncthreads();
+    for (uint32_t a0 = 0; a0 < nb; a0 += blockDim.x) { // scan over buckets, a chunk at a time
+        const uint32_t a = a0 + tid;
+        uint32_t v[3] = {0, 0, 0};
+        if (a < nb) {
+            for (uint32_t w = 0; w < warps; ++w) {
+                const uint32_t c = hist[w * nb + a];
+                hist[w * nb + a] = v[0];
+                v[0] += c;
+            }
+            v[1] = (v[0] + kTile - 1) / kTile;
+            v[2] = (v[0] + kFew - 1) / kFew;
+        }
+        uint32_t own[3] = {v[0], v[1], v[2]};
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+#pragma unroll
+            for (uint32_t d = 1; d < 32; d <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v[q], d);
+                if (lane >= d) v[q] += u;
+            }
+            if (lane == 31) s_scan[q][warp] = v[q];
+        }
+        __syncthreads();
+        if (warp < 3) {
+            uint32_t u = lane < blockDim.x / 32 ? s_scan[warp][lane] : 0;
+#pragma unroll
+            for (uint32_t d = 1; d < 32; d <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, u, d);
+                if (lane >= d) u += up;
+            }
+            s_scan[warp][lane] = u; // inclusive over warps
+        }
+        __syncthreads();
+        if (a < nb) {
+            uint32_t* dst[3] = {first, t128, t8};
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                dst[q][a] = s_carry[q] + (warp ? s_scan[q][warp - 1] : 0) + v[q] - own[q];
+        }
+        __syncthreads();
+        if (tid < 3) s_carry[tid] += s_scan[tid][blockDim.x / 32 - 1];
+        __syncthreads();
+    }
+    const PlanAt o = plan_at(tokens, n);
+    if (tid == 0) {
+        first[nb] = s_carry[0];
+        t128[nb] = s_carry[1];
+        t8[nb] = s_carry[2];
+        const bool few = tokens <= kFewTokens;
+        plan[0] = t128[n];
+        plan[1] = t128[nb];
+        plan[2] = few ? t8[n] : 0;
+        plan[3] = few ? t8[nb] : 0;
+        plan[4] = tokens;
+        plan[5] = n;
+    }
+    __syncthreads();
+    for (uint32_t a = tid; a <= nb; a += blockDim.x) plan[o.begin + a] = first[a];
+    if (warp < warps)
+        for (uint32_t t = b0; t < b1; t += 32) {
+            const uint32_t a = t + lane < b1 ? bucket(t + lane) : nb;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+            uint32_t at = 0;
+            if (a < nb) at = first[a] + hist[warp * nb + a] + __popc(same & lanemask_lt());
+            __syncwarp();
+            if (a < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a] += __popc(same);
+            __syncwarp();
+            if (a < nb) plan[o.perm + at] = t + lane;
+        }
+    auto tiles = [&](const uint32_t* tb, uint32_t size, uint64_t at) {
+        for (uint32_t i = tid; i < tb[nb]; i += blockDim.x) {
+            uint32_t lo = 0, hi = nb - 1; // the last bucket whose first tile is at or before i
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi + 1) >> 1;
+                if (tb[mid] <= i) lo = mid;
+                else hi = mid - 1;
+            }
+            const uint32_t f = first[lo] + (i - tb[lo]) * size;
+            reinterpret_cast<uint4*>(plan + at)[i] = make_uint4(lo, f, min(size, first[lo + 1] - f), 0);
+        }
+    };
+    tiles(t128, kTile, o.tiles);
+    if (tokens <= kFewTokens) tiles(t8, kFew, o.few);
+}
+
+// ---------------------------------------------------------------- what the tiled kernels share
+struct Batch {
+    uint32_t tokens, n, rank_max, part_stride; // part_stride: elements of one of the three parts
+    const uint32_t* plan;
+    const int32_t* ranks;  // nullptr: every adapter has rank_max
+    const float* scales;   // nullptr: 1
+};
+__device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
+    if (!b.ranks) return b.rank_max;
+    const int32_t r = __ldg(b.ranks + a);
+    return r < 0 ? 0u : min(static_cast<uint32_t>(r), b.rank_max);
+}
+
+constexpr int kTiledThreads = 256;
+// Rows in shared memory are padded by 16 bytes, so that the 8 rows of an 8 x 8 matrix lie in
+// different banks for every rank.
+template <int BYTES>
+constexpr uint32_t padded = BYTES + 16;
+
+struct ShrinkJob {
+    const uint16_t* src; // [tokens][stride]: x or dy
+    const uint16_t* w;   // A [n][rank_max][width], or B [n][width][rank_max]
+    uint16_t* out;       // three parts of [tokens][R], in the plan's order
+    uint64_t stride;
+    uint32_t width, pad;
+};
+struct ShrinkParams {
+    Batch b;
+    uint32_t split; // CTAs of a cluster
+    uint32_t pad;
+    ShrinkJob job[kMaxItems];
+};
+
+constexpr int kShrinkStages = 3;
+template <int R, bool WT>
+__host__ __device__ constexpr uint32_t shrink_stage() { return kTile * padded<128> + (WT ? 64 * padded<2 * R> : R * padded<128>); }
+template <int R, bool WT>
+constexpr uint32_t shrink_smem() {
+    return std::max<uint32_t>(kShrinkStages * shrink_stage<R, WT>(), kTile * (R + 4) * 4);
+}
+
+// WT: the weights' rank index is the contiguous one (B), else the summed index is (A).
+template <int R, bool WT>
+__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int WN = R == 16 ? 1 : 2, WM = 8 / WN, MT = 8 / WM, NT = R / WN / 8; // warps, 16-token and 8-rank tiles of a warp
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp % WM, wn = warp / WM;
+    const uint32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    if (tile >= p.b.plan[0]) return; // the whole cluster
+    const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[tile];
+    const ShrinkJob& job = p.job[blockIdx.y];
+    const uint32_t a = tl.x, first = tl.y, count = tl.z, rank = rank_of(p.b, a), K = job.width;
+    const uint32_t steps = (K + 63) / 64, per = (steps + p.split - 1) / p.split;
+    const uint32_t k_begin = min(part * per, steps), k_end = min(k_begin + per, steps);
+    // this thread's pieces: x rows tid / 8 + 32 i, 16 bytes at 8 (tid % 8) of the step's 64 columns
+    const uint32_t chunk = tid & 7u;
+    const uint16_t* xrow[4];
+    bool live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = (tid >> 3) + 32 * i;
+        live[i] = r < count;
+        xrow[i] = live[i] ? job.src + uint64_t(p.b.plan[o.perm + first + r]) * job.stride : job.src;
+    }
+    const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
+    const uint32_t s0 = smem_u32(smem);
+    constexpr uint32_t kStage = shrink_stage<R, WT>(), kW = kTile * padded<128>;
+    auto load = [&](uint32_t step) {
+        const uint32_t k = step * 64, sb = s0 + (step - k_begin) % kShrinkStages * kStage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool on = live[i] && k + 8 * chunk < K;
+            cp_async16(sb + ((tid >> 3) + 32 * i) * padded<128> + 16 * chunk, on ? xrow[i] + k + 8 * chunk : job.src, on ? 16u : 0u);
+        }
+        if (!WT) {
+#pragma unroll
+            for (uint32_t c = tid; c < R * 8; c += kTiledThreads) {
+                const uint32_t j = c >> 3, kc = k + 8 * (c & 7u);
+                const bool on = j < rank && kc < K;
+                cp_async16(sb + kW + j * padded<128> + 16 * (c & 7u), on ? w + uint64_t(j) * K + kc : job.w, on ? 16u : 0u);
+            }
+        } else {
+            constexpr uint32_t kC = R / 8; // pieces of a row
+#pragma unroll
+            for (uint32_t c = tid; c < 64 * kC; c += kTiledThreads) {
+                const uint32_t kr = c / kC, j = 8 * (c % kC);
+                const uint32_t bytes = k + kr < K && j < rank ? min(rank - j, 8u) * 2u : 0u;
+                cp_async16(sb + kW + kr * padded<2 * R> + 2 * j, bytes ? w + uint64_t(k + kr) * p.b.rank_max + j : job.w, bytes);
+            }
+        }
+    };
+    float sum[MT][NT][4] = {}, acc[MT][NT][4] = {};
+    for (uint32_t s = k_begin; s < k_begin + kShrinkStages - 1; ++s) {
+        if (s < k_end) load(s);
+        cp_async_commit();
+    }
+    for (uint32_t s = k_begin; s < k_end; ++s) {
+        cp_async_wait<kShrinkStages - 2>();
+        __syncthreads();
+        if (s + kShrinkStages - 1 < k_end) load(s + kShrinkStages - 1);
+        cp_async_commit();
+        const uint32_t sb = s0 + (s - k_begin) % kShrinkStages * kStage;
+#pragma unroll
+        for (uint32_t kk = 0; kk < 4; ++kk) {
+            uint32_t af[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                ldsm4(af[m], sb + (wm * MT * 16 + m * 16 + (lane & 15u)) * padded<128> + 16 * (2 * kk + (lane >> 4)));
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t bf[4];
+                const uint32_t j = wn * NT * 8 + n * 8;
+                if (!WT) ldsm4(bf, sb + kW + (j + (lane & 7u) + ((lane >> 4) << 3)) * padded<128> + 16 * (2 * kk + ((lane >> 3) & 1u)));
+                else ldsm4t(bf, sb + kW + (kk * 16 + (lane & 15u)) * padded<2 * R> + 2 * (j + 8 * (lane >> 4)));
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma16816(acc[m][n], af[m], bf[0], bf[1]);
+                    mma16816(acc[m][n + 1], af[m], bf[2], bf[3]);
+                }
+            }
+        }
+        if (((s - k_begin) & 3u) == 3u || s + 1 == k_end) { // 16 matrix instructions long
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) { sum[m][n][q] += acc[m][n][q]; acc[m][n][q] = 0.f; }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem); // [128][R + 4]
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t r = wm * MT * 16 + m * 16 + (lane >> 2), c = wn * NT * 8 + n * 8 + 2 * (lane & 3u);
+            *reinterpret_cast<float2*>(red + r * (R + 4) + c) = make_float2(sum[m][n][0], sum[m][n][1]);
+            *reinterpret_cast<float2*>(red + (r + 8) * (R + 4) + c) = make_float2(sum[m][n][2], sum[m][n][3]);
+        }
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
+    const uint32_t rows = kTile / p.split; // rows that this CTA adds up and writes
+    for (uint32_t i = tid; i < rows * (R / 8); i += kTiledThreads) {
+        const uint32_t r = part * rows + i / (R / 8), c = 8 * (i % (R / 8));
+        if (r >= count) continue;
+        float v[8] = {};
+        for (uint32_t q = 0; q < p.split; ++q) {
+            const float* src = cluster.map_shared_rank(red, q) + r * (R + 4) + c;
+            const float4 lo = *reinterpret_cast<const float4*>(src), hi = *reinterpret_cast<const float4*>(src + 4);
+            v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+            v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        }
+        uint32_t w3[3][4] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t q[3];
+            split3(c + j < rank ? v[j] * scale : 0.f, q);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) w3[t][j >> 1] |= q[t] << (16 * (j & 1));
+        }
+        uint16_t* dst = job.out + uint64_t(first + r) * R + c;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+            *reinterpret_cast<uint4*>(dst + uint64_t(t) * p.b.part_stride) = make_uint4(w3[t][0], w3[t][1], w3[t][2], w3[t][3]);
+    }
+    cluster.sync(); // the peers may still read this CTA's sums
+}
+
+// ---------------------------------------------------------------- expand
+struct ExpandSrc {
+    const uint16_t* parts; // three parts of [tokens][R]
+    const uint16_t* w;     // B [n][width][rank_max], or A [n][rank_max][width]
+};
+struct ExpandJob {
+    const uint8_t* base; // nullptr: 0
+    uint8_t* out;
+    uint64_t base_stride, out_stride; // elements
+    uint32_t width;
+    uint32_t src, n_src; // sources whose products are added up
+    uint32_t bf16;       // type of base and out
+};
+struct ExpandParams {
+    Batch b;
+    uint32_t blocks; // blocks of 128 columns a CTA takes
+    uint32_t pad;
+    ExpandJob job[kMaxItems];
+    ExpandSrc src[kMaxItems];
+};
+template <int R, bool WT>
+__host__ __device__ constexpr uint32_t expand_w() { return WT ? R * padded<256> : 128 * padded<2 * R>; }
+template <int R, bool WT>
+constexpr uint32_t expand_smem() { return 3 * kTile * padded<2 * R> + 2 * expand_w<R, WT>(); }
+
+// WT: the weights' column index is the contiguous one (A), else the rank index is (B).
+template <int R, bool WT>
+__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp & 3u, wn = warp >> 2;
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    if (blockIdx.y >= p.b.plan[1]) return;
+    const ExpandJob& job = p.job[blockIdx.z];
+    const uint32_t N = job.width, blocks = (N + 127) / 128;
+    const uint32_t nb0 = blockIdx.x * p.blocks, nb1 = min(nb0 + p.blocks, blocks);
+    if (nb0 >= nb1) return;
+    const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[blockIdx.y];
+    const uint32_t a = tl.x, first = tl.y, count = tl.z;
+    const bool none = a >= p.b.n; // tokens without an adapter: base as it is
+    if (none && job.base == job.out && job.base_stride == job.out_stride) return;
+    const uint32_t rank = none ? 0u : rank_of(p.b, a);
+    const uint32_t s0 = smem_u32(smem);
+    constexpr uint32_t kPart = kTile * padded<2 * R>, kW0 = 3 * kPart, kWb = expand_w<R, WT>();
+    auto load_parts = [&](const ExpandSrc& s) {
+        constexpr uint32_t kC = R / 8;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+            for (uint32_t c = tid; c < kTile * kC; c += kTiledThreads) {
+                const uint32_t r = c / kC, j = 8 * (c % kC);
+                cp_async16(s0 + t * kPart + r * padded<2 * R> + 2 * j,
+                           s.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < count ? first + r : first) * R + j, r < count ? 16u : 0u);
+            }
+    };
+    auto load_w = [&](const ExpandSrc& s, uint32_t nb, uint32_t buf) {
+        const uint16_t* w = s.w + uint64_t(a) * p.b.rank_max * N;
+        const uint32_t sb = s0 + kW0 + buf * kWb;
+        if (!WT) {
+            constexpr uint32_t kC = R / 8;
+#pragma unroll
+            for (uint32_t c = tid; c < 128 * kC; c += kTiledThreads) {
+                const uint32_t n = c / kC, j = 8 * (c % kC);
+                const uint32_t bytes = nb * 128 + n < N && j < rank ? min(rank - j, 8u) * 2u : 0u;
+                cp_async16(sb + n * padded<2 * R> + 2 * j, bytes ? w + uint64_t(nb * 128 + n) * p.b.rank_max + j : s.w, bytes);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t c = tid; c < R * 16; c += kTiledThreads) {
+                const uint32_t j = c >> 4, n = nb * 128 + 8 * (c & 15u);
+                const bool on = j < rank && n < N;
+                cp_async16(sb + j * padded<256> + 16 * (c & 15u), on ? w + uint64_t(j) * N + n : s.w, on ? 16u : 0u);
+            }
+        }
+    };
+    // the steps: every block's sources, one after the other; step i's weights in buffer i % 2
+    const uint32_t n_src = none ? 0u : job.n_src, n_steps = (nb1 - nb0) * n_src;
+    if (n_steps) {
+        load_parts(p.src[job.src]);
+        load_w(p.src[job.src], nb0, 0);
+        cp_async_commit();
+    }
+    uint32_t tok[4]; // this thread's rows: lane / 4 + 8 i of the warp's 32
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = wm * 32 + 8 * i + (lane >> 2);
+        tok[i] = r < count ? p.b.plan[o.perm + first + r] : ~0u;
+    }
+    float acc[2][8][4] = {};
+    uint32_t step = 0;
+    for (uint32_t nb = nb0; nb < nb1; ++nb) {
+        for (uint32_t s = 0; s < n_src; ++s, ++step) {
+            if (n_src > 1 && step > 0) { // another source's parts take the place of the last one's
+                __syncthreads();
+                load_parts(p.src[job.src + s]);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+            if (step + 1 < n_steps) {
+                const uint32_t s2 = s + 1 < n_src ? s + 1 : 0;
+                load_w(p.src[job.src + s2], s2 ? nb : nb + 1, (step + 1) & 1u);
+            }
+            cp_async_commit();
+            const uint32_t sb = s0 + kW0 + (step & 1u) * kWb;
+#pragma unroll
+            for (uint32_t kk = 0; kk < R / 16; ++kk) {
+                if (kk * 16 >= rank) break;
+                uint32_t bf[4][4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint32_t c = wn * 64 + n * 16;
+                    if (!WT) ldsm4(bf[n], sb + (c + (lane & 7u) + ((lane >> 4) << 3)) * padded<2 * R> + 16 * (2 * kk + ((lane >> 3) & 1u)));
+                    else ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<256> + 2 * (c + 8 * (lane >> 4)));
+                }
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t af[4];
+                        ldsm4(af, s0 + t * kPart + (wm * 32 + m * 16 + (lane & 15u)) * padded<2 * R> + 16 * (2 * kk + (lane >> 4)));
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            mma16816(acc[m][2 * n], af, bf[n][0], bf[n][1]);
+                            mma16816(acc[m][2 * n + 1], af, bf[n][2], bf[n][3]);
+                        }
+                    }
+            }
+        }
+        const uint32_t c0 = nb * 128 + wn * 64 + 2 * (lane & 3u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (tok[i] == ~0u) continue;
+            const uint64_t bo = uint64_t(tok[i]) * job.base_stride + c0, oo = uint64_t(tok[i]) * job.out_stride + c0;
+            float2 v[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[n] = make_float2(0.f, 0.f);
+            if (job.base) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    if (c0 + 8 * n < N) {
+                        if (job.bf16) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(job.base + 2 * (bo + 8 * n));
+                            v[n] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+                        } else {
+                            v[n] = *reinterpret_cast<const float2*>(job.base + 4 * (bo + 8 * n));
+                        }
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (c0 + 8 * n < N) {
+                    const float x = v[n].x + acc[i >> 1][n][2 * (i & 1)], y = v[n].y + acc[i >> 1][n][2 * (i & 1) + 1];
+                    if (job.bf16) *reinterpret_cast<uint32_t*>(job.out + 2 * (oo + 8 * n)) = bf16_of(x) | (bf16_of(y) << 16);
+                    else *reinterpret_cast<float2*>(job.out + 4 * (oo + 8 * n)) = make_float2(x, y);
+                }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
+    }
+    cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------- outer
+struct OuterJob {
+    const uint16_t* src;   // [tokens][stride]: x or dy
+    const uint16_t* parts; // three parts of [tokens][R]: g or h
+    float* out;            // dA [n][rank_max][width], or dB [n][width][rank_max]
+    uint64_t stride;
+    uint32_t width, transposed;
+};
+struct OuterParams {
+    Batch b;
+    uint32_t split;
+    uint32_t accumulate; // add to out, adapters without tokens left as they are
+    OuterJob job[2 * kMaxItems];
+};
+constexpr int kOuterStages = 3;
+constexpr uint32_t kOuterTok = 32; // tokens of a step
+template <int R>
+__host__ __device__ constexpr uint32_t outer_stage() { return kOuterTok * padded<256> + 3 * kOuterTok * padded<2 * R>; }
+template <int R>
+constexpr uint32_t outer_smem() { return std::max<uint32_t>(kOuterStages * outer_stage<R>(), R * 132 * 4); }
+
+template <int R>
+__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int WM = R == 16 ? 1 : R / 32, WN = 8 / WM, MT = R / WM / 16, NT = 16 / WN; // warps, 16-rank and 8-column tiles
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp % WM, wn = warp / WM;
+    const uint32_t part = blockIdx.x % p.split, c0 = blockIdx.x / p.split * 128, a = blockIdx.y;
+    const OuterJob& job = p.job[blockIdx.z];
+    if (c0 >= job.width) return; // the whole cluster
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    const uint32_t t_begin = p.b.plan[o.begin + a], t_end = p.b.plan[o.begin + a + 1];
+    if (p.accumulate && t_begin == t_end) return;
+    const uint32_t steps = (t_end - t_begin + kOuterTok - 1) / kOuterTok, per = (steps + p.split - 1) / p.split;
+    const uint32_t s_begin = min(part * per, steps), s_end = min(s_begin + per, steps);
+    const uint32_t s0 = smem_u32(smem);
+    constexpr uint32_t kStage = outer_stage<R>(), kP = kOuterTok * padded<256>, kPart = kOuterTok * padded<2 * R>;
+    auto load = [&](uint32_t s) {
+        const uint32_t t0 = t_begin + s * kOuterTok, sb = s0 + (s - s_begin) % kOuterStages * kStage;
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) { // 32 rows of 16 pieces
+            const uint32_t r = (tid >> 4) + 16 * i, c = c0 + 8 * (tid & 15u);
+            const bool on = t0 + r < t_end && c < job.width;
+            cp_async16(sb + r * padded<256> + 16 * (tid & 15u), on ? job.src + uint64_t(p.b.plan[o.perm + t0 + r]) * job.stride + c : job.src,
+                       on ? 16u : 0u);
+        }
+        constexpr uint32_t kC = R / 8;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (uint32_t c = tid; c < kOuterTok * kC; c += kTiledThreads) {
+                const uint32_t r = c / kC, j = 8 * (c % kC);
+                const bool on = t0 + r < t_end;
+                cp_async16(sb + kP + t * kPart + r * padded<2 * R> + 2 * j,
+                           job.parts + uint64_t(t) * p.b.part_stride + uint64_t(on ? t0 + r : t_begin) * R + j, on ? 16u : 0u);
+            }
+    };
+    float sum[MT][NT][4] = {}, acc[MT][NT][4] = {};
+    for (uint32_t s = s_begin; s < s_begin + kOuterStages - 1; ++s) {
+        if (s < s_end) load(s);
+        cp_async_commit();
+    }
+    for (uint32_t s = s_begin; s < s_end; ++s) {
+        cp_async_wait<kOuterStages - 2>();
+        __syncthreads();
+        if (s + kOuterStages - 1 < s_end) load(s + kOuterStages - 1);
+        cp_async_commit();
+        const uint32_t sb = s0 + (s - s_begin) % kOuterStages * kStage;
+#pragma unroll
+        for (uint32_t kk = 0; kk < kOuterTok / 16; ++kk) {
+            uint32_t bf[NT / 2][4];
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n)
+                ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<256> + 2 * (wn * NT * 8 + n * 16 + 8 * (lane >> 4)));
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t af[4]; // the transpose of [tokens][ranks]: (ranks lo, tokens lo), (hi, lo), (lo, hi), (hi, hi)
+                    ldsm4t(af, sb + kP + t * kPart + (kk * 16 + (lane & 7u) + ((lane >> 4) << 3)) * padded<2 * R> +
+                                   2 * ((wm * MT + m) * 16 + 8 * ((lane >> 3) & 1u)));
+#pragma unroll
+                    for (int n = 0; n < NT / 2; ++n) {
+                        mma16816(acc[m][2 * n], af, bf[n][0], bf[n][1]);
+                        mma16816(acc[m][2 * n + 1], af, bf[n][2], bf[n][3]);
+                    }
+                }
+        }
+        if (((s - s_begin) & 3u) == 3u || s + 1 == s_end) { // 24 matrix instructions long
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) { sum[m][n][q] += acc[m][n][q]; acc[m][n][q] = 0.f; }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem); // [R][132]
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t j = (wm * MT + m) * 16 + (lane >> 2), c = (wn * NT + n) * 8 + 2 * (lane & 3u);
+            *reinterpret_cast<float2*>(red + j * 132 + c) = make_float2(sum[m][n][0], sum[m][n][1]);
+            *reinterpret_cast<float2*>(red + (j + 8) * 132 + c) = make_float2(sum[m][n][2], sum[m][n][3]);
+        }
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const uint32_t rm = p.b.rank_max, cols = min(128u, job.width - c0);
+    float* out = job.out + uint64_t(a) * rm * job.width;
+    if (!job.transposed) { // rows j = part, part + split, ..: 128 columns, one a thread
+        for (uint32_t i = tid; i < (rm - part + p.split - 1) / p.split * 128; i += kTiledThreads) {
+            const uint32_t j = part + (i >> 7) * p.split, c = i & 127u;
+            if (c >= cols) continue;
+            float v = 0.f;
+            for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[j * 132 + c];
+            float* d = out + uint64_t(j) * job.width + c0 + c;
+            *d = p.accumulate ? *d + v : v;
+        }
+    } else { // columns c = 128 part / split ..: rm ranks of each, contiguous
+        const uint32_t each = 128 / p.split;
+        for (uint32_t i = tid; i < each * rm; i += kTiledThreads) {
+            const uint32_t c = part * each + i / rm, j = i % rm;
+            if (c >= cols) continue;
+            float v = 0.f;
+            for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[j * 132 + c];
+            float* d = out + uint64_t(c0 + c) * rm + j;
+            *d = p.accumulate ? *d + v : v;
+        }
+    }
+    cluster.sync(); // the peers may still read this CTA's sums
+}
+
+// ---------------------------------------------------------------- host
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bs_status check_batch(const bs_lora_batch* b) {
+    if (!b || b->tokens > kMaxTokens || b->n_adapters < 1 || b->n_adapters > kMaxAdapters || b->reserved) return BS_E_ARG;
+    if (b->rank_max < 8 || b->rank_max > kMaxRank || b->rank_max % 8) return BS_E_ARG;
+    if (!b->d_plan || !aligned(b->d_plan, 16) || !aligned(b->d_ranks, 4) || !aligned(b->d_scales, 4)) return BS_E_ARG;
+    return BS_OK;
+}
+bs_status check_item(const bs_lora_item& t) {
+    if (t.rows < 8 || t.cols < 8 || t.rows % 8 || t.cols % 8 || t.rows > (1u << 24) || t.cols > (1u << 24)) return BS_E_ARG;
+    if (!t.d_a || !t.d_b || !aligned(t.d_a, 16) || !aligned(t.d_b, 16)) return BS_E_ARG;
+    if (t.type > BS_TYPE_BF16 || t.reserved) return BS_E_ARG;
+    return BS_OK;
+}
+bool row_ok(const void* p, uint64_t stride, uint32_t width) { // BF16 rows read 16 bytes at a time
+    return p && aligned(p, 16) && stride >= width && stride % 8 == 0 && stride <= (1ull << 32);
+}
+bool out_ok(const void* p, uint64_t stride, uint32_t width, uint32_t type) {
+    return p && aligned(p, 16) && stride >= width && stride % (type == BS_TYPE_BF16 ? 8 : 4) == 0 && stride <= (1ull << 32);
+}
+bs_status device_sms(int* sms) {
+    int dev = 0, major = 0, minor = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return major == 10 && minor == 0 ? BS_OK : BS_E_UNSUPPORTED;
+}
+Batch batch_of(const bs_lora_batch& b) {
+    Batch o;
+    o.tokens = b.tokens;
+    o.n = b.n_adapters;
+    o.rank_max = b.rank_max;
+    o.part_stride = b.tokens * padded_rank(b.rank_max); // below 2^27
+    o.plan = static_cast<const uint32_t*>(b.d_plan);
+    o.ranks = b.d_ranks;
+    o.scales = b.d_scales;
+    return o;
+}
+template <typename Params>
+bs_status launch(void (*fn)(const Params), dim3 grid, uint32_t smem, uint32_t cluster, cudaStream_t s, const Params& p) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_status(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kTiledThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fn, p);
+    count_launch();
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? BS_OK : cuda_status(e);
+}
+// CTAs of a cluster that share a sum: the least power of two up to 8 that fills the GPU
+uint32_t split_for(uint64_t ctas, uint32_t steps, int sms) {
+    uint32_t c = 1;
+    while (c < 8 && ctas * c < 2u * static_cast<uint32_t>(sms) && steps >= 4 * c) c *= 2;
+    return c;
+}
+
+template <bool WT>
+bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+    uint32_t steps = ~0u;
+    for (uint32_t k = 0; k < jobs; ++k) steps = std::min(steps, (p.job[k].width + 63) / 64);
+    const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
+    p.split = split_for(uint64_t(std::min(cap, (p.b.tokens + kTile - 1) / kTile)) * jobs, steps, sms);
+    const dim3 grid(cap * p.split, jobs);
+    switch (R) {
+    case 16: return launch(lora_shrink_kernel<16, WT>, grid, shrink_smem<16, WT>(), p.split, s, p);
+    case 32: return launch(lora_shrink_kernel<32, WT>, grid, shrink_smem<32, WT>(), p.split, s, p);
+    case 64: return launch(lora_shrink_kernel<64, WT>, grid, shrink_smem<64, WT>(), p.split, s, p);
+    default: return launch(lora_shrink_kernel<128, WT>, grid, shrink_smem<128, WT>(), p.split, s, p);
+    }
+}
+template <bool WT>
+bs_status launch_expand(ExpandParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+    uint32_t blocks = 1;
+    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
+    const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
+    // a CTA keeps its tokens' parts for up to 8 blocks, as long as 8 CTAs an SM are left
+    p.blocks = 1;
+    while (p.blocks < 8 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 8ull * sms) p.blocks *= 2;
+    const dim3 grid((blocks + p.blocks - 1) / p.blocks, cap, jobs);
+    switch (R) {
+    case 16: return launch(lora_expand_kernel<16, WT>, grid, expand_smem<16, WT>(), 1, s, p);
+    case 32: return launch(lora_expand_kernel<32, WT>, grid, expand_smem<32, WT>(), 1, s, p);
+    case 64: return launch(lora_expand_kernel<64, WT>, grid, expand_smem<64, WT>(), 1, s, p);
+    default: return launch(lora_expand_kernel<128, WT>, grid, expand_smem<128, WT>(), 1, s, p);
+    }
+}
+bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+    uint32_t blocks = 1;
+    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
+    p.split = split_for(uint64_t(blocks) * jobs * p.b.n, p.b.tokens / p.b.n / kOuterTok, sms);
+    const dim3 grid(blocks * p.split, p.b.n, jobs);
+    switch (R) {
+    case 16: return launch(lora_outer_kernel<16>, grid, outer_smem<16>(), p.split, s, p);
+    case 32: return launch(lora_outer_kernel<32>, grid, outer_smem<32>(), p.split, s, p);
+    case 64: return launch(lora_outer_kernel<64>, grid, outer_smem<64>(), p.split, s, p);
+    default: return launch(lora_outer_kernel<128>, grid, outer_smem<128>(), p.split, s, p);
+    }
+}
+
+} // namespace
+} // namespace bs
+
+using namespace bs;
+using namespace bs::lora;
+
+extern "C" size_t bs_lora_plan_bytes(uint32_t tokens, uint32_t n_adapters) {
+    if (tokens > kMaxTokens || n_adapters < 1 || n_adapters > kMaxAdapters) return 0;
+    return 4 * plan_at(tokens, n_adapters).words;
+}
+
+extern "C" size_t bs_lora_state_bytes(uint32_t tokens, uint32_t rank_max) {
+    if (tokens > kMaxTokens || rank_max < 8 || rank_max > kMaxRank || rank_max % 8) return 0;
+    return std::max<size_t>(16, size_t(6) * tokens * padded_rank(rank_max));
+}
+
+extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_t n_adapters, void* d_plan, size_t plan_bytes,
+                                  uint32_t* d_err, void* stream) {
+    const size_t need = bs_lora_plan_bytes(tokens, n_adapters);
+    if (need == 0) return BS_E_ARG;
+    if ((tokens && !d_idx) || !aligned(d_idx, 4) || !d_plan || !aligned(d_plan, 16) || !aligned(d_err, 4)) return BS_E_ARG;
+    if (plan_bytes < need) return BS_E_SIZE;
+    int sms = 148;
+    const bs_status st = device_sms(&sms);
+    if (st != BS_OK) return st;
+    // as many counting warps as their tables fit into shared memory, and as have tokens
+    const uint32_t nb = n_adapters + 1;
+    const uint32_t fit = 220 * 1024 / 4 / nb - 4;
+    const uint32_t warps = std::max(1u, std::min({32u, fit, (tokens + 31) / 32}));
+    const uint32_t smem = 4 * (warps * nb + 3 * (nb + 1));
+    cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_status(e);
+    lora_plan_kernel<<<1, 1024, smem, static_cast<cudaStream_t>(stream)>>>(d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
+    count_launch();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? BS_OK : cuda_status(e);
+}
+
+extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, void* stream) {
+    bs_status st = check_batch(batch);
+    if (st != BS_OK) return st;
+    if (n < 0 || (n > 0 && !items)) return BS_E_ARG;
+    for (int32_t k = 0; k < n; ++k) {
+        const bs_lora_item& t = items[k];
+        if ((st = check_item(t)) != BS_OK) return st;
+        if (batch->tokens == 0) continue;
+        if (!row_ok(t.d_x, t.x_stride, t.cols) || !t.d_h || !aligned(t.d_h, 16)) return BS_E_ARG;
+        if (t.d_y && !out_ok(t.d_y, t.y_stride, t.rows, t.type)) return BS_E_ARG;
+        for (int32_t q = 0; q < k; ++q) // two items that write the same memory
+            if (items[q].d_h == t.d_h || (t.d_y && items[q].d_y == t.d_y)) return BS_E_ARG;
+        if (t.d_base && (!t.d_y || !out_ok(t.d_base, t.base_stride, t.rows, t.type))) return BS_E_ARG;
+    }
+    int sms = 148;
+    if ((st = device_sms(&sms)) != BS_OK) return st;
+    if (n == 0 || batch->tokens == 0) return BS_OK;
+    const uint32_t R = padded_rank(batch->rank_max);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ShrinkParams sp;
+    ExpandParams ep;
+    sp.b = ep.b = batch_of(*batch);
+    for (int32_t k0 = 0; k0 < n; k0 += kMaxItems) {
+        const uint32_t m = static_cast<uint32_t>(std::min(n - k0, kMaxItems));
+        uint32_t outs = 0;
+        for (uint32_t k = 0; k < m; ++k) {
+            const bs_lora_item& t = items[k0 + k];
+            sp.job[k] = ShrinkJob{static_cast<const uint16_t*>(t.d_x), static_cast<const uint16_t*>(t.d_a),
+                                  static_cast<uint16_t*>(t.d_h), t.x_stride, t.cols, 0};
+            if (!t.d_y) continue;
+            ep.src[outs] = ExpandSrc{static_cast<const uint16_t*>(t.d_h), static_cast<const uint16_t*>(t.d_b)};
+            ep.job[outs] = ExpandJob{static_cast<const uint8_t*>(t.d_base), static_cast<uint8_t*>(t.d_y), t.base_stride, t.y_stride,
+                                     t.rows, outs, 1, t.type};
+            ++outs;
+        }
+        if ((st = launch_shrink<false>(sp, m, R, sms, s)) != BS_OK) return st;
+        if (outs && (st = launch_expand<false>(ep, outs, R, sms, s)) != BS_OK) return st;
+    }
+    return BS_OK;
+}
+
+extern "C" bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, uint32_t flags, void* stream) {
+    bs_status st = check_batch(batch);
+    if (st != BS_OK) return st;
+    if (n < 0 || (n > 0 && !items) || (flags & ~BS_LORA_ACCUMULATE)) return BS_E_ARG;
+    for (int32_t k = 0; k < n; ++k) {
+        const bs_lora_item& t = items[k];
+        if ((st = check_item(t)) != BS_OK) return st;
+        if (!t.d_da || !t.d_db || !aligned(t.d_da, 16) || !aligned(t.d_db, 16)) return BS_E_ARG;
+        if (batch->tokens == 0) continue;
+        if (!row_ok(t.d_x, t.x_stride, t.cols) || !row_ok(t.d_dy, t.dy_stride, t.rows)) return BS_E_ARG;
+        if (!t.d_h || !t.d_g || !aligned(t.d_h, 16) || !aligned(t.d_g, 16)) return BS_E_ARG;
+        if (t.d_dx && !out_ok(t.d_dx, t.dx_stride, t.cols, t.type)) return BS_E_ARG;
+        if (t.d_dx_base && (!t.d_dx || !out_ok(t.d_dx_base, t.dx_base_stride, t.cols, t.type))) return BS_E_ARG;
+        for (int32_t q = 0; q < k; ++q) // two items that write the same memory
+            if (items[q].d_g == t.d_g || items[q].d_da == t.d_da || items[q].d_db == t.d_db) return BS_E_ARG;
+        // items that share dx share its base, strides and type too
+        for (int32_t q = 0; q < k; ++q)
+            if (t.d_dx && items[q].d_dx == t.d_dx &&
+                (items[q].d_dx_base != t.d_dx_base || items[q].dx_stride != t.dx_stride || items[q].dx_base_stride != t.dx_base_stride ||
+                 items[q].type != t.type || items[q].cols != t.cols || q / kMaxItems != k / kMaxItems))
+                return BS_E_ARG;
+    }
+    int sms = 148;
+    if ((st = device_sms(&sms)) != BS_OK) return st;
+    if (n == 0) return BS_OK;
+    const uint32_t R = padded_rank(batch->rank_max);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ShrinkParams sp;
+    ExpandParams ep;
+    OuterParams op;
+    sp.b = ep.b = op.b = batch_of(*batch);
+    op.accumulate = flags & BS_LORA_ACCUMULATE;
+    for (int32_t k0 = 0; k0 < n; k0 += kMaxItems) {
+        const uint32_t m = static_cast<uint32_t>(std::min(n - k0, kMaxItems));
+        uint32_t outs = 0, srcs = 0;
+        bool done[kMaxItems] = {};
+        for (uint32_t k = 0; k < m; ++k) {
+            const bs_lora_item& t = items[k0 + k];
+            sp.job[k] = ShrinkJob{static_cast<const uint16_t*>(t.d_dy), static_cast<const uint16_t*>(t.d_b),
+                                  static_cast<uint16_t*>(t.d_g), t.dy_stride, t.rows, 0};
+            op.job[2 * k] = OuterJob{static_cast<const uint16_t*>(t.d_x), static_cast<const uint16_t*>(t.d_g), t.d_da, t.x_stride, t.cols, 0};
+            op.job[2 * k + 1] = OuterJob{static_cast<const uint16_t*>(t.d_dy), static_cast<const uint16_t*>(t.d_h), t.d_db, t.dy_stride, t.rows, 1};
+            if (!t.d_dx || done[k]) continue;
+            ExpandJob& e = ep.job[outs++];
+            e = ExpandJob{static_cast<const uint8_t*>(t.d_dx_base), static_cast<uint8_t*>(t.d_dx), t.dx_base_stride, t.dx_stride,
+                          t.cols, srcs, 0, t.type};
+            for (uint32_t q = k; q < m; ++q) // every item with this dx is a source of it
+                if (items[k0 + q].d_dx == t.d_dx) {
+                    done[q] = true;
+                    ep.src[srcs++] = ExpandSrc{static_cast<const uint16_t*>(items[k0 + q].d_g), static_cast<const uint16_t*>(items[k0 + q].d_a)};
+                    ++e.n_src;
+                }
+        }
+        if (batch->tokens) {
+            if ((st = launch_shrink<true>(sp, m, R, sms, s)) != BS_OK) return st;
+            if (outs && (st = launch_expand<true>(ep, outs, R, sms, s)) != BS_OK) return st;
+        }
+        if ((st = launch_outer(op, 2 * m, R, sms, s)) != BS_OK) return st;
+    }
+    return BS_OK;
+}

@@ -1,0 +1,79 @@
+// bs_lora.cuh -- definitions shared by the kernels of the low-rank adapters (bs_lora*.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bs_device.cuh"
+#include "bs_host.h"
+#include "bs_internal.h"
+
+namespace bs {
+namespace lora {
+
+constexpr uint32_t kMaxTokens = 1u << 20, kMaxAdapters = 8192, kMaxRank = 128;
+constexpr uint32_t kTile = 128;   // tokens of one adapter that a CTA of the tiled kernels takes
+constexpr uint32_t kFew = 8;      // the same for the decoding kernel
+constexpr uint32_t kFewTokens = 1024; // the largest batch whose plan lists tiles of kFew tokens
+constexpr int kMaxItems = 16;     // projections of one launch
+
+// The plan of a batch, in 32-bit words: the tokens sorted by adapter, those without one last
+// (bucket n_adapters), each adapter's tokens in their own order.
+//   [0] tiles of kTile tokens that have an adapter, [1] all tiles of kTile (those without an
+//   adapter follow), [2] and [3] the same for kFew (0 above kFewTokens), [4] tokens, [5] adapters
+//   begin[n_adapters + 2]: the first place of each bucket, then the end
+//   perm[tokens]: the token at each place
+//   tiles, tiles of kFew: (bucket, first place, tokens, 0) each
+struct PlanAt {
+    uint64_t begin, perm, tiles, few, words;
+};
+__host__ __device__ inline uint32_t tile_cap(uint32_t tokens, uint32_t n, uint32_t size) {
+    const uint32_t most = tokens / size + n + 1; // every bucket ends in a part-filled tile
+    return most < tokens ? most : tokens;
+}
+__host__ __device__ inline PlanAt plan_at(uint32_t tokens, uint32_t n) {
+    PlanAt o;
+    auto up4 = [](uint64_t v) { return (v + 3) & ~uint64_t(3); };
+    o.begin = 16;
+    o.perm = o.begin + up4(n + 2);
+    o.tiles = o.perm + up4(tokens);
+    o.few = o.tiles + 4ull * tile_cap(tokens, n, kTile);
+    o.words = o.few + (tokens <= kFewTokens ? 4ull * tile_cap(tokens, n, kFew) : 0);
+    return o;
+}
+// Rank rows of the kernels: 16, 32, 64 or 128, the least that holds rank_max.
+inline uint32_t padded_rank(uint32_t rank_max) { return rank_max <= 16 ? 16 : rank_max <= 32 ? 32 : rank_max <= 64 ? 64 : 128; }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16_of(float f) { // to nearest, ties to even
+    uint32_t r;
+    asm("{\n .reg .b16 h;\n cvt.rn.bf16.f32 h, %1;\n mov.b32 %0, {h, 0};\n}" : "=r"(r) : "f"(f));
+    return r;
+}
+// The three BF16 numbers whose sum is f: each takes 8 bits of what the ones before it left, 24 in
+// all, so a rank-wide FP32 intermediate goes through the BF16 tensor cores without loss. What an
+// infinity or NaN leaves is taken as 0, not as the NaN of inf - inf.
+__device__ __forceinline__ void split3(float f, uint32_t (&q)[3]) {
+    q[0] = bf16_of(f);
+    const float h = __uint_as_float(q[0] << 16);
+    const float r1 = (q[0] & 0x7F80u) == 0x7F80u ? 0.f : f - h;
+    q[1] = bf16_of(r1);
+    const float r2 = r1 - __uint_as_float(q[1] << 16);
+    q[2] = bf16_of(r2);
+}
+
+} // namespace lora
+} // namespace bs

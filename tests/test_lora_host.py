@@ -1,0 +1,84 @@
+"""CPU checks of the adapters' entry points: sizes, and refusals before any launch."""
+import ctypes
+
+import pytest
+
+bs = pytest.importorskip("lossless_entropy_coding_interleaved_b200")
+L = bs.lib
+
+
+def _item(**kw):
+    it = bs.LoraItem(d_a=256, d_b=512, rows=64, cols=128, d_x=1024, x_stride=128, d_h=2048, d_y=4096, y_stride=64,
+                     d_dy=8192, dy_stride=64, d_g=16384, d_da=32768, d_db=65536)
+    for k, v in kw.items():
+        setattr(it, k, v)
+    return it
+
+
+def _batch(**kw):
+    b = bs.LoraBatch(10, 4, 16, 0, None, None, 256)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return b
+
+
+def _forward(items, batch=None):
+    arr = (bs.LoraItem * max(1, len(items)))(*items)
+    return L.bs_lora_forward(len(items), arr, ctypes.byref(batch or _batch()), None)
+
+
+def _backward(items, batch=None, flags=0):
+    arr = (bs.LoraItem * max(1, len(items)))(*items)
+    return L.bs_lora_backward(len(items), arr, ctypes.byref(batch or _batch()), flags, None)
+
+
+def test_sizes():
+    assert L.bs_lora_plan_bytes(0, 1) > 0 and L.bs_lora_plan_bytes(1 << 20, 8192) > 4 << 20
+    for t, n in (((1 << 20) + 1, 1), (5, 0), (5, 8193)):
+        assert L.bs_lora_plan_bytes(t, n) == 0
+    assert [L.bs_lora_state_bytes(10, r) for r in (8, 16, 24, 32, 40, 64, 72, 128)] == [60 * p for p in (16, 16, 32, 32, 64, 64, 128, 128)]
+    assert L.bs_lora_state_bytes(0, 8) > 0
+    for t, r in (((1 << 20) + 1, 8), (5, 0), (5, 4), (5, 12), (5, 136)):
+        assert L.bs_lora_state_bytes(t, r) == 0
+
+
+def test_plan_refusals_before_any_launch():
+    need = L.bs_lora_plan_bytes(10, 4)
+    plan = lambda idx=256, t=10, n=4, p=256, b=need, e=None: L.bs_lora_plan(idx, t, n, p, b, e, None)  # noqa: E731
+    assert plan(idx=None) == bs.E_ARG and plan(idx=258) == bs.E_ARG and plan(p=None) == bs.E_ARG and plan(p=264) == bs.E_ARG
+    assert plan(n=0) == bs.E_ARG and plan(t=(1 << 20) + 1) == bs.E_ARG and plan(e=2) == bs.E_ARG and plan(b=need - 1) == bs.E_SIZE
+
+
+def test_batch_refusals_before_any_launch():
+    for b in (_batch(tokens=(1 << 20) + 1), _batch(n_adapters=0), _batch(n_adapters=8193), _batch(rank_max=0), _batch(rank_max=12),
+              _batch(rank_max=136), _batch(reserved=1), _batch(d_plan=None), _batch(d_plan=8), _batch(d_ranks=2), _batch(d_scales=1)):
+        assert _forward([_item()], b) == bs.E_ARG and _backward([_item()], b) == bs.E_ARG
+    assert L.bs_lora_forward(1, None, ctypes.byref(_batch()), None) == bs.E_ARG
+    assert L.bs_lora_forward(-1, ctypes.byref(_item()), ctypes.byref(_batch()), None) == bs.E_ARG
+    assert L.bs_lora_backward(0, None, None, 0, None) == bs.E_ARG
+
+
+def test_item_refusals_before_any_launch():
+    common = [dict(d_a=None), dict(d_a=264), dict(d_b=None), dict(d_b=520), dict(rows=0), dict(rows=60), dict(cols=4), dict(cols=130),
+              dict(rows=(1 << 24) + 8), dict(type=2), dict(reserved=1), dict(d_x=None), dict(d_x=1026), dict(x_stride=120),
+              dict(x_stride=132), dict(d_h=None), dict(d_h=2056)]
+    for kw in common + [dict(d_y=4100), dict(y_stride=56), dict(y_stride=66), dict(type=1, y_stride=68), dict(d_base=4100, base_stride=64),
+                        dict(d_base=4096, base_stride=60), dict(d_y=None, d_base=4096, base_stride=64)]:
+        assert _forward([_item(**kw)]) == bs.E_ARG, kw
+    for kw in common + [dict(d_dy=None), dict(d_dy=8194), dict(dy_stride=56), dict(dy_stride=68), dict(d_g=None), dict(d_g=8),
+                        dict(d_da=None), dict(d_db=None), dict(d_da=32772), dict(d_dx=4104, dx_stride=128), dict(d_dx=4096, dx_stride=64),
+                        dict(d_dx=4096, dx_stride=130), dict(d_dx_base=4096, dx_base_stride=128)]:
+        assert _backward([_item(**kw)]) == bs.E_ARG, kw
+    assert _backward([_item()], flags=2) == bs.E_ARG
+
+
+def test_two_items_of_one_call_may_not_write_the_same_memory():
+    other = dict(d_h=1 << 20, d_y=1 << 21, d_g=1 << 22, d_da=1 << 23, d_db=1 << 24)
+    for k in ("d_h", "d_y"):
+        assert _forward([_item(), _item(**{**other, k: getattr(_item(), k)})]) == bs.E_ARG, k
+    for k in ("d_g", "d_da", "d_db"):
+        assert _backward([_item(), _item(**{**other, k: getattr(_item(), k)})]) == bs.E_ARG, k
+    # one dx for two items has to be described alike
+    dx = dict(d_dx=1 << 25, dx_stride=128)
+    for kw in (dict(dx_stride=136), dict(type=1), dict(d_dx_base=1 << 26, dx_base_stride=128)):
+        assert _backward([_item(**dx), _item(**{**other, **dx, **kw})]) == bs.E_ARG, kw
