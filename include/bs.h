@@ -573,7 +573,7 @@ typedef struct {
     void* d_v;           /* the same */
     float* d_m_scale;    /* 8 bits: ceil(n / BS_ADAMW_BLOCK) scales; 32 bits: NULL */
     float* d_v_scale;
-    uint64_t n;          /* elements, at most 2^38 */
+    uint64_t n;          /* elements, at most 2^34 */
     uint32_t param_type; /* BS_TYPE_* */
     uint32_t grad_type;
     float weight_decay;
@@ -585,7 +585,7 @@ typedef struct {
 typedef struct {
     float lr;
     float clip;        /* factor on every gradient; bs_grad_norm writes it */
-    int32_t step;      /* completed steps; bs_adamw counts on */
+    int32_t step;      /* completed steps: bs_adamw leaves its step's number */
     uint32_t skip;     /* nonzero: bs_adamw changes nothing, the step count included */
     float norm;        /* of the last bs_grad_norm */
     uint32_t arrived;  /* internal, 0 between calls */
@@ -595,7 +595,7 @@ typedef struct {
 typedef struct {
     double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0 */
     uint32_t bits;            /* 32 or 8: how d_m and d_v are held */
-    uint32_t reserved;        /* 0 */
+    uint32_t step;            /* 0: the step is number d_ctl->step + 1. Else its number, 1 .. 2^31 - 1 */
     uint64_t seed;            /* of the 8-bit rounding */
 } bs_adamw_params;
 
@@ -608,10 +608,15 @@ size_t bs_grad_norm_scratch_bytes(int32_t n, const bs_adamw_item* items);
  * that follows is left out. d_scratch: 8-byte aligned. Enqueued on stream. */
 bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs_adamw_ctl* d_ctl, void* d_scratch,
                        size_t scratch_bytes, void* stream);
-/* One step over every item. Pointers need their type's alignment (16 bytes, 8 for codes, are faster).
- * The items' buffers must not overlap, but for empty items (n = 0). Two calls that share d_ctl must
- * be ordered (one stream, or events). Enqueued on stream: one launch for 384 tensors. */
-bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_params* params, bs_adamw_ctl* d_ctl, void* stream);
+/* One step over every item. to: NULL, and the items are updated in place; or n items whose d_param,
+ * d_master, d_m, d_v and scales receive what the step makes of those of items, which stay as they are
+ * (with the same n, param_type and kinds of buffers). So the weights of a step can be coded for a
+ * checkpoint (bs_encoder_run needs them unchanged until bs_encoder_emit) while the next steps run. Pointers need their type's alignment (16 bytes, 8 for codes, are faster).
+ * Written buffers must not overlap each other nor anything that is read, but for an item's own in a
+ * step in place. Two calls that share d_ctl must be ordered (one stream, or events). Enqueued on
+ * stream: one launch for 250 tensors. */
+bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, const bs_adamw_params* params,
+                   bs_adamw_ctl* d_ctl, void* stream);
 /* The values that 8-bit moments stand for, as FP32: d_m[k] and d_v[k] receive items[k].n values each
  * (only d_m, d_v, their scales and n of an item are used). Enqueued on stream. */
 bs_status bs_adamw_read_states(int32_t n, const bs_adamw_item* items, float* const* d_m, float* const* d_v, void* stream);

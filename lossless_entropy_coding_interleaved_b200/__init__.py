@@ -108,7 +108,7 @@ class AdamWItem(ctypes.Structure):
 
 class AdamWParams(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
-                ("bits", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
+                ("bits", ctypes.c_uint32), ("step", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
 
 
 def _load():
@@ -182,7 +182,7 @@ def _load():
     L.bs_grad_norm_scratch_bytes.argtypes = [i32, IT]
     L.bs_grad_norm_scratch_bytes.restype = sz
     L.bs_grad_norm.argtypes = [i32, IT, ctypes.c_float, P, P, sz, P]
-    L.bs_adamw.argtypes = [i32, IT, ctypes.POINTER(AdamWParams), P, P]
+    L.bs_adamw.argtypes = [i32, IT, IT, ctypes.POINTER(AdamWParams), P, P]
     L.bs_adamw_read_states.argtypes = [i32, IT, P, P, P]
     for fn in ("bs_grad_norm", "bs_adamw", "bs_adamw_read_states"):
         getattr(L, fn).restype = ctypes.c_int
@@ -887,7 +887,7 @@ class AdamW:
     """
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
-                 bits: int = 32, masters=None, seed: int = 0, step: int = 0, clip: float = 1.0, states=None):
+                 bits: int = 32, masters=None, seed: int = 0, step: int = 0, clip: float = 1.0, states=None, _ctl=None):
         params = list(params)
         if not torch.cuda.is_available():
             raise BsError(E_UNSUPPORTED, "adamw", "no CUDA device")
@@ -938,9 +938,11 @@ class AdamW:
             it.weight_decay = decay[k]
         self._n = n
         self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
-        self.ctl = torch.zeros(8, dtype=torch.int32, device=dev)
+        self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
         self._lr, self._clip, self.norm, self.steps = f[0], f[1], f[4], self.ctl[2]
+        if _ctl is not None:
+            return
         self.lr, self.clip = lr, clip
         self.steps.fill_(step)
         self._scratch = torch.empty(max(8, lib.bs_grad_norm_scratch_bytes(n, self._items)), dtype=torch.uint8, device=dev)
@@ -969,12 +971,32 @@ class AdamW:
                                     self._scratch.numel(), _stream(stream)), "grad_norm")
         return self.norm
 
-    def step(self, max_norm: float | None = None, stream=None):
-        """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first."""
+    def twin(self, params=None, masters=None, states=None) -> "AdamW":
+        """A second set of parameters, masters and moments (new tensors where none are given) for the
+        same gradients and the same ctl: step(into=twin) leaves this handle's as they are, to be
+        coded or compared, and the twin's next step, into this one, goes on from there."""
+        new = lambda ts, given: (None if ts is None else list(given) if given is not None else [torch.empty_like(t) for t in ts])  # noqa: E731
+        if states is None:
+            m, v, ms, vs = (new(ts, None) for ts in (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))
+            states = (m, v) if self.bits == 32 else ((m, ms), (v, vs))
+        t = AdamW(new(self.params, params), self.grads, betas=(self._prm.beta1, self._prm.beta2), eps=self._prm.eps,
+                  weight_decay=[it.weight_decay for it in self._items], bits=self.bits, masters=new(self.masters, masters),
+                  seed=self._prm.seed, states=states, _ctl=self.ctl)
+        t._scratch = self._scratch
+        return t
+
+    def step(self, max_norm: float | None = None, into: "AdamW | None" = None, number: int = 0, stream=None):
+        """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first. into: a twin
+        that receives the results, while this handle's tensors stay as they are. number: the step's
+        number (from 1), instead of one more than the last one's."""
         if max_norm is not None:
             self.grad_norm(max_norm, stream)
+        if into is not None and into.ctl is not self.ctl:
+            raise BsError(E_ARG, "adamw", "into: a twin of this handle")
+        self._prm.step = number
         with torch.cuda.device(self.device):
-            _check(lib.bs_adamw(self._n, self._items, ctypes.byref(self._prm), self.ctl.data_ptr(), _stream(stream)), "adamw")
+            _check(lib.bs_adamw(self._n, self._items, into._items if into is not None else None, ctypes.byref(self._prm),
+                                self.ctl.data_ptr(), _stream(stream)), "adamw")
 
     def read_states(self, ms=None, vs=None, stream=None):
         """The moments as float32 lists, (exp_avgs, exp_avg_sqs). 32-bit moments are returned as they

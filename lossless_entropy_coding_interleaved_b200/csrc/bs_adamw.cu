@@ -44,25 +44,30 @@ constexpr uint32_t kBlock = BS_ADAMW_BLOCK; // elements of a warp's group and of
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr float kTopM = 448.f, kTopV = 61440.f; // the formats' largest values
 constexpr float kDead = 7.8886090522101181e-31f; // 2^-100: a block below this counts as zero
-constexpr int kFewItems = 24, kManyItems = 384;
+constexpr int kFewItems = 16, kManyItems = 250;
 
-struct OptItem {
+struct OptOut { // where a step goes
     uint8_t *p, *m, *v;
-    const uint8_t* g;
     float *master, *ms, *vs;
+};
+struct OptItem {
+    const uint8_t *p, *m, *v, *g;
+    const float *master, *ms, *vs;
+    OptOut to;
     uint64_t n;
     uint32_t group_begin; // first 256-element group of this tensor in the launch
     float decay;
     uint32_t tensor;      // its number in the call
     uint32_t flags;       // kP16, kG16, kVec
 };
-static_assert(sizeof(OptItem) == 80, "OptItem layout");
+static_assert(sizeof(OptItem) == 128, "OptItem layout");
 constexpr uint32_t kP16 = 1, kG16 = 2, kVec = 4; // BF16 parameters, BF16 gradients, all pointers aligned for vectors
 
 template <int CAP>
 struct OptParams {
     uint32_t n_items, groups, per_cta; // groups of the launch, groups a CTA takes
     uint32_t last;                     // the call's last launch
+    uint32_t step;                     // the step's number, 0: one more than ctl->step
     float b1, b2, c1, c2, eps;         // c = 1 - b, rounded from 64 bits
     float max_norm;
     double log_b1, log_b2;
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const bool skip = ctl->skip != 0;
     if (!skip) {
         const float lr = ctl->lr, clip = ctl->clip;
-        const uint32_t t = static_cast<uint32_t>(ctl->step) + 1u;
+        const uint32_t t = p.step ? p.step : static_cast<uint32_t>(ctl->step) + 1u;
         // 1 - b^t = -expm1(t log b): relative error of a few 2^-24 for every t
         const float bc1 = -expm1f(static_cast<float>(t * p.log_b1)), bc2 = -expm1f(static_cast<float>(t * p.log_b2));
         const float step = lr / bc1, r2 = rsqrtf(bc2);
@@ -233,11 +238,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                 v[i] = __fadd_rn(__fmul_rn(v[i], p.b2), __fmul_rn(__fmul_rn(gi, p.c2), gi));
                 w[i] = w[i] * keep - step * __fdividef(m[i], sqrtf(v[i]) * r2 + p.eps);
             }
-            store8(w, it.p, at, p16, full, cnt);
-            if (it.master) store8(w, reinterpret_cast<uint8_t*>(it.master), at, false, full, cnt);
+            store8(w, it.to.p, at, p16, full, cnt);
+            if (it.master) store8(w, reinterpret_cast<uint8_t*>(it.to.master), at, false, full, cnt);
             if (BITS == 32) {
-                store8(m, it.m, at, false, full, cnt);
-                store8(v, it.v, at, false, full, cnt);
+                store8(m, it.to.m, at, false, full, cnt);
+                store8(v, it.to.v, at, false, full, cnt);
             } else {
                 const float bm = block_max(m), bv = block_max(v);
                 const bool dm = bm < kDead, dv = bv < kDead; // false for NaN, which the scale then carries
@@ -257,18 +262,19 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
                         qv[e >> 2] |= cv << sh;
                     }
                 }
-                store_codes(make_uint2(qm[0], qm[1]), it.m, at, full, cnt);
-                store_codes(make_uint2(qv[0], qv[1]), it.v, at, full, cnt);
+                store_codes(make_uint2(qm[0], qm[1]), it.to.m, at, full, cnt);
+                store_codes(make_uint2(qv[0], qv[1]), it.to.v, at, full, cnt);
                 if (lane == 0) {
-                    it.ms[block] = dm ? 0.f : __fdiv_rn(bm, kTopM);
-                    it.vs[block] = dv ? 0.f : __fdiv_rn(bv, kTopV);
+                    it.to.ms[block] = dm ? 0.f : __fdiv_rn(bm, kTopM);
+                    it.to.vs[block] = dv ? 0.f : __fdiv_rn(bv, kTopV);
                 }
             }
         }
     }
     if (!p.last) return;
     __syncthreads();
-    if (threadIdx.x == 0 && atomicInc(&p.ctl->arrived, gridDim.x - 1) == gridDim.x - 1 && !skip) p.ctl->step += 1;
+    if (threadIdx.x == 0 && atomicInc(&p.ctl->arrived, gridDim.x - 1) == gridDim.x - 1 && !skip)
+        p.ctl->step = p.step ? static_cast<int32_t>(p.step) : p.ctl->step + 1;
 }
 
 // Sum of squares: FP32 over a lane's elements of 8 groups at most, 64 bits from there on. Every
@@ -336,21 +342,21 @@ __global__ void __launch_bounds__(kThreads) read_states_kernel(const __grid_cons
     int k = item_of(p, g0, 0);
     for (uint32_t gr = g0 + warp; gr < g1; gr += kWarps) {
         if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
-        const OptItem& it = p.item[k]; // master: where m goes; p: where v goes
+        const OptItem& it = p.item[k]; // to.m, to.v: FP32
         const uint64_t block = gr - it.group_begin, at = block * kBlock + 8u * lane;
         const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
         const bool full = cnt == 8 && (it.flags & kVec);
         float f[8];
         decode_m(f, load_codes(it.m, at, full, cnt), it.ms[block]);
-        store8(f, reinterpret_cast<uint8_t*>(it.master), at, false, full, cnt);
+        store8(f, it.to.m, at, false, full, cnt);
         decode_v(f, load_codes(it.v, at, full, cnt), it.vs[block]);
-        store8(f, it.p, at, false, full, cnt);
+        store8(f, it.to.v, at, false, full, cnt);
     }
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-enum class Pass { Step, Norm, Read };
+enum class Pass { Step, To, Norm, Read };
 
 // What the three entry points check of an item alike; the pointers that the pass uses must be set
 // and naturally aligned.
@@ -358,15 +364,15 @@ bs_status check_items(int32_t n, const bs_adamw_item* items, uint32_t bits, Pass
     if (n < 0 || (n > 0 && !items)) return BS_E_ARG;
     for (int32_t k = 0; k < n; ++k) {
         const bs_adamw_item& t = items[k];
-        if (t.n > (1ull << 38)) return BS_E_SIZE; // 2^30 groups
+        if (t.n > (1ull << 34)) return BS_E_SIZE; // 2^26 groups
         if (t.param_type > BS_TYPE_BF16 || t.grad_type > BS_TYPE_BF16) return BS_E_ARG;
         if (t.n == 0) continue;
         const uint32_t ga = t.grad_type == BS_TYPE_BF16 ? 2 : 4, pa = t.param_type == BS_TYPE_BF16 ? 2 : 4;
-        if (pass != Pass::Read && (!t.d_grad || !aligned(t.d_grad, ga))) return BS_E_ARG;
+        if ((pass == Pass::Step || pass == Pass::Norm) && (!t.d_grad || !aligned(t.d_grad, ga))) return BS_E_ARG;
         if (pass == Pass::Norm) continue;
-        if (pass == Pass::Step) {
+        if (pass != Pass::Read) {
             if (!t.d_param || !aligned(t.d_param, pa) || !aligned(t.d_master, 4)) return BS_E_ARG;
-            if (!(t.weight_decay >= 0.f) || std::isinf(t.weight_decay)) return BS_E_ARG;
+            if (pass == Pass::Step && !(t.weight_decay >= 0.f && t.weight_decay < INFINITY)) return BS_E_ARG;
         }
         if (!t.d_m || !t.d_v) return BS_E_ARG;
         if (bits == 32 && (!aligned(t.d_m, 4) || !aligned(t.d_v, 4))) return BS_E_ARG;
@@ -387,50 +393,49 @@ bs_status device_ok(int* sms) {
 
 uint64_t groups_of(uint64_t n) { return (n + kBlock - 1) / kBlock; }
 
-// Groups a CTA takes: two a warp once that still gives every SM 16 CTAs, else one a warp. More a
-// warp saves nothing (the CTA's set-up is a few loads); fewer would leave small steps on few SMs.
-uint32_t per_cta_of(uint64_t groups, int sms) { return groups >= uint64_t(sms) * 16 * 2 * kWarps ? 2 * kWarps : kWarps; }
+// The CTAs of a pass: one wave of them (4 an SM, the most that fit), each with an equal run of
+// groups and at least one group a warp. More CTAs than that pay their set-up (the step's
+// constants, the search for the first tensor) for every few groups.
+constexpr uint32_t kNormCtas = 148 * 4;
 
 template <int CAP>
-bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, uint32_t bits, float* const* rm, float* const* rv,
-                     OptParams<CAP>& p, int sms, cudaStream_t s) {
+bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, uint32_t bits, float* const* rm,
+                     float* const* rv, OptParams<CAP>& p, int sms, cudaStream_t s) {
     int32_t k = 0, left = 0;
-    uint64_t total = 0;
-    for (int32_t i = 0; i < n; ++i) {
-        left += items[i].n != 0;
-        total += groups_of(items[i].n);
-    }
-    p.per_cta = pass == Pass::Norm ? 8 * kWarps : per_cta_of(total, sms);
+    for (int32_t i = 0; i < n; ++i) left += items[i].n != 0;
     p.partial_at = 0;
     do {
         p.n_items = 0;
         uint64_t groups = 0;
         for (; k < n && p.n_items < static_cast<uint32_t>(CAP); ++k) {
-            const bs_adamw_item& t = items[k];
+            const bs_adamw_item &t = items[k], &d = to[k];
             if (t.n == 0) continue;
             if (groups + groups_of(t.n) > (1ull << 31)) break;
             OptItem& it = p.item[p.n_items++];
-            it.p = static_cast<uint8_t*>(t.d_param);
+            it.p = static_cast<const uint8_t*>(t.d_param);
             it.g = static_cast<const uint8_t*>(t.d_grad);
-            it.m = static_cast<uint8_t*>(t.d_m);
-            it.v = static_cast<uint8_t*>(t.d_v);
+            it.m = static_cast<const uint8_t*>(t.d_m);
+            it.v = static_cast<const uint8_t*>(t.d_v);
             it.master = t.d_master;
             it.ms = t.d_m_scale;
             it.vs = t.d_v_scale;
+            it.to = OptOut{static_cast<uint8_t*>(d.d_param), static_cast<uint8_t*>(d.d_m), static_cast<uint8_t*>(d.d_v),
+                           d.d_master, d.d_m_scale, d.d_v_scale};
             it.n = t.n;
             it.group_begin = static_cast<uint32_t>(groups);
             it.decay = t.weight_decay;
             it.tensor = static_cast<uint32_t>(k);
             bool vec;
             if (pass == Pass::Read) {
-                it.master = rm[k];
-                it.p = reinterpret_cast<uint8_t*>(rv[k]);
-                vec = aligned(it.m, 8) && aligned(it.v, 8) && aligned(it.master, 16) && aligned(it.p, 16);
+                it.to.m = reinterpret_cast<uint8_t*>(rm[k]);
+                it.to.v = reinterpret_cast<uint8_t*>(rv[k]);
+                vec = aligned(it.m, 8) && aligned(it.v, 8) && aligned(it.to.m, 16) && aligned(it.to.v, 16);
             } else if (pass == Pass::Norm) {
                 vec = aligned(it.g, 16);
             } else {
                 const uintptr_t a = bits == 8 ? 8 : 16;
-                vec = aligned(it.p, 16) && aligned(it.g, 16) && aligned(it.master, 16) && aligned(it.m, a) && aligned(it.v, a);
+                vec = aligned(it.p, 16) && aligned(it.g, 16) && aligned(it.master, 16) && aligned(it.m, a) && aligned(it.v, a) &&
+                      aligned(it.to.p, 16) && aligned(it.to.master, 16) && aligned(it.to.m, a) && aligned(it.to.v, a);
             }
             it.flags = (t.param_type == BS_TYPE_BF16 ? kP16 : 0u) | (t.grad_type == BS_TYPE_BF16 ? kG16 : 0u) | (vec ? kVec : 0u);
             groups += groups_of(t.n);
@@ -438,6 +443,8 @@ bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, uint32_t 
         }
         p.groups = static_cast<uint32_t>(groups);
         p.last = left == 0;
+        const uint64_t wave = pass == Pass::Norm ? kNormCtas : uint64_t(sms) * 4;
+        p.per_cta = static_cast<uint32_t>(std::max<uint64_t>(kWarps, (groups + wave - 1) / wave));
         const uint32_t ctas = static_cast<uint32_t>(std::max<uint64_t>(1, (groups + p.per_cta - 1) / p.per_cta));
         if (pass == Pass::Norm) grad_norm_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
         else if (pass == Pass::Read) read_states_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
@@ -453,19 +460,19 @@ bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, uint32_t 
 
 // The parameter block of a launch takes the room of its items: calls of few tensors use a small one.
 template <typename Fill>
-bs_status launch_sized(Pass pass, int32_t n, const bs_adamw_item* items, uint32_t bits, float* const* rm, float* const* rv,
-                       int sms, cudaStream_t s, Fill fill) {
+bs_status launch_sized(Pass pass, int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, uint32_t bits,
+                       float* const* rm, float* const* rv, int sms, cudaStream_t s, Fill fill) {
     if (n <= kFewItems) {
         OptParams<kFewItems> p;
         std::memset(&p, 0, offsetof(OptParams<kFewItems>, item));
         fill(p);
-        return launch_all(pass, n, items, bits, rm, rv, p, sms, s);
+        return launch_all(pass, n, items, to, bits, rm, rv, p, sms, s);
     }
     std::unique_ptr<OptParams<kManyItems>> p(new (std::nothrow) OptParams<kManyItems>);
     if (!p) return BS_E_NOMEM;
     std::memset(p.get(), 0, offsetof(OptParams<kManyItems>, item));
     fill(*p);
-    return launch_all(pass, n, items, bits, rm, rv, *p, sms, s);
+    return launch_all(pass, n, items, to, bits, rm, rv, *p, sms, s);
 }
 
 } // namespace
@@ -475,9 +482,8 @@ using namespace bs;
 
 extern "C" size_t bs_grad_norm_scratch_bytes(int32_t n, const bs_adamw_item* items) {
     if (check_items(n, items, 32, Pass::Norm) != BS_OK) return 0;
-    uint64_t ctas = 1;
-    for (int32_t k = 0; k < n; ++k) ctas += groups_of(items[k].n) / (8 * kWarps) + 1;
-    return sizeof(double) * ctas;
+    // a launch takes kFewItems tensors at least, or all: that many of 2^26 groups stay below 2^31
+    return sizeof(double) * kNormCtas * (2 + static_cast<size_t>(n) / kFewItems);
 }
 
 extern "C" bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs_adamw_ctl* d_ctl, void* d_scratch,
@@ -488,23 +494,30 @@ extern "C" bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float m
     if (scratch_bytes < bs_grad_norm_scratch_bytes(n, items)) return BS_E_SIZE;
     int sms = 148;
     if ((st = device_ok(&sms)) != BS_OK) return st;
-    return launch_sized(Pass::Norm, n, items, 32, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
+    return launch_sized(Pass::Norm, n, items, items, 32, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
         p.max_norm = max_norm;
         p.ctl = d_ctl;
         p.partial = static_cast<double*>(d_scratch);
     });
 }
 
-extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_params* prm, bs_adamw_ctl* d_ctl,
-                              void* stream) {
-    if (!prm || !d_ctl || !aligned(d_ctl, 16) || (prm->bits != 8 && prm->bits != 32) || prm->reserved) return BS_E_ARG;
+extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, const bs_adamw_params* prm,
+                              bs_adamw_ctl* d_ctl, void* stream) {
+    if (!prm || !d_ctl || !aligned(d_ctl, 16) || (prm->bits != 8 && prm->bits != 32) || prm->step > 0x7FFFFFFFu) return BS_E_ARG;
     if (!(prm->beta1 >= 0 && prm->beta1 < 1) || !(prm->beta2 >= 0 && prm->beta2 < 1) || !(prm->eps >= 0) || std::isinf(prm->eps))
         return BS_E_ARG;
     bs_status st = check_items(n, items, prm->bits, Pass::Step);
     if (st != BS_OK) return st;
+    if (!to) {
+        to = items;
+    } else {
+        if ((st = check_items(n, to, prm->bits, Pass::To)) != BS_OK) return st;
+        for (int32_t k = 0; k < n; ++k)
+            if (to[k].n != items[k].n || to[k].param_type != items[k].param_type || !to[k].d_master != !items[k].d_master) return BS_E_ARG;
+    }
     int sms = 148;
     if ((st = device_ok(&sms)) != BS_OK) return st;
-    return launch_sized(Pass::Step, n, items, prm->bits, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
+    return launch_sized(Pass::Step, n, items, to, prm->bits, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
         p.b1 = static_cast<float>(prm->beta1);
         p.b2 = static_cast<float>(prm->beta2);
         p.c1 = static_cast<float>(1.0 - prm->beta1);
@@ -513,6 +526,7 @@ extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_ad
         p.log_b1 = prm->beta1 > 0 ? std::log(prm->beta1) : -1e9; // beta 0: 1 - 0^t = 1
         p.log_b2 = prm->beta2 > 0 ? std::log(prm->beta2) : -1e9;
         p.seed = prm->seed;
+        p.step = prm->step;
         p.ctl = d_ctl;
     });
 }
@@ -530,5 +544,5 @@ extern "C" bs_status bs_adamw_read_states(int32_t n, const bs_adamw_item* items,
     if (!any) return BS_OK;
     int sms = 148;
     if ((st = device_ok(&sms)) != BS_OK) return st;
-    return launch_sized(Pass::Read, n, items, 8, d_m, d_v, sms, static_cast<cudaStream_t>(stream), [](auto&) {});
+    return launch_sized(Pass::Read, n, items, items, 8, d_m, d_v, sms, static_cast<cudaStream_t>(stream), [](auto&) {});
 }

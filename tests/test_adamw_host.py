@@ -24,8 +24,8 @@ def _prm(**kw):
     return p
 
 
-def _step(item, prm=None, ctl=256, n=1):
-    return bs.lib.bs_adamw(n, ctypes.byref(item) if item is not None else None,
+def _step(item, prm=None, ctl=256, n=1, to=None):
+    return bs.lib.bs_adamw(n, ctypes.byref(item) if item is not None else None, ctypes.byref(to) if to is not None else None,
                            ctypes.byref(prm) if prm is not None else None, ctl, None)
 
 
@@ -35,10 +35,10 @@ def test_step_refusals_before_any_launch():
                _item(d_m=1026), _item(d_v=2047), _item(d_master=2), _item(param_type=2), _item(grad_type=7),
                _item(weight_decay=-0.5), _item(weight_decay=float("inf")), _item(weight_decay=float("nan"))):
         assert _step(it, ok) == bs.E_ARG
-    assert _step(_item(n=(1 << 38) + 1), ok) == bs.E_SIZE
+    assert _step(_item(n=(1 << 34) + 1), ok) == bs.E_SIZE
     assert _step(_item(), None) == bs.E_ARG and _step(_item(), ok, ctl=None) == bs.E_ARG and _step(_item(), ok, ctl=8) == bs.E_ARG
     assert _step(None, ok) == bs.E_ARG and _step(_item(), ok, n=-1) == bs.E_ARG
-    for p in (_prm(bits=16), _prm(bits=0), _prm(reserved=1), _prm(beta1=1.0), _prm(beta2=1.5), _prm(beta1=-0.1),
+    for p in (_prm(bits=16), _prm(bits=0), _prm(step=1 << 31), _prm(beta1=1.0), _prm(beta2=1.5), _prm(beta1=-0.1),
               _prm(beta2=float("nan")), _prm(eps=-1e-8), _prm(eps=float("inf"))):
         assert _step(_item(), p) == bs.E_ARG
     for it in (_item(d_m_scale=None), _item(d_v_scale=None), _item(d_m_scale=2), _item(d_v_scale=3)):
@@ -86,3 +86,10 @@ def test_plain_random_bits_are_splitmix64():
     assert int(z[0]) == 0xE220A8397B1DCDAF
     um, uv = A.random_bits(1, 2, 3, 1 << 16)
     assert abs(um.mean() - 32767.5) < 6 * 18919 / 256 and abs(uv.mean() - 32767.5) < 6 * 18919 / 256
+
+
+def test_a_step_into_other_buffers_is_checked_alike():
+    for to in (_item(n=99), _item(param_type=1), _item(d_master=64), _item(d_param=None), _item(d_m=None), _item(d_v=2049)):
+        assert _step(_item(), _prm(), to=to) == bs.E_ARG
+    assert _step(_item(), _prm(bits=8), to=_item(d_v_scale=None)) == bs.E_ARG
+    assert _step(_item(d_master=64), _prm(), to=_item()) == bs.E_ARG

@@ -253,3 +253,28 @@ def test_overlapping_buffers_and_wrong_sizes_are_refused():
         with pytest.raises(bs.BsError) as e:
             bs.AdamW([z()], [g], **kw).step()
         assert e.value.code == bs.E_ARG
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("sizes", [(5000, 257, 3), (300,) * 300])
+def test_a_step_into_a_twin_is_the_step_in_place(bits, sizes):
+    def make():
+        rng = np.random.default_rng(8)
+        ps = [_tensor(n, BF, rng, 0.02) for n in sizes]
+        return bs.AdamW(ps, [_tensor(n, BF, rng, 0.01) for n in sizes], bits=bits, masters=[p.float() for p in ps], seed=3)
+    held = lambda o: [t.clone() for ts in (o.params, o.masters, o.exp_avg, o.exp_avg_sq, o.exp_avg_scale or [], o.exp_avg_sq_scale or [])  # noqa: E731
+                      for t in ts]
+    a, b = make(), make()
+    there, here = b, b.twin()
+    for t in range(4):
+        a.step(max_norm=0.5)
+        before = held(there)
+        for _ in range(2):  # its results do not depend on what stands in the twin
+            there.step(max_norm=0.5, into=here, number=t + 1)
+        assert all(torch.equal(x, y) for x, y in zip(before, held(there)))
+        assert all(torch.equal(x, y) for x, y in zip(held(a), held(here))), t
+        assert int(b.steps) == int(a.steps) == t + 1
+        there, here = here, there
+    with pytest.raises(bs.BsError) as e:
+        a.step(into=b)
+    assert e.value.code == bs.E_ARG
