@@ -240,6 +240,14 @@ def prepare(case, seed):
         s["opt"] = bs.AdamW(cut(s["param"]), cut(s["grad"]), lr=s["lr"], betas=s["betas"], eps=s["eps"], weight_decay=s["decay"],
                             bits=s["bits"], masters=cut(s["master"]) if s["master"] is not None else None, seed=s["seed"],
                             step=s["step"], clip=s["clip"], states=states)
+        # a pass leaves the state as it was and writes another one, as a program does that codes the
+        # weights of this step while the next one runs
+        like = lambda flat: None if flat is None else torch.zeros_like(flat)  # noqa: E731
+        s["new"] = {k: like(s.get(k)) for k in ("param", "master", "m", "v", "mc", "vc", "ms", "vs")}
+        into = ((cut(s["new"]["m"]), cut(s["new"]["v"])) if s["bits"] == 32 else
+                tuple([cut(s["new"][c]), [s["new"][f][at // BLOCK: at // BLOCK + -(-n // BLOCK)] for n, at in zip(s["sizes"], s["starts"])]]
+                      for c, f in (("mc", "ms"), ("vc", "vs"))))
+        s["twin"] = s["opt"].twin(cut(s["new"]["param"]), cut(s["new"]["master"]) if s["master"] is not None else None, into)
         if s["bits"] == 8:
             s["read"] = [torch.zeros(s["grad"].numel(), device="cuda") for _ in range(2)]
             s["read_cut"] = [cut(f) for f in s["read"]]
@@ -266,15 +274,15 @@ def _run_own(s):
         k = len(s["a"])
         s["set"].backward(s["plan"], [s["x"]] * k, s["dy"], s["state"], s["da"], s["db"], dxs=[s["dx"]] * k, work=s["work"])
         return {"dx": s["dx"], "da": s["da"], "db": s["db"]}
-    s["opt"].step(max_norm=s["max_norm"] or None)
-    out = {"param": s["param"]}
+    s["opt"].step(max_norm=s["max_norm"] or None, into=s["twin"], number=s["step"] + 1)
+    out = {"param": s["new"]["param"]}
     if s["max_norm"]:
         out["norm"] = s["opt"].norm
     if s["master"] is not None:
-        out["master"] = s["master"]
+        out["master"] = s["new"]["master"]
     if s["bits"] == 32:
-        return out | {"m": s["m"], "v": s["v"]}
-    s["opt"].read_states(*s["read_cut"])
+        return out | {"m": s["new"]["m"], "v": s["new"]["v"]}
+    s["twin"].read_states(*s["read_cut"])
     return out | {"m": s["read"][0], "v": s["read"][1]}
 
 
