@@ -593,7 +593,7 @@ typedef struct {
 } bs_adamw_ctl;
 
 typedef struct {
-    double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0 */
+    double beta1, beta2, eps; /* 0 <= beta < 1, eps at least 1e-12 */
     uint32_t bits;            /* 32 or 8: how d_m and d_v are held */
     uint32_t step;            /* 0: the step is number d_ctl->step + 1. Else its number, 1 .. 2^31 - 1 */
     uint64_t seed;            /* of the 8-bit rounding */

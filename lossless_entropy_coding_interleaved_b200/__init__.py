@@ -18,6 +18,7 @@ from __future__ import annotations
 import bisect
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -243,6 +244,26 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(index: int, what: str, fn, *args, stream=None):
+    """fn(*args, stream) with device `index` current; the stream is that device's current one by default."""
+    def go():
+        if stream is not None:
+            st = _stream(stream)
+        else:
+            st = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+        r = fn(*args, st)
+        if r != OK:
+            _check(r, what)
+    if torch.cuda.current_device() == index:
+        go()
+    else:
+        with torch.cuda.device(index):
+            go()
 
 
 def _host_bytes(container) -> np.ndarray:
@@ -712,6 +733,8 @@ def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = F
 # ------------------------------------------------------------ low-rank adapters
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 LORA_ACCUMULATE = 1
+_LORA_ITEM = struct.Struct("=QQIIII16Q")  # LoraItem's fields in order
+assert _LORA_ITEM.size == ctypes.sizeof(LoraItem) == 160
 
 
 class LoraPlan:
@@ -729,14 +752,14 @@ class LoraPlan:
         self.data = torch.zeros(nb, dtype=torch.uint8, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.device = self.data.device
+        self._index = self.data.get_device()
+        self._args = (tokens, n_adapters, self.data.data_ptr(), nb, self.err.data_ptr())
 
     def update(self, idx: torch.Tensor, stream=None) -> "LoraPlan":
         """Enqueued on the stream. An index past the adapters counts as none and sets bit 2 of ``err``."""
-        if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.numel() != self.tokens or idx.device != self.device:
+        if idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.numel() != self.tokens or idx.get_device() != self._index:
             raise BsError(E_ARG, "lora_plan", "idx: one int32 for each token, contiguous, on the plan's device")
-        with torch.cuda.device(self.device):
-            _check(lib.bs_lora_plan(idx.data_ptr() if self.tokens else None, self.tokens, self.n_adapters, self.data.data_ptr(),
-                                    self.data.numel(), self.err.data_ptr(), _stream(stream)), "lora_plan")
+        _on(self._index, "lora_plan", lib.bs_lora_plan, idx.data_ptr() if self.tokens else None, *self._args, stream=stream)
         return self
 
 
@@ -773,11 +796,10 @@ class LoraAdapters:
                 raise bad(f"scales float32 and ranks int32: one for each of {self.n} adapters")
         self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
         self._n = len(a)
-        self._items = (LoraItem * self._n)()
-        for it, x, y in zip(self._items, a, b):
-            it.d_a, it.d_b, it.rows, it.cols = x.data_ptr(), y.data_ptr(), y.shape[1], x.shape[2]
-        self._batch = LoraBatch(0, self.n, self.rank_max, 0, ranks.data_ptr() if ranks is not None else None,
-                                scales.data_ptr() if scales is not None else None, None)
+        self._index = a[0].get_device()
+        self._fixed = [(x.data_ptr(), y.data_ptr(), y.shape[1], x.shape[2]) for x, y in zip(a, b)]
+        self._ranks_at, self._scales_at = (t.data_ptr() if t is not None else None for t in (ranks, scales))
+        self._need = (-1, 0)  # the bytes of a state for the last batch's number of tokens
 
     def state(self, tokens: int) -> list:
         """Buffers for one batch: what forward leaves for backward, or backward's own workspace."""
@@ -786,41 +808,54 @@ class LoraAdapters:
             raise BsError(E_ARG, "lora", "tokens up to 2^20, rank_max a multiple of 8 in 8..128")
         return [torch.empty(nb, dtype=torch.uint8, device=self.device) for _ in range(self._n)]
 
-    def _rows(self, t, width, dtypes, what, tokens):
-        if t.dim() != 2 or t.shape[0] != tokens or t.shape[1] != width or t.dtype not in dtypes or t.device != self.device or (
-                tokens and t.stride(1) != 1):
-            raise BsError(E_ARG, "lora", f"{what}: [{tokens}, {width}] of {dtypes}, rows contiguous, on the adapters' device")
-        return t.data_ptr(), width if tokens <= 1 else t.stride(0)
+    def _rows(self, t, width, dtype, what, tokens):
+        """(address, stride) of a [tokens, width] tensor of contiguous rows."""
+        if t.shape == (tokens, width) and t.dtype is dtype and t.get_device() == self._index:
+            s0, s1 = t.stride()
+            if tokens <= 1:
+                return t.data_ptr(), width
+            if s1 == 1:
+                return t.data_ptr(), s0
+        raise BsError(E_ARG, "lora", f"{what}: [{tokens}, {width}] of {dtype}, rows contiguous, on the adapters' device")
+
+    def _out(self, t, base, width, what, tokens):
+        """(type, base, its stride, output, its stride); no output: zeros."""
+        if t is None:
+            return 0, 0, 0, 0, 0
+        if t.dtype not in _TYPES:
+            raise BsError(E_ARG, "lora", f"{what}: float32 or bfloat16")
+        at = self._rows(t, width, t.dtype, what, tokens)
+        from_ = at if base is t else (0, 0) if base is None else self._rows(base, width, t.dtype, what + " base", tokens)
+        return (_TYPES[t.dtype], *from_, *at)
 
     def _begin(self, plan, lists, states):
-        if plan.n_adapters != self.n or plan.device != self.device:
+        if plan.n_adapters != self.n or plan._index != self._index:
             raise BsError(E_ARG, "lora", "the plan is of another set of adapters")
-        if any(len(v) != self._n for v in lists + states):
-            raise BsError(E_ARG, "lora", "one entry for each projection")
-        need = lib.bs_lora_state_bytes(plan.tokens, self.rank_max)
+        for v in lists + states:
+            if len(v) != self._n:
+                raise BsError(E_ARG, "lora", "one entry for each projection")
+        if plan.tokens != self._need[0]:
+            self._need = (plan.tokens, lib.bs_lora_state_bytes(plan.tokens, self.rank_max))
+        need = self._need[1]
         for v in states:
             for t in v:
-                if t.dtype != torch.uint8 or t.device != self.device or t.numel() < need:
+                if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != self._index:
                     raise BsError(E_SIZE, "lora", "a state is of another batch")
-        self._batch.tokens, self._batch.d_plan = plan.tokens, plan.data.data_ptr()
+        batch = LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2])
+        return (LoraItem * self._n)(), batch
 
     def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
         xs = list(xs)
         state = self.state(plan.tokens) if state is None else list(state)
         ys = [None] * self._n if ys is None else list(ys)
         bases = ys if bases is None else list(bases)
-        self._begin(plan, [xs, ys, bases], [state])
-        T, both = plan.tokens, (torch.float32, torch.bfloat16)
-        for it, x, y, base, h in zip(self._items, xs, ys, bases, state):
-            it.d_x, it.x_stride = self._rows(x, it.cols, (torch.bfloat16,), "x", T)
-            it.d_h, it.d_y, it.d_base, it.type = h.data_ptr(), None, None, 0
-            if y is not None:
-                it.d_y, it.y_stride = self._rows(y, it.rows, both, "y", T)
-                it.type = _TYPES[y.dtype]
-                if base is not None:
-                    it.d_base, it.base_stride = self._rows(base, it.rows, (y.dtype,), "base", T)
-        with torch.cuda.device(self.device):
-            _check(lib.bs_lora_forward(self._n, self._items, ctypes.byref(self._batch), _stream(stream)), "lora_forward")
+        items, batch = self._begin(plan, [xs, ys, bases], [state])
+        T, pack = plan.tokens, _LORA_ITEM.pack_into
+        for k, (a, b, rows, cols) in enumerate(self._fixed):
+            ty, base, bs_, y, ys_ = self._out(ys[k], bases[k], rows, "y", T)
+            pack(items, 160 * k, a, b, rows, cols, ty, 0, *self._rows(xs[k], cols, torch.bfloat16, "x", T), state[k].data_ptr(),
+                 base, bs_, y, ys_, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        _on(self._index, "lora_forward", lib.bs_lora_forward, self._n, items, ctypes.byref(batch), stream=stream)
         return ys
 
     def backward(self, plan: LoraPlan, xs, dys, state, das, dbs, dxs=None, dx_bases=None, work=None, accumulate: bool = False,
@@ -829,25 +864,17 @@ class LoraAdapters:
         work = self.state(plan.tokens) if work is None else list(work)
         dxs = [None] * self._n if dxs is None else list(dxs)
         dx_bases = [None] * self._n if dx_bases is None else list(dx_bases)
-        self._begin(plan, [xs, dys, das, dbs, dxs, dx_bases], [state, work])
-        T, both = plan.tokens, (torch.float32, torch.bfloat16)
-        for it, a, b, x, dy, h, g, da, db, dx, base in zip(self._items, self.a, self.b, xs, dys, state, work, das, dbs, dxs, dx_bases):
-            it.d_x, it.x_stride = self._rows(x, it.cols, (torch.bfloat16,), "x", T)
-            it.d_dy, it.dy_stride = self._rows(dy, it.rows, (torch.bfloat16,), "dy", T)
-            for t, like in ((da, a), (db, b)):
-                if t.dtype != torch.float32 or t.shape != like.shape or not t.is_contiguous() or t.device != self.device:
+        items, batch = self._begin(plan, [xs, dys, das, dbs, dxs, dx_bases], [state, work])
+        T, pack, bf = plan.tokens, _LORA_ITEM.pack_into, torch.bfloat16
+        for k, (a, b, rows, cols) in enumerate(self._fixed):
+            for t, shape in ((das[k], self.a[k].shape), (dbs[k], self.b[k].shape)):
+                if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
                     raise BsError(E_ARG, "lora", "das and dbs: contiguous float32, of the pools' shapes")
-            it.d_h, it.d_g, it.d_da, it.d_db = h.data_ptr(), g.data_ptr(), da.data_ptr(), db.data_ptr()
-            it.d_dx, it.d_dx_base, it.type = None, None, 0
-            it.dx_stride = it.dx_base_stride = 0
-            if dx is not None:
-                it.d_dx, it.dx_stride = self._rows(dx, it.cols, both, "dx", T)
-                it.type = _TYPES[dx.dtype]
-                if base is not None:
-                    it.d_dx_base, it.dx_base_stride = self._rows(base, it.cols, (dx.dtype,), "dx_base", T)
-        with torch.cuda.device(self.device):
-            _check(lib.bs_lora_backward(self._n, self._items, ctypes.byref(self._batch), LORA_ACCUMULATE if accumulate else 0,
-                                        _stream(stream)), "lora_backward")
+            ty, base, bs_, dx, dxs_ = self._out(dxs[k], dx_bases[k], cols, "dx", T)
+            pack(items, 160 * k, a, b, rows, cols, ty, 0, *self._rows(xs[k], cols, bf, "x", T), state[k].data_ptr(), 0, 0, 0, 0,
+                 *self._rows(dys[k], rows, bf, "dy", T), work[k].data_ptr(), base, bs_, dx, dxs_, das[k].data_ptr(), dbs[k].data_ptr())
+        _on(self._index, "lora_backward", lib.bs_lora_backward, self._n, items, ctypes.byref(batch),
+            LORA_ACCUMULATE if accumulate else 0, stream=stream)
         return das, dbs, dxs
 
 
@@ -910,6 +937,8 @@ class AdamW:
             z = lambda dt, of: [torch.zeros(k, dtype=dt, device=dev) for k in of]  # noqa: E731
             states = ((z(torch.float32, sizes), z(torch.float32, sizes)) if bits == 32 else
                       tuple((z(torch.uint8, sizes), z(torch.float32, blocks)) for _ in range(2)))
+        if not params[0].is_cuda:
+            raise BsError(E_ARG, "adamw", "params: CUDA tensors")
         if bits == 32:
             self.exp_avg, self.exp_avg_sq = (_flat_list(v, "states", n, sizes, (torch.float32,), dev) for v in states)
             self.exp_avg_scale = self.exp_avg_sq_scale = None
@@ -936,16 +965,16 @@ class AdamW:
             it.d_m_scale, it.d_v_scale = ptr(self.exp_avg_scale, k), ptr(self.exp_avg_sq_scale, k)
             it.n, it.param_type, it.grad_type = sizes[k], _TYPES[self.params[k].dtype], _TYPES[self.grads[k].dtype]
             it.weight_decay = decay[k]
-        self._n = n
+        self._n, self._sizes, self._index = n, sizes, self.params[0].get_device()
         self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
         self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
         self._lr, self._clip, self.norm, self.steps = f[0], f[1], f[4], self.ctl[2]
-        if _ctl is not None:
-            return
-        self.lr, self.clip = lr, clip
-        self.steps.fill_(step)
+        if _ctl is None:
+            self.lr, self.clip = lr, clip
+            self.steps.fill_(step)
         self._scratch = torch.empty(max(8, lib.bs_grad_norm_scratch_bytes(n, self._items)), dtype=torch.uint8, device=dev)
+        self._at = (self.ctl.data_ptr(), self._scratch.data_ptr(), self._scratch.numel())
 
     @property
     def lr(self):
@@ -966,9 +995,7 @@ class AdamW:
     def grad_norm(self, max_norm: float = float("inf"), stream=None) -> torch.Tensor:
         """bs_grad_norm: the norm of all gradients as a device scalar; sets the factor of the next
         step to min(1, max_norm / (norm + 1e-6)), or marks it to be left out if the norm is not finite."""
-        with torch.cuda.device(self.device):
-            _check(lib.bs_grad_norm(self._n, self._items, max_norm, self.ctl.data_ptr(), self._scratch.data_ptr(),
-                                    self._scratch.numel(), _stream(stream)), "grad_norm")
+        _on(self._index, "grad_norm", lib.bs_grad_norm, self._n, self._items, max_norm, *self._at, stream=stream)
         return self.norm
 
     def twin(self, params=None, masters=None, states=None) -> "AdamW":
@@ -979,11 +1006,9 @@ class AdamW:
         if states is None:
             m, v, ms, vs = (new(ts, None) for ts in (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))
             states = (m, v) if self.bits == 32 else ((m, ms), (v, vs))
-        t = AdamW(new(self.params, params), self.grads, betas=(self._prm.beta1, self._prm.beta2), eps=self._prm.eps,
+        return AdamW(new(self.params, params), self.grads, betas=(self._prm.beta1, self._prm.beta2), eps=self._prm.eps,
                   weight_decay=[it.weight_decay for it in self._items], bits=self.bits, masters=new(self.masters, masters),
                   seed=self._prm.seed, states=states, _ctl=self.ctl)
-        t._scratch = self._scratch
-        return t
 
     def step(self, max_norm: float | None = None, into: "AdamW | None" = None, number: int = 0, stream=None):
         """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first. into: a twin
@@ -994,19 +1019,19 @@ class AdamW:
         if into is not None and into.ctl is not self.ctl:
             raise BsError(E_ARG, "adamw", "into: a twin of this handle")
         self._prm.step = number
-        with torch.cuda.device(self.device):
-            _check(lib.bs_adamw(self._n, self._items, into._items if into is not None else None, ctypes.byref(self._prm),
-                                self.ctl.data_ptr(), _stream(stream)), "adamw")
+        _on(self._index, "adamw", lib.bs_adamw, self._n, self._items, into._items if into is not None else None,
+            ctypes.byref(self._prm), self._at[0], stream=stream)
 
     def read_states(self, ms=None, vs=None, stream=None):
         """The moments as float32 lists, (exp_avgs, exp_avg_sqs). 32-bit moments are returned as they
         stand; 8-bit ones are decoded (bs_adamw_read_states) into ms and vs, or into new tensors."""
         if self.bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        sizes = [p.numel() for p in self.params]
-        ms, vs = ([torch.empty(k, dtype=torch.float32, device=self.device) for k in sizes] if t is None else
-                  _flat_list(t, "read_states", self._n, sizes, (torch.float32,), self.device) for t in (ms, vs))
-        pm, pv = ((ctypes.c_void_p * self._n)(*[t.data_ptr() if t.numel() else None for t in ts]) for ts in (ms, vs))
-        with torch.cuda.device(self.device):
-            _check(lib.bs_adamw_read_states(self._n, self._items, pm, pv, _stream(stream)), "adamw_read_states")
+        ms, vs = ([torch.empty(k, dtype=torch.float32, device=self.device) for k in self._sizes] if t is None else list(t) for t in (ms, vs))
+        for ts in (ms, vs):
+            if len(ts) != self._n or any(t.numel() != k or t.dtype is not torch.float32 or t.get_device() != self._index or
+                                         not t.is_contiguous() for t, k in zip(ts, self._sizes)):
+                raise BsError(E_ARG, "adamw", "read_states: a contiguous float32 tensor of each parameter's size")
+        pm, pv = ((ctypes.c_void_p * self._n)(*[t.data_ptr() or None for t in ts]) for ts in (ms, vs))
+        _on(self._index, "adamw_read_states", lib.bs_adamw_read_states, self._n, self._items, pm, pv, stream=stream)
         return ms, vs

@@ -63,18 +63,31 @@ struct OptItem {
 static_assert(sizeof(OptItem) == 128, "OptItem layout");
 constexpr uint32_t kP16 = 1, kG16 = 2, kVec = 4; // BF16 parameters, BF16 gradients, all pointers aligned for vectors
 
+struct NormItem {
+    const uint8_t* g;
+    uint64_t n;
+    uint32_t group_begin, flags;
+};
+constexpr int kFewNorm = 64, kManyNorm = 1300;
+template <int CAP>
+struct NormParams {
+    uint32_t n_items, groups, last, partial_at;
+    float max_norm;
+    bs_adamw_ctl* ctl;
+    double* partial; // one sum a CTA, those of earlier launches before it
+    NormItem item[CAP];
+};
+static_assert(sizeof(NormParams<kManyNorm>) < 32764, "kernel parameters");
+
 template <int CAP>
 struct OptParams {
     uint32_t n_items, groups, per_cta; // groups of the launch, groups a CTA takes
     uint32_t last;                     // the call's last launch
     uint32_t step;                     // the step's number, 0: one more than ctl->step
     float b1, b2, c1, c2, eps;         // c = 1 - b, rounded from 64 bits
-    float max_norm;
     double log_b1, log_b2;
     uint64_t seed;
     bs_adamw_ctl* ctl;
-    double* partial;                   // norm: one sum a CTA, those of earlier launches before it
-    uint32_t partial_at;
     OptItem item[CAP];
 };
 static_assert(sizeof(OptParams<kManyItems>) < 32764, "kernel parameters");
@@ -84,48 +97,76 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z) { // splitmix64's output f
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
     return z ^ (z >> 31);
 }
-__device__ __forceinline__ float bf16_bits(uint32_t lo16) { return __uint_as_float(lo16 << 16); }
-__device__ __forceinline__ uint32_t to_bf16(float f) { // to nearest, ties to even; NaN stays NaN
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) { // to nearest, ties to even; NaN stays NaN
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// sqrt and 1 / x within 2^-23, numbers below the normal range as 0: a v below 2^-126 is a root below
+// 2^-63, which eps (at least 1e-12) hides.
+__device__ __forceinline__ float sqrt_fast(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) { // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// 8 elements of a lane, from `at` on; with `full` false only the first `cnt` exist (0 for the others).
-__device__ __forceinline__ void load8(float (&f)[8], const uint8_t* base, uint64_t at, bool b16, bool full, uint32_t cnt) {
+// 8 elements of a lane as they stand in memory, from `at` on (4 words of BF16 pairs, or 8 of FP32);
+// with `full` false only the first `cnt` exist (0 for the others).
+__device__ __forceinline__ void load_raw(uint32_t (&r)[8], const uint8_t* base, uint64_t at, bool b16, bool full, uint32_t cnt) {
     if (b16) {
         const uint16_t* s = reinterpret_cast<const uint16_t*>(base) + at;
         if (full) {
             const uint4 w = *reinterpret_cast<const uint4*>(s);
-            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { f[2 * i] = bf16_bits(q[i] & 0xFFFFu); f[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u); }
+            r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = i < cnt ? bf16_bits(s[i]) : 0.f;
+            for (int i = 0; i < 8; i += 2)
+                r[i >> 1] = (i < cnt ? uint32_t(s[i]) : 0u) | (i + 1 < cnt ? uint32_t(s[i + 1]) << 16 : 0u);
         }
     } else {
         const float* s = reinterpret_cast<const float*>(base) + at;
         if (full) {
-            const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            const uint4 a = *reinterpret_cast<const uint4*>(s), b = *reinterpret_cast<const uint4*>(s + 4);
+            r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w; r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = i < cnt ? s[i] : 0.f;
+            for (int i = 0; i < 8; ++i) r[i] = i < cnt ? __float_as_uint(s[i]) : 0u;
         }
     }
+}
+__device__ __forceinline__ void unpack(float (&f)[8], const uint32_t (&r)[8], bool b16) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        f[i] = b16 ? __uint_as_float(r[i >> 1] << 16) : __uint_as_float(r[i]);
+        f[i + 1] = b16 ? __uint_as_float(r[i >> 1] & 0xFFFF0000u) : __uint_as_float(r[i + 1]);
+    }
+}
+__device__ __forceinline__ void load8(float (&f)[8], const uint8_t* base, uint64_t at, bool b16, bool full, uint32_t cnt) {
+    uint32_t r[8];
+    load_raw(r, base, at, b16, full, cnt);
+    unpack(f, r, b16);
 }
 __device__ __forceinline__ void store8(const float (&f)[8], uint8_t* base, uint64_t at, bool b16, bool full, uint32_t cnt) {
     if (b16) {
         uint16_t* d = reinterpret_cast<uint16_t*>(base) + at;
         if (full) {
             uint4 w;
-            w.x = to_bf16(f[0]) | (to_bf16(f[1]) << 16); w.y = to_bf16(f[2]) | (to_bf16(f[3]) << 16);
-            w.z = to_bf16(f[4]) | (to_bf16(f[5]) << 16); w.w = to_bf16(f[6]) | (to_bf16(f[7]) << 16);
+            w.x = to_bf16x2(f[0], f[1]); w.y = to_bf16x2(f[2], f[3]);
+            w.z = to_bf16x2(f[4], f[5]); w.w = to_bf16x2(f[6], f[7]);
             *reinterpret_cast<uint4*>(d) = w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) if (i < cnt) d[i] = static_cast<uint16_t>(to_bf16(f[i]));
+            for (int i = 0; i < 8; ++i) if (i < cnt) d[i] = static_cast<uint16_t>(to_bf16x2(f[i], 0.f));
         }
     } else {
         float* d = reinterpret_cast<float*>(base) + at;
@@ -164,29 +205,47 @@ __device__ __forceinline__ void decode_m(float (&f)[8], uint2 w, float scale) {
 __device__ __forceinline__ void decode_v(float (&f)[8], uint2 w, float scale) {
     const uint32_t q[2] = {w.x, w.y};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = (q[i >> 2] >> (8 * (i & 3))) & 0xFFu;
-        f[i] = __fmul_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(c << 7))), scale);
+    for (int i = 0; i < 8; i += 2) { // two codes to the upper bytes of two halves, then down by one bit
+        const uint32_t h = (__byte_perm(q[i >> 2], 0, (i & 2) ? 0x3424 : 0x1404) >> 1) & 0x7F807F80u;
+        __half2 hh;
+        std::memcpy(&hh, &h, 4);
+        const float2 d = __half22float2(hh);
+        f[i] = __fmul_rn(d.x, scale);
+        f[i + 1] = __fmul_rn(d.y, scale);
     }
 }
-// The code of y >= 0, rounded up where the 16 random bits u reach what is left of y below it.
+// The code (in the upper byte) of y >= 0, rounded up where its 16 random bits u reach what is left of
+// it below. Scaled by 2^(BIAS - 127), the format's exponent range becomes FP32's lowest, so bits 20
+// and up of the number are the code, and adding the random bits 16 times carries into it. Below the
+// format's normal range the scaled number is subnormal; there the sum is taken as the definition has
+// it, in FP32, where the last bit could differ (code_small). Such values are few: they cost a test.
 template <int BIAS, uint32_t MOST>
-__device__ __forceinline__ uint32_t encode(float y, uint32_t u) {
-    const uint32_t normal = ((__float_as_uint(y) + (u << 4)) >> 20) - ((127 - BIAS) << 3);
-    const uint32_t small = static_cast<uint32_t>(static_cast<int>(
-        __fadd_rn(__fmul_rn(y, static_cast<float>(1 << (BIAS + 2))), __fmul_rn(static_cast<float>(u), 1.f / 65536.f))));
-    return min(y < 1.f / static_cast<float>(1 << (BIAS - 1)) ? small : normal, MOST);
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t u) {
+    const float down = __uint_as_float(static_cast<uint32_t>(BIAS) << 23); // 2^(BIAS - 127)
+    return min(__float_as_uint(__fmul_rn(y, down)) + u * 16u, (MOST << 20) | 0xFFFFFu) * 16u;
 }
-// The largest magnitude of the block; NaN when any is NaN (as integers, every NaN is above infinity).
+template <int BIAS>
+constexpr uint32_t kSmall = (static_cast<uint32_t>(128 - BIAS) << 23) - 1u; // the bits of 2^(1 - BIAS), less one
+template <int BIAS, uint32_t MOST>
+__device__ __forceinline__ uint32_t code_small(float y, uint32_t u) {
+    if (__float_as_uint(y) - 1u >= kSmall<BIAS>) return code_of<BIAS, MOST>(y, u);
+    return static_cast<uint32_t>(static_cast<int>(
+        __fadd_rn(__fmul_rn(y, static_cast<float>(1 << (BIAS + 2))), __fmul_rn(static_cast<float>(u), 1.f / 65536.f)))) << 24;
+}
+// 4 codes from the upper bytes of 4 words
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// The largest magnitude of the block, NaN when any is NaN.
 __device__ __forceinline__ float block_max(const float (&f)[8]) {
-    uint32_t b = 0;
+    float b = fabsf(f[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b = max(b, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, b));
+    for (int i = 1; i < 8; ++i) b = max_nan(b, fabsf(f[i]));
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(b))); // as integers every NaN is above infinity
 }
 
-template <int CAP>
-__device__ __forceinline__ int item_of(const OptParams<CAP>& p, uint32_t group, int lo) {
+template <typename Params>
+__device__ __forceinline__ int item_of(const Params& p, uint32_t group, int lo) {
     int hi = static_cast<int>(p.n_items) - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -196,79 +255,198 @@ __device__ __forceinline__ int item_of(const OptParams<CAP>& p, uint32_t group, 
     return lo;
 }
 
+// What a lane has loaded of one group: 8 elements of everything the step reads.
+template <int BITS>
+struct Held {
+    uint32_t w[8], g[8];
+    float m[8], v[8];
+};
+template <>
+struct Held<8> {
+    uint32_t w[8], g[8];
+    uint2 cm, cv;
+    float sm, sv;
+};
+// The constants of a step.
+struct StepConst {
+    float b1, b2, c1, c2, eps, clip, lr, step, r2;
+};
+
+template <int BITS>
+__device__ __forceinline__ void load_group(Held<BITS>& h, const OptItem& it, uint64_t block, uint64_t at, bool p16, bool g16, bool master,
+                                           bool full, uint32_t cnt) {
+    if (master) load_raw(h.w, reinterpret_cast<const uint8_t*>(it.master), at, false, full, cnt);
+    else load_raw(h.w, it.p, at, p16, full, cnt);
+    load_raw(h.g, it.g, at, g16, full, cnt);
+    if constexpr (BITS == 32) {
+        load8(h.m, it.m, at, false, full, cnt);
+        load8(h.v, it.v, at, false, full, cnt);
+    } else {
+        h.cm = load_codes(it.m, at, full, cnt);
+        h.cv = load_codes(it.v, at, full, cnt);
+        h.sm = it.ms[block];
+        h.sv = it.vs[block];
+    }
+}
+
+template <int BITS>
+__device__ __forceinline__ void step_group(const Held<BITS>& h, const OptItem& it, const StepConst& c, float keep, uint64_t key, uint32_t lane,
+                                           uint64_t block, uint64_t at, bool p16, bool g16, bool master, bool full, uint32_t cnt) {
+    float w[8], g[8], m[8], v[8];
+    unpack(w, h.w, p16 && !master);
+    unpack(g, h.g, g16);
+    if constexpr (BITS == 32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { m[i] = h.m[i]; v[i] = h.v[i]; }
+    } else {
+        decode_m(m, h.cm, h.sm);
+        decode_v(v, h.cv, h.sv);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float gi = __fmul_rn(g[i], c.clip);
+        m[i] = __fadd_rn(__fmul_rn(m[i], c.b1), __fmul_rn(gi, c.c1));
+        v[i] = __fadd_rn(__fmul_rn(v[i], c.b2), __fmul_rn(__fmul_rn(gi, c.c2), gi));
+        w[i] = w[i] * keep - c.step * m[i] * rcp_fast(sqrt_fast(v[i]) * c.r2 + c.eps);
+    }
+    store8(w, it.to.p, at, p16, full, cnt);
+    if (master) store8(w, reinterpret_cast<uint8_t*>(it.to.master), at, false, full, cnt);
+    if constexpr (BITS == 32) {
+        store8(m, it.to.m, at, false, full, cnt);
+        store8(v, it.to.v, at, false, full, cnt);
+    } else {
+        const float bm = block_max(m), bv = block_max(v);
+        const bool dm = bm < kDead, dv = bv < kDead; // false for NaN, which the scale then carries
+        float im = dm ? 0.f : __fdiv_rn(kTopM, bm), iv = dv ? 0.f : __fdiv_rn(kTopV, bv);
+        uint64_t pair0 = key + 0x9E3779B97F4A7C15ull * ((at >> 1) + 1);
+        uint32_t qm[2], qv[2], least_m = ~0u, least_v = ~0u;
+        auto codes = [&](auto code_m, auto code_v) {
+            uint64_t pair = pair0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t cm[4], cv[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int e = 4 * q + j;
+                    uint64_t z = 0;
+                    if (!(j & 1)) {
+                        z = mix64(pair);
+                        pair += 0x9E3779B97F4A7C15ull;
+                        cm[j + 1] = static_cast<uint32_t>(z >> 32);
+                    }
+                    const uint32_t u = j & 1 ? cm[j] : static_cast<uint32_t>(z);
+                    const float ym = __fmul_rn(fabsf(m[e]), im), yv = __fmul_rn(v[e], iv);
+                    least_m = min(least_m, __float_as_uint(ym) - 1u); // 0 is not small
+                    least_v = min(least_v, __float_as_uint(yv) - 1u);
+                    cm[j] = code_m(ym, __byte_perm(u, 0, 0x4410)) | (__float_as_uint(m[e]) & 0x80000000u);
+                    cv[j] = code_v(yv, __byte_perm(u, 0, 0x4432));
+                }
+                qm[q] = pack4(cm[0], cm[1], cm[2], cm[3]);
+                qv[q] = pack4(cv[0], cv[1], cv[2], cv[3]);
+            }
+        };
+        codes(code_of<7, 0x7E>, code_of<15, 0xF7>);
+        if (least_m < kSmall<7> || least_v < kSmall<15>) {
+            asm volatile("" : "+l"(pair0), "+f"(im), "+f"(iv)); // nothing of the usual way is kept in registers for this one
+            codes(code_small<7, 0x7E>, code_small<15, 0xF7>);
+        }
+        auto has_zero = [](uint32_t q) { return (q - 0x01010101u) & ~q & 0x80808080u; };
+        if (!dv && (has_zero(qv[0]) | has_zero(qv[1]))) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) // what is above zero stays above it
+                if (v[e] > 0.f && ((qv[e >> 2] >> (8 * (e & 3))) & 0xFFu) == 0) qv[e >> 2] |= 1u << (8 * (e & 3));
+        }
+        store_codes(make_uint2(qm[0], qm[1]), it.to.m, at, full, cnt);
+        store_codes(make_uint2(qv[0], qv[1]), it.to.v, at, full, cnt);
+        if (lane == 0) {
+            it.to.ms[block] = dm ? 0.f : __fdiv_rn(bm, kTopM);
+            it.to.vs[block] = dv ? 0.f : __fdiv_rn(bv, kTopV);
+        }
+    }
+}
+
+// Groups begin, begin + kWarps, .. below end of one tensor, all of them whole and aligned. With BF16
+// parameters and gradients the next group's loads are under way during a group's arithmetic; the
+// wider ones do not fit into the registers beside it.
+template <int BITS, bool P16, bool G16, bool MASTER>
+__device__ __forceinline__ void whole_groups(const OptItem& it, const StepConst& c, float keep, uint64_t key, uint32_t lane, uint32_t begin,
+                                             uint32_t end) {
+    if (begin >= end) return;
+    constexpr bool kAhead = P16 && G16 && !MASTER;
+    Held<BITS> h;
+    if constexpr (kAhead) load_group<BITS>(h, it, begin, uint64_t(begin) * kBlock + 8u * lane, P16, G16, MASTER, true, 8);
+    for (uint32_t b = begin; b < end; b += kWarps) {
+        const uint64_t at = uint64_t(b) * kBlock + 8u * lane;
+        if constexpr (kAhead) {
+            Held<BITS> next;
+            if (b + kWarps < end) load_group<BITS>(next, it, b + kWarps, at + kWarps * kBlock, P16, G16, MASTER, true, 8);
+            step_group<BITS>(h, it, c, keep, key, lane, b, at, P16, G16, MASTER, true, 8);
+            h = next;
+        } else {
+            load_group<BITS>(h, it, b, at, P16, G16, MASTER, true, 8);
+            step_group<BITS>(h, it, c, keep, key, lane, b, at, P16, G16, MASTER, true, 8);
+        }
+    }
+}
+
+// CTAs of a pass that an SM holds: with 32-bit moments 2 of up to 128 registers, which hold the next
+// group, with 8-bit ones 3 of up to 80.
+constexpr int ctas_per_sm(int bits) { return bits == 8 ? 3 : 2; }
+constexpr int kReadCtas = 4;
+// With 32-bit moments the CTAs go through the groups together, 32 (4 a warp) at a time, so that the
+// memory being read and written at any time is a few contiguous stretches: 198M BF16 weights take 655
+// us, against 740 us with one equal run a CTA. With 8-bit ones the search for each run's tensor costs
+// more than that gives (570 us with one run, 600 us with these).
+constexpr uint32_t kRun = 32;
+
 template <int CAP, int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ OptParams<CAP> p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) adamw_kernel(const __grid_constant__ OptParams<CAP> p) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     // Read before this CTA arrives below: the step count moves only after every CTA has arrived.
     const volatile bs_adamw_ctl* ctl = p.ctl;
     const bool skip = ctl->skip != 0;
     if (!skip) {
-        const float lr = ctl->lr, clip = ctl->clip;
         const uint32_t t = p.step ? p.step : static_cast<uint32_t>(ctl->step) + 1u;
         // 1 - b^t = -expm1(t log b): relative error of a few 2^-24 for every t
         const float bc1 = -expm1f(static_cast<float>(t * p.log_b1)), bc2 = -expm1f(static_cast<float>(t * p.log_b2));
-        const float step = lr / bc1, r2 = rsqrtf(bc2);
+        StepConst c{p.b1, p.b2, p.c1, p.c2, p.eps, ctl->clip, ctl->lr, 0.f, rsqrtf(bc2)};
+        c.step = c.lr / bc1;
         const uint64_t key0 = mix64(p.seed + t * 2654435769ull);
-        const uint32_t g0 = blockIdx.x * p.per_cta, g1 = min(g0 + p.per_cta, p.groups);
-        int k = item_of(p, g0, 0);
-        for (uint32_t gr = g0 + warp; gr < g1; gr += kWarps) {
-            if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
+        // A CTA's runs of per_cta groups; a run may cross tensors, and warp w takes the groups at w,
+        // w + 8, .. of it.
+        for (uint32_t g0 = blockIdx.x * p.per_cta; g0 < p.groups; g0 += gridDim.x * p.per_cta) {
+        const uint32_t g1 = min(g0 + p.per_cta, p.groups);
+        for (uint32_t k = static_cast<uint32_t>(item_of(p, g0, 0)); k < p.n_items; ++k) {
             const OptItem& it = p.item[k];
-            const uint64_t block = gr - it.group_begin, at = block * kBlock + 8u * lane;
-            const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
-            const bool full = cnt == 8 && (it.flags & kVec);
-            const bool p16 = it.flags & kP16, g16 = it.flags & kG16;
-            float g[8], m[8], v[8], w[8];
-            load8(g, it.g, at, g16, full, cnt);
-            if (it.master) load8(w, reinterpret_cast<const uint8_t*>(it.master), at, false, full, cnt);
-            else load8(w, it.p, at, p16, full, cnt);
-            if (BITS == 32) {
-                load8(m, it.m, at, false, full, cnt);
-                load8(v, it.v, at, false, full, cnt);
-            } else {
-                const uint2 cm = load_codes(it.m, at, full, cnt), cv = load_codes(it.v, at, full, cnt);
-                decode_m(m, cm, it.ms[block]);
-                decode_v(v, cv, it.vs[block]);
+            const uint32_t base = it.group_begin, lo = max(g0, base);
+            if (lo >= g1) break;
+            const uint32_t last = k + 1 < p.n_items ? p.item[k + 1].group_begin : p.groups;
+            const uint32_t begin = lo + ((warp - (lo - g0)) & (kWarps - 1u)) - base, end = min(g1, last) - base;
+            const float keep = 1.f - c.lr * it.decay;
+            const uint64_t key = BITS == 8 ? mix64(key0 + it.tensor) : 0;
+            const uint32_t whole = it.flags & kVec ? min(end, static_cast<uint32_t>(it.n / kBlock)) : 0u;
+            switch ((it.flags & (kP16 | kG16)) | (it.master ? 4u : 0u)) {
+            case 0: whole_groups<BITS, false, false, false>(it, c, keep, key, lane, begin, whole); break;
+            case kP16: whole_groups<BITS, true, false, false>(it, c, keep, key, lane, begin, whole); break;
+            case kG16: whole_groups<BITS, false, true, false>(it, c, keep, key, lane, begin, whole); break;
+            case kP16 | kG16: whole_groups<BITS, true, true, false>(it, c, keep, key, lane, begin, whole); break;
+            case 4: whole_groups<BITS, false, false, true>(it, c, keep, key, lane, begin, whole); break;
+            case kP16 | 4: whole_groups<BITS, true, false, true>(it, c, keep, key, lane, begin, whole); break;
+            case kG16 | 4: whole_groups<BITS, false, true, true>(it, c, keep, key, lane, begin, whole); break;
+            default: whole_groups<BITS, true, true, true>(it, c, keep, key, lane, begin, whole); break;
             }
-            const float keep = 1.f - lr * it.decay;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float gi = __fmul_rn(g[i], clip);
-                m[i] = __fadd_rn(__fmul_rn(m[i], p.b1), __fmul_rn(gi, p.c1));
-                v[i] = __fadd_rn(__fmul_rn(v[i], p.b2), __fmul_rn(__fmul_rn(gi, p.c2), gi));
-                w[i] = w[i] * keep - step * __fdividef(m[i], sqrtf(v[i]) * r2 + p.eps);
+            // the tensor's last group where it is part-filled, and every group of unaligned tensors
+            uint32_t b = begin;
+            if (whole > begin) b += (whole - begin + kWarps - 1) / kWarps * kWarps;
+            for (; b < end; b += kWarps) {
+                const uint64_t at = uint64_t(b) * kBlock + 8u * lane;
+                const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
+                const bool p16 = it.flags & kP16, g16 = it.flags & kG16, master = it.master != nullptr;
+                Held<BITS> h;
+                load_group<BITS>(h, it, b, at, p16, g16, master, false, cnt);
+                step_group<BITS>(h, it, c, keep, key, lane, b, at, p16, g16, master, false, cnt);
             }
-            store8(w, it.to.p, at, p16, full, cnt);
-            if (it.master) store8(w, reinterpret_cast<uint8_t*>(it.to.master), at, false, full, cnt);
-            if (BITS == 32) {
-                store8(m, it.to.m, at, false, full, cnt);
-                store8(v, it.to.v, at, false, full, cnt);
-            } else {
-                const float bm = block_max(m), bv = block_max(v);
-                const bool dm = bm < kDead, dv = bv < kDead; // false for NaN, which the scale then carries
-                const float im = dm ? 0.f : __fdiv_rn(kTopM, bm), iv = dv ? 0.f : __fdiv_rn(kTopV, bv);
-                const uint64_t key = mix64(key0 + it.tensor);
-                uint32_t qm[2] = {0, 0}, qv[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const uint64_t z = mix64(key + 0x9E3779B97F4A7C15ull * (((at + i) >> 1) + 1));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t u = static_cast<uint32_t>(z >> (32 * h)), e = i + h, sh = 8 * (e & 3);
-                        const uint32_t cm = encode<7, 0x7E>(__fmul_rn(fabsf(m[e]), im), u & 0xFFFFu);
-                        uint32_t cv = encode<15, 0xF7>(__fmul_rn(v[e], iv), u >> 16);
-                        if (v[e] > 0.f && !dv) cv = max(cv, 1u);
-                        qm[e >> 2] |= (cm | ((__float_as_uint(m[e]) >> 24) & 0x80u)) << sh;
-                        qv[e >> 2] |= cv << sh;
-                    }
-                }
-                store_codes(make_uint2(qm[0], qm[1]), it.to.m, at, full, cnt);
-                store_codes(make_uint2(qv[0], qv[1]), it.to.v, at, full, cnt);
-                if (lane == 0) {
-                    it.to.ms[block] = dm ? 0.f : __fdiv_rn(bm, kTopM);
-                    it.to.vs[block] = dv ? 0.f : __fdiv_rn(bv, kTopV);
-                }
-            }
+        }
         }
     }
     if (!p.last) return;
@@ -277,31 +455,49 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         p.ctl->step = p.step ? static_cast<int32_t>(p.step) : p.ctl->step + 1;
 }
 
-// Sum of squares: FP32 over a lane's elements of 8 groups at most, 64 bits from there on. Every
+// Sum of squares: FP32 over a lane's 8 elements of a group, 64 bits from there on. Every
 // CTA's sum goes to its place; the last CTA to arrive adds them in the order of their places.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ OptParams<CAP> p) {
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormParams<CAP> p) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     __shared__ double s_sum[kWarps];
     __shared__ bool s_last;
     double sum = 0;
-    const uint32_t g0 = blockIdx.x * p.per_cta, g1 = min(g0 + p.per_cta, p.groups);
-    if (g0 < g1) {
+    for (uint32_t g0 = blockIdx.x * kRun; g0 < p.groups; g0 += gridDim.x * kRun) { // 4 groups' loads at once
         int k = item_of(p, g0, 0);
-        float part = 0;
-        uint32_t held = 0;
-        for (uint32_t gr = g0 + warp; gr < g1; gr += kWarps) {
-            if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
-            const OptItem& it = p.item[k];
-            const uint64_t at = uint64_t(gr - it.group_begin) * kBlock + 8u * lane;
-            const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
-            float g[8];
-            load8(g, it.g, at, it.flags & kG16, cnt == 8 && (it.flags & kVec), cnt);
+        uint32_t r[4][8];
+        bool b16[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) part = fmaf(g[i], g[i], part);
-            if (++held == 8) { sum += part; part = 0; held = 0; }
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t gr = g0 + warp + j * kWarps;
+            b16[j] = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[j][i] = 0;
+            if (gr < p.groups) {
+                if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
+                const NormItem& it = p.item[k];
+                const uint64_t at = uint64_t(gr - it.group_begin) * kBlock + 8u * lane;
+                const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
+                b16[j] = it.flags & kG16;
+                load_raw(r[j], it.g, at, b16[j], cnt == 8 && (it.flags & kVec), cnt);
+            }
         }
-        sum += part;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            float part = 0;
+            if (b16[j]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float lo = __uint_as_float(r[j][i] << 16), hi = __uint_as_float(r[j][i] & 0xFFFF0000u);
+                    part = fmaf(lo, lo, part);
+                    part = fmaf(hi, hi, part);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) part = fmaf(__uint_as_float(r[j][i]), __uint_as_float(r[j][i]), part);
+            }
+            sum += part;
+        }
     }
     auto cta_sum = [&](double x) { // every thread's x, added in a fixed order; valid in thread 0
 #pragma unroll
@@ -338,19 +534,21 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) read_states_kernel(const __grid_constant__ OptParams<CAP> p) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t g0 = blockIdx.x * p.per_cta, g1 = min(g0 + p.per_cta, p.groups);
-    int k = item_of(p, g0, 0);
-    for (uint32_t gr = g0 + warp; gr < g1; gr += kWarps) {
-        if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
-        const OptItem& it = p.item[k]; // to.m, to.v: FP32
-        const uint64_t block = gr - it.group_begin, at = block * kBlock + 8u * lane;
-        const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
-        const bool full = cnt == 8 && (it.flags & kVec);
-        float f[8];
-        decode_m(f, load_codes(it.m, at, full, cnt), it.ms[block]);
-        store8(f, it.to.m, at, false, full, cnt);
-        decode_v(f, load_codes(it.v, at, full, cnt), it.vs[block]);
-        store8(f, it.to.v, at, false, full, cnt);
+    for (uint32_t g0 = blockIdx.x * p.per_cta; g0 < p.groups; g0 += gridDim.x * p.per_cta) {
+        const uint32_t g1 = min(g0 + p.per_cta, p.groups);
+        int k = item_of(p, g0, 0);
+        for (uint32_t gr = g0 + warp; gr < g1; gr += kWarps) {
+            if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= gr) k = item_of(p, gr, k);
+            const OptItem& it = p.item[k]; // to.m, to.v: FP32
+            const uint64_t block = gr - it.group_begin, at = block * kBlock + 8u * lane;
+            const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
+            const bool full = cnt == 8 && (it.flags & kVec);
+            float f[8];
+            decode_m(f, load_codes(it.m, at, full, cnt), it.ms[block]);
+            store8(f, it.to.m, at, false, full, cnt);
+            decode_v(f, load_codes(it.v, at, full, cnt), it.vs[block]);
+            store8(f, it.to.v, at, false, full, cnt);
+        }
     }
 }
 
@@ -381,29 +579,17 @@ bs_status check_items(int32_t n, const bs_adamw_item* items, uint32_t bits, Pass
     return BS_OK;
 }
 
-bs_status device_ok(int* sms) {
-    int dev = 0, major = 0, minor = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e);
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return major == 10 && minor == 0 ? BS_OK : BS_E_UNSUPPORTED;
-}
-
 uint64_t groups_of(uint64_t n) { return (n + kBlock - 1) / kBlock; }
 
-// The CTAs of a pass: one wave of them (4 an SM, the most that fit), each with an equal run of
-// groups and at least one group a warp. More CTAs than that pay their set-up (the step's
-// constants, the search for the first tensor) for every few groups.
-constexpr uint32_t kNormCtas = 148 * 4;
+// The CTAs of a pass are one wave: more of them would pay their set-up (the step's constants, the
+// search for the first tensor) for every few groups.
+constexpr uint32_t kNormCtas = 148 * 5; // of the norm; not the device's own number, so that the order of the sums is one
 
 template <int CAP>
 bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, uint32_t bits, float* const* rm,
                      float* const* rv, OptParams<CAP>& p, int sms, cudaStream_t s) {
     int32_t k = 0, left = 0;
     for (int32_t i = 0; i < n; ++i) left += items[i].n != 0;
-    p.partial_at = 0;
     do {
         p.n_items = 0;
         uint64_t groups = 0;
@@ -430,8 +616,6 @@ bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, const bs_
                 it.to.m = reinterpret_cast<uint8_t*>(rm[k]);
                 it.to.v = reinterpret_cast<uint8_t*>(rv[k]);
                 vec = aligned(it.m, 8) && aligned(it.v, 8) && aligned(it.to.m, 16) && aligned(it.to.v, 16);
-            } else if (pass == Pass::Norm) {
-                vec = aligned(it.g, 16);
             } else {
                 const uintptr_t a = bits == 8 ? 8 : 16;
                 vec = aligned(it.p, 16) && aligned(it.g, 16) && aligned(it.master, 16) && aligned(it.m, a) && aligned(it.v, a) &&
@@ -443,13 +627,39 @@ bs_status launch_all(Pass pass, int32_t n, const bs_adamw_item* items, const bs_
         }
         p.groups = static_cast<uint32_t>(groups);
         p.last = left == 0;
-        const uint64_t wave = pass == Pass::Norm ? kNormCtas : uint64_t(sms) * 4;
-        p.per_cta = static_cast<uint32_t>(std::max<uint64_t>(kWarps, (groups + wave - 1) / wave));
-        const uint32_t ctas = static_cast<uint32_t>(std::max<uint64_t>(1, (groups + p.per_cta - 1) / p.per_cta));
-        if (pass == Pass::Norm) grad_norm_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
-        else if (pass == Pass::Read) read_states_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
+        const uint64_t wave = uint64_t(sms) * (pass == Pass::Read ? kReadCtas : ctas_per_sm(bits));
+        p.per_cta = static_cast<uint32_t>(std::max<uint64_t>(kWarps, std::min<uint64_t>(pass == Pass::Step && bits == 32 ? kRun : ~0u, (groups + wave - 1) / wave)));
+        const uint32_t ctas = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(wave, (groups + p.per_cta - 1) / p.per_cta)));
+        if (pass == Pass::Read) read_states_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
         else if (bits == 8) adamw_kernel<CAP, 8><<<ctas, kThreads, 0, s>>>(p);
         else adamw_kernel<CAP, 32><<<ctas, kThreads, 0, s>>>(p);
+        count_launch();
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_status(e);
+    } while (left > 0);
+    return BS_OK;
+}
+
+template <int CAP>
+bs_status launch_norm(int32_t n, const bs_adamw_item* items, NormParams<CAP>& p, cudaStream_t s) {
+    int32_t k = 0, left = 0;
+    for (int32_t i = 0; i < n; ++i) left += items[i].n != 0;
+    do {
+        p.n_items = 0;
+        uint64_t groups = 0;
+        for (; k < n && p.n_items < static_cast<uint32_t>(CAP); ++k) {
+            const bs_adamw_item& t = items[k];
+            if (t.n == 0) continue;
+            if (groups + groups_of(t.n) > (1ull << 31)) break;
+            p.item[p.n_items++] = NormItem{static_cast<const uint8_t*>(t.d_grad), t.n, static_cast<uint32_t>(groups),
+                                           (t.grad_type == BS_TYPE_BF16 ? kG16 : 0u) | (aligned(t.d_grad, 16) ? kVec : 0u)};
+            groups += groups_of(t.n);
+            --left;
+        }
+        p.groups = static_cast<uint32_t>(groups);
+        p.last = left == 0;
+        const uint32_t ctas = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(kNormCtas, (groups + kRun - 1) / kRun)));
+        grad_norm_kernel<CAP><<<ctas, kThreads, 0, s>>>(p);
         count_launch();
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_status(e);
@@ -482,8 +692,8 @@ using namespace bs;
 
 extern "C" size_t bs_grad_norm_scratch_bytes(int32_t n, const bs_adamw_item* items) {
     if (check_items(n, items, 32, Pass::Norm) != BS_OK) return 0;
-    // a launch takes kFewItems tensors at least, or all: that many of 2^26 groups stay below 2^31
-    return sizeof(double) * kNormCtas * (2 + static_cast<size_t>(n) / kFewItems);
+    // a launch takes 32 tensors at least, or all: that many of 2^26 groups stay within 2^31
+    return sizeof(double) * kNormCtas * (2 + static_cast<size_t>(n) / 32);
 }
 
 extern "C" bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs_adamw_ctl* d_ctl, void* d_scratch,
@@ -492,19 +702,28 @@ extern "C" bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float m
     if (st != BS_OK) return st;
     if (!d_ctl || !aligned(d_ctl, 16) || !d_scratch || !aligned(d_scratch, 8) || !(max_norm > 0.f)) return BS_E_ARG;
     if (scratch_bytes < bs_grad_norm_scratch_bytes(n, items)) return BS_E_SIZE;
-    int sms = 148;
-    if ((st = device_ok(&sms)) != BS_OK) return st;
-    return launch_sized(Pass::Norm, n, items, items, 32, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != BS_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto& p) {
+        p.partial_at = 0;
         p.max_norm = max_norm;
         p.ctl = d_ctl;
         p.partial = static_cast<double*>(d_scratch);
-    });
+        return launch_norm(n, items, p, s);
+    };
+    if (n <= kFewNorm) {
+        NormParams<kFewNorm> p;
+        return go(p);
+    }
+    std::unique_ptr<NormParams<kManyNorm>> p(new (std::nothrow) NormParams<kManyNorm>);
+    return p ? go(*p) : BS_E_NOMEM;
 }
 
 extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_adamw_item* to, const bs_adamw_params* prm,
                               bs_adamw_ctl* d_ctl, void* stream) {
     if (!prm || !d_ctl || !aligned(d_ctl, 16) || (prm->bits != 8 && prm->bits != 32) || prm->step > 0x7FFFFFFFu) return BS_E_ARG;
-    if (!(prm->beta1 >= 0 && prm->beta1 < 1) || !(prm->beta2 >= 0 && prm->beta2 < 1) || !(prm->eps >= 0) || std::isinf(prm->eps))
+    if (!(prm->beta1 >= 0 && prm->beta1 < 1) || !(prm->beta2 >= 0 && prm->beta2 < 1) || !(prm->eps >= 1e-12 && prm->eps < INFINITY))
         return BS_E_ARG;
     bs_status st = check_items(n, items, prm->bits, Pass::Step);
     if (st != BS_OK) return st;
@@ -515,8 +734,8 @@ extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_ad
         for (int32_t k = 0; k < n; ++k)
             if (to[k].n != items[k].n || to[k].param_type != items[k].param_type || !to[k].d_master != !items[k].d_master) return BS_E_ARG;
     }
-    int sms = 148;
-    if ((st = device_ok(&sms)) != BS_OK) return st;
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != BS_OK) return st;
     return launch_sized(Pass::Step, n, items, to, prm->bits, nullptr, nullptr, sms, static_cast<cudaStream_t>(stream), [&](auto& p) {
         p.b1 = static_cast<float>(prm->beta1);
         p.b2 = static_cast<float>(prm->beta2);
@@ -542,7 +761,7 @@ extern "C" bs_status bs_adamw_read_states(int32_t n, const bs_adamw_item* items,
         if (!d_m[k] || !d_v[k] || !aligned(d_m[k], 4) || !aligned(d_v[k], 4)) return BS_E_ARG;
     }
     if (!any) return BS_OK;
-    int sms = 148;
-    if ((st = device_ok(&sms)) != BS_OK) return st;
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != BS_OK) return st;
     return launch_sized(Pass::Read, n, items, items, 8, d_m, d_v, sms, static_cast<cudaStream_t>(stream), [](auto&) {});
 }

@@ -98,4 +98,8 @@ void fill_tensor_info(const Tensor& t, bs_tensor_info* o);
 // Records e for bs_last_cuda_error and returns BS_E_CUDA.
 bs_status cuda_status(int e);
 
+// The current device and its SMs; BS_E_UNSUPPORTED off sm_100. A device's properties do not change,
+// so they are asked for once.
+bs_status current_device(int* dev, int* sms);
+
 } // namespace bs

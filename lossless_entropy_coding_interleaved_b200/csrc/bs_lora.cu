@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     if (tokens <= kFewTokens) tiles(t8, kFew, o.few);
 }
 
+constexpr uint32_t kPlanSmem = 220 * 1024;
+
 // ---------------------------------------------------------------- what the tiled kernels share
 struct Batch {
     uint32_t tokens, n, rank_max, part_stride; // part_stride: elements of one of the three parts
@@ -642,15 +644,6 @@ bool row_ok(const void* p, uint64_t stride, uint32_t width) { // BF16 rows read 
 bool out_ok(const void* p, uint64_t stride, uint32_t width, uint32_t type) {
     return p && aligned(p, 16) && stride >= width && stride % (type == BS_TYPE_BF16 ? 8 : 4) == 0 && stride <= (1ull << 32);
 }
-bs_status device_sms(int* sms) {
-    int dev = 0, major = 0, minor = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e);
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return major == 10 && minor == 0 ? BS_OK : BS_E_UNSUPPORTED;
-}
 Batch batch_of(const bs_lora_batch& b) {
     Batch o;
     o.tokens = b.tokens;
@@ -662,15 +655,19 @@ Batch batch_of(const bs_lora_batch& b) {
     o.scales = b.d_scales;
     return o;
 }
-template <typename Params>
-bs_status launch(void (*fn)(const Params), dim3 grid, uint32_t smem, uint32_t cluster, cudaStream_t s, const Params& p) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+struct Gpu {
+    int dev = 0, sms = 148;
+    cudaStream_t s = nullptr;
+};
+template <auto FN, typename Params>
+bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, const Params& p) {
+    cudaError_t e = allow_smem<FN>(gpu.dev, smem);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kTiledThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
+    cfg.stream = gpu.s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
@@ -678,7 +675,7 @@ bs_status launch(void (*fn)(const Params), dim3 grid, uint32_t smem, uint32_t cl
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fn, p);
+    e = cudaLaunchKernelEx(&cfg, FN, p);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
@@ -691,45 +688,45 @@ uint32_t split_for(uint64_t ctas, uint32_t steps, int sms) {
 }
 
 template <bool WT>
-bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     uint32_t steps = ~0u;
     for (uint32_t k = 0; k < jobs; ++k) steps = std::min(steps, (p.job[k].width + 63) / 64);
     const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
-    p.split = split_for(uint64_t(std::min(cap, (p.b.tokens + kTile - 1) / kTile)) * jobs, steps, sms);
+    p.split = split_for(uint64_t(std::min(cap, (p.b.tokens + kTile - 1) / kTile)) * jobs, steps, gpu.sms);
     const dim3 grid(cap * p.split, jobs);
     switch (R) {
-    case 16: return launch(lora_shrink_kernel<16, WT>, grid, shrink_smem<16, WT>(), p.split, s, p);
-    case 32: return launch(lora_shrink_kernel<32, WT>, grid, shrink_smem<32, WT>(), p.split, s, p);
-    case 64: return launch(lora_shrink_kernel<64, WT>, grid, shrink_smem<64, WT>(), p.split, s, p);
-    default: return launch(lora_shrink_kernel<128, WT>, grid, shrink_smem<128, WT>(), p.split, s, p);
+    case 16: return launch<lora_shrink_kernel<16, WT>>(grid, shrink_smem<16, WT>(), p.split, gpu, p);
+    case 32: return launch<lora_shrink_kernel<32, WT>>(grid, shrink_smem<32, WT>(), p.split, gpu, p);
+    case 64: return launch<lora_shrink_kernel<64, WT>>(grid, shrink_smem<64, WT>(), p.split, gpu, p);
+    default: return launch<lora_shrink_kernel<128, WT>>(grid, shrink_smem<128, WT>(), p.split, gpu, p);
     }
 }
 template <bool WT>
-bs_status launch_expand(ExpandParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+bs_status launch_expand(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     uint32_t blocks = 1;
     for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
     const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
     // a CTA keeps its tokens' parts for up to 8 blocks, as long as 8 CTAs an SM are left
     p.blocks = 1;
-    while (p.blocks < 8 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 8ull * sms) p.blocks *= 2;
+    while (p.blocks < 8 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 8ull * gpu.sms) p.blocks *= 2;
     const dim3 grid((blocks + p.blocks - 1) / p.blocks, cap, jobs);
     switch (R) {
-    case 16: return launch(lora_expand_kernel<16, WT>, grid, expand_smem<16, WT>(), 1, s, p);
-    case 32: return launch(lora_expand_kernel<32, WT>, grid, expand_smem<32, WT>(), 1, s, p);
-    case 64: return launch(lora_expand_kernel<64, WT>, grid, expand_smem<64, WT>(), 1, s, p);
-    default: return launch(lora_expand_kernel<128, WT>, grid, expand_smem<128, WT>(), 1, s, p);
+    case 16: return launch<lora_expand_kernel<16, WT>>(grid, expand_smem<16, WT>(), 1, gpu, p);
+    case 32: return launch<lora_expand_kernel<32, WT>>(grid, expand_smem<32, WT>(), 1, gpu, p);
+    case 64: return launch<lora_expand_kernel<64, WT>>(grid, expand_smem<64, WT>(), 1, gpu, p);
+    default: return launch<lora_expand_kernel<128, WT>>(grid, expand_smem<128, WT>(), 1, gpu, p);
     }
 }
-bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     uint32_t blocks = 1;
     for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
-    p.split = split_for(uint64_t(blocks) * jobs * p.b.n, p.b.tokens / p.b.n / kOuterTok, sms);
+    p.split = split_for(uint64_t(blocks) * jobs * p.b.n, p.b.tokens / p.b.n / kOuterTok, gpu.sms);
     const dim3 grid(blocks * p.split, p.b.n, jobs);
     switch (R) {
-    case 16: return launch(lora_outer_kernel<16>, grid, outer_smem<16>(), p.split, s, p);
-    case 32: return launch(lora_outer_kernel<32>, grid, outer_smem<32>(), p.split, s, p);
-    case 64: return launch(lora_outer_kernel<64>, grid, outer_smem<64>(), p.split, s, p);
-    default: return launch(lora_outer_kernel<128>, grid, outer_smem<128>(), p.split, s, p);
+    case 16: return launch<lora_outer_kernel<16>>(grid, outer_smem<16>(), p.split, gpu, p);
+    case 32: return launch<lora_outer_kernel<32>>(grid, outer_smem<32>(), p.split, gpu, p);
+    case 64: return launch<lora_outer_kernel<64>>(grid, outer_smem<64>(), p.split, gpu, p);
+    default: return launch<lora_outer_kernel<128>>(grid, outer_smem<128>(), p.split, gpu, p);
     }
 }
 
@@ -755,15 +752,15 @@ extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_
     if (need == 0) return BS_E_ARG;
     if ((tokens && !d_idx) || !aligned(d_idx, 4) || !d_plan || !aligned(d_plan, 16) || !aligned(d_err, 4)) return BS_E_ARG;
     if (plan_bytes < need) return BS_E_SIZE;
-    int sms = 148;
-    const bs_status st = device_sms(&sms);
+    int dev = 0, sms = 0;
+    const bs_status st = current_device(&dev, &sms);
     if (st != BS_OK) return st;
     // as many counting warps as their tables fit into shared memory, and as have tokens
     const uint32_t nb = n_adapters + 1;
-    const uint32_t fit = 220 * 1024 / 4 / nb - 4;
+    const uint32_t fit = kPlanSmem / 4 / nb - 4;
     const uint32_t warps = std::max(1u, std::min({32u, fit, (tokens + 31) / 32}));
     const uint32_t smem = 4 * (warps * nb + 3 * (nb + 1));
-    cudaError_t e = cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_smem<lora_plan_kernel>(dev, kPlanSmem);
     if (e != cudaSuccess) return cuda_status(e);
     lora_plan_kernel<<<1, 1024, smem, static_cast<cudaStream_t>(stream)>>>(d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
     count_launch();
@@ -785,11 +782,11 @@ extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const
             if (items[q].d_h == t.d_h || (t.d_y && items[q].d_y == t.d_y)) return BS_E_ARG;
         if (t.d_base && (!t.d_y || !out_ok(t.d_base, t.base_stride, t.rows, t.type))) return BS_E_ARG;
     }
-    int sms = 148;
-    if ((st = device_sms(&sms)) != BS_OK) return st;
+    Gpu gpu;
+    gpu.s = static_cast<cudaStream_t>(stream);
+    if ((st = current_device(&gpu.dev, &gpu.sms)) != BS_OK) return st;
     if (n == 0 || batch->tokens == 0) return BS_OK;
     const uint32_t R = padded_rank(batch->rank_max);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     ShrinkParams sp;
     ExpandParams ep;
     sp.b = ep.b = batch_of(*batch);
@@ -806,8 +803,8 @@ extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const
                                      t.rows, outs, 1, t.type};
             ++outs;
         }
-        if ((st = launch_shrink<false>(sp, m, R, sms, s)) != BS_OK) return st;
-        if (outs && (st = launch_expand<false>(ep, outs, R, sms, s)) != BS_OK) return st;
+        if ((st = launch_shrink<false>(sp, m, R, gpu)) != BS_OK) return st;
+        if (outs && (st = launch_expand<false>(ep, outs, R, gpu)) != BS_OK) return st;
     }
     return BS_OK;
 }
@@ -834,11 +831,11 @@ extern "C" bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, cons
                  items[q].type != t.type || items[q].cols != t.cols || q / kMaxItems != k / kMaxItems))
                 return BS_E_ARG;
     }
-    int sms = 148;
-    if ((st = device_sms(&sms)) != BS_OK) return st;
+    Gpu gpu;
+    gpu.s = static_cast<cudaStream_t>(stream);
+    if ((st = current_device(&gpu.dev, &gpu.sms)) != BS_OK) return st;
     if (n == 0) return BS_OK;
     const uint32_t R = padded_rank(batch->rank_max);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     ShrinkParams sp;
     ExpandParams ep;
     OuterParams op;
@@ -866,10 +863,10 @@ extern "C" bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, cons
                 }
         }
         if (batch->tokens) {
-            if ((st = launch_shrink<true>(sp, m, R, sms, s)) != BS_OK) return st;
-            if (outs && (st = launch_expand<true>(ep, outs, R, sms, s)) != BS_OK) return st;
+            if ((st = launch_shrink<true>(sp, m, R, gpu)) != BS_OK) return st;
+            if (outs && (st = launch_expand<true>(ep, outs, R, gpu)) != BS_OK) return st;
         }
-        if ((st = launch_outer(op, 2 * m, R, sms, s)) != BS_OK) return st;
+        if ((st = launch_outer(op, 2 * m, R, gpu)) != BS_OK) return st;
     }
     return BS_OK;
 }

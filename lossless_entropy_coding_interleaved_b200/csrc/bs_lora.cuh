@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "bs_device.cuh"
@@ -73,6 +74,17 @@ __device__ __forceinline__ void split3(float f, uint32_t (&q)[3]) {
     q[1] = bf16_of(r1);
     const float r2 = r1 - __uint_as_float(q[1] << 16);
     q[2] = bf16_of(r2);
+}
+
+// Raises a kernel's limit of dynamic shared memory, once per device (the limit stays).
+template <auto FN>
+inline cudaError_t allow_smem(int dev, uint32_t smem) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 } // namespace lora

@@ -124,6 +124,23 @@ bs_status bs::cuda_status(int e) {
     return BS_E_CUDA;
 }
 
+bs_status bs::current_device(int* dev, int* sms) {
+    static std::atomic<int> known[64]; // 0: not asked yet, -1: not sm_100, else the SMs
+    const cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    int n = *dev < 64 ? known[*dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        int major = 0, minor = 0;
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (major != 10 || minor != 0 || n <= 0) n = -1;
+        if (*dev < 64) known[*dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return n > 0 ? BS_OK : BS_E_UNSUPPORTED;
+}
+
 bs_status bs::parse_host_container(const uint8_t* h, uint64_t len, std::vector<Tensor>& out) {
     if (!h) return BS_E_ARG;
     Reader rd;

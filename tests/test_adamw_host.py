@@ -39,7 +39,7 @@ def test_step_refusals_before_any_launch():
     assert _step(_item(), None) == bs.E_ARG and _step(_item(), ok, ctl=None) == bs.E_ARG and _step(_item(), ok, ctl=8) == bs.E_ARG
     assert _step(None, ok) == bs.E_ARG and _step(_item(), ok, n=-1) == bs.E_ARG
     for p in (_prm(bits=16), _prm(bits=0), _prm(step=1 << 31), _prm(beta1=1.0), _prm(beta2=1.5), _prm(beta1=-0.1),
-              _prm(beta2=float("nan")), _prm(eps=-1e-8), _prm(eps=float("inf"))):
+              _prm(beta2=float("nan")), _prm(eps=-1e-8), _prm(eps=0.0), _prm(eps=float("inf"))):
         assert _step(_item(), p) == bs.E_ARG
     for it in (_item(d_m_scale=None), _item(d_v_scale=None), _item(d_m_scale=2), _item(d_v_scale=3)):
         assert _step(it, _prm(bits=8)) == bs.E_ARG

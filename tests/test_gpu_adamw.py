@@ -4,7 +4,7 @@ Tolerances, in roundings of 2^-24 each. m: a term of it has its factor, the clip
 product and the sum rounded: 4 of the sum of the terms' magnitudes (they can cancel). v: its factor,
 the clip product (squared: 2), two products and the sum: 6, taken as 8. The step
 s = lr / c1 * m / (sqrt(v) r + eps): lr 1, c1 4 (its argument and two units in the last place of
-expm1f), their quotient 1, r 2 + 4 (half of c2's, two units of rsqrtf), root 1 + half of v's 8,
+expm1f), their quotient 1, r 2 + 4 (half of c2's, two units of rsqrtf), root 2 + half of v's 8,
 product 1, sum 1, quotient 4 (two units), product 1: 24, plus m's own; the parameter is rounded
 three times on its way: 3 of (|p| + |s|). A BF16 parameter is rounded once more, 2^-8 of its value.
 8-bit codes have to be equal to those of the same formula in rounded FP32 operations, bit for bit.
