@@ -37,7 +37,7 @@ namespace cg = cooperative_groups;
 // bucket, and after a scan over buckets and warps put them in their places, 32 at a time; lanes of
 // the same bucket are ranked by their lane. No order depends on timing.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restrict__ idx, uint32_t tokens, uint32_t n,
-                                                         uint32_t* __restrict__ plan, uint32_t warps, uint32_t* err) {
+                                                         uint32_t* plan, uint32_t warps, uint32_t* err) {
     extern __shared__ uint32_t sm[];
     __shared__ uint32_t s_scan[3][32], s_carry[3];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, nb = n + 1; // buckets
@@ -134,37 +134,31 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
             __syncwarp();
             if (a < nb) plan[o.perm + at] = t + lane;
         }
-    auto tiles = [&](const uint32_t* tb, uint32_t size, uint64_t at) {
-        for (uint32_t i = tid; i < tb[nb]; i += blockDim.x) {
-            uint32_t lo = 0, hi = nb - 1; // the last bucket whose first tile is at or before i
-            while (lo < hi) {
-                const uint32_t mid = (lo + hi + 1) >> 1;
-                if (tb[mid] <= i) lo = mid;
-                else hi = mid - 1;
-            }
-            const uint32_t f = first[lo] + (i - tb[lo]) * size;
-            reinterpret_cast<uint4*>(plan + at)[i] = make_uint4(lo, f, min(size, first[lo + 1] - f), 0);
+    auto tile_at = [&](const uint32_t* tb, uint32_t size, uint32_t i) {
+        uint32_t lo = 0, hi = nb - 1; // the last bucket whose first tile is at or before i
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi + 1) >> 1;
+            if (tb[mid] <= i) lo = mid;
+            else hi = mid - 1;
         }
+        const uint32_t f = first[lo] + (i - tb[lo]) * size;
+        return make_uint4(lo, f, min(size, first[lo + 1] - f), 0);
     };
-    tiles(t128, kTile, o.tiles);
-    if (tokens <= kFewTokens) tiles(t8, kFew, o.few);
+    for (uint32_t i = tid; i < t128[nb]; i += blockDim.x) reinterpret_cast<uint4*>(plan + o.tiles)[i] = tile_at(t128, kTile, i);
+    if (tokens > kFewTokens) return;
+    __syncthreads(); // perm is complete
+    for (uint32_t i = tid; i < t8[nb] * kFew; i += blockDim.x) { // a thread for each token of a tile
+        const uint4 t = tile_at(t8, kFew, i / kFew);
+        FewTile& e = reinterpret_cast<FewTile*>(plan + o.few)[i / kFew];
+        const uint32_t j = i % kFew;
+        e.token[j] = j < t.z ? plan[o.perm + t.y + j] : ~0u;
+        if (j == 0) *reinterpret_cast<uint4*>(&e) = t;
+    }
 }
 
 constexpr uint32_t kPlanSmem = 220 * 1024;
 
 // ---------------------------------------------------------------- what the tiled kernels share
-struct Batch {
-    uint32_t tokens, n, rank_max, part_stride; // part_stride: elements of one of the three parts
-    const uint32_t* plan;
-    const int32_t* ranks;  // nullptr: every adapter has rank_max
-    const float* scales;   // nullptr: 1
-};
-__device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
-    if (!b.ranks) return b.rank_max;
-    const int32_t r = __ldg(b.ranks + a);
-    return r < 0 ? 0u : min(static_cast<uint32_t>(r), b.rank_max);
-}
-
 constexpr int kTiledThreads = 256;
 // Rows in shared memory are padded by 16 bytes, so that the 8 rows of an 8 x 8 matrix lie in
 // different banks for every rank.
@@ -680,6 +674,9 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
 }
+// Whether a batch goes through the decoding kernel.
+bool few_tokens(uint32_t tokens, uint32_t n) { return tokens <= 128 || (tokens <= kFewTokens && tokens <= 4 * n); }
+
 // CTAs of a cluster that share a sum: the least power of two up to 8 that fills the GPU
 uint32_t split_for(uint64_t ctas, uint32_t steps, int sms) {
     uint32_t c = 1;
@@ -758,11 +755,13 @@ extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_
     // as many counting warps as their tables fit into shared memory, and as have tokens
     const uint32_t nb = n_adapters + 1;
     const uint32_t fit = kPlanSmem / 4 / nb - 4;
-    const uint32_t warps = std::max(1u, std::min({32u, fit, (tokens + 31) / 32}));
+    const uint32_t warps = std::max(1u, std::min({32u, fit, (tokens + 31) / 32})); // at most threads / 32 below
     const uint32_t smem = 4 * (warps * nb + 3 * (nb + 1));
     cudaError_t e = allow_smem<lora_plan_kernel>(dev, kPlanSmem);
     if (e != cudaSuccess) return cuda_status(e);
-    lora_plan_kernel<<<1, 1024, smem, static_cast<cudaStream_t>(stream)>>>(d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
+    // a thread for each token or bucket; a small block passes its barriers sooner (the scan needs 3 warps)
+    const uint32_t threads = std::min(1024u, std::max(128u, (std::max(tokens, nb) + 31) & ~31u));
+    lora_plan_kernel<<<1, threads, smem, static_cast<cudaStream_t>(stream)>>>(d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
     count_launch();
     e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
@@ -787,6 +786,21 @@ extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const
     if ((st = current_device(&gpu.dev, &gpu.sms)) != BS_OK) return st;
     if (n == 0 || batch->tokens == 0) return BS_OK;
     const uint32_t R = padded_rank(batch->rank_max);
+    if (few_tokens(batch->tokens, batch->n_adapters)) {
+        FewParams fp;
+        fp.b = batch_of(*batch);
+        for (int32_t k0 = 0; k0 < n; k0 += kMaxItems) {
+            const uint32_t m = static_cast<uint32_t>(std::min(n - k0, kMaxItems));
+            for (uint32_t k = 0; k < m; ++k) {
+                const bs_lora_item& t = items[k0 + k];
+                fp.job[k] = FewJob{static_cast<const uint16_t*>(t.d_x), static_cast<const uint16_t*>(t.d_a), static_cast<const uint16_t*>(t.d_b),
+                                   static_cast<const uint8_t*>(t.d_base), static_cast<uint8_t*>(t.d_y), static_cast<uint16_t*>(t.d_h),
+                                   t.x_stride, t.base_stride, t.y_stride, t.rows, t.cols, t.type, 0};
+            }
+            if ((st = launch_few(fp, m, R, gpu.sms, gpu.s)) != BS_OK) return st;
+        }
+        return BS_OK;
+    }
     ShrinkParams sp;
     ExpandParams ep;
     sp.b = ep.b = batch_of(*batch);

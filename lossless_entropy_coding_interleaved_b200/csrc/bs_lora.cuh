@@ -25,7 +25,11 @@ constexpr int kMaxItems = 16;     // projections of one launch
 //   adapter follow), [2] and [3] the same for kFew (0 above kFewTokens), [4] tokens, [5] adapters
 //   begin[n_adapters + 2]: the first place of each bucket, then the end
 //   perm[tokens]: the token at each place
-//   tiles, tiles of kFew: (bucket, first place, tokens, 0) each
+//   tiles: (bucket, first place, tokens, 0) each
+//   tiles of kFew: the same, and the tokens themselves
+struct FewTile {
+    uint32_t bucket, first, count, pad, token[kFew]; // token: ~0 past the count
+};
 struct PlanAt {
     uint64_t begin, perm, tiles, few, words;
 };
@@ -40,11 +44,42 @@ __host__ __device__ inline PlanAt plan_at(uint32_t tokens, uint32_t n) {
     o.perm = o.begin + up4(n + 2);
     o.tiles = o.perm + up4(tokens);
     o.few = o.tiles + 4ull * tile_cap(tokens, n, kTile);
-    o.words = o.few + (tokens <= kFewTokens ? 4ull * tile_cap(tokens, n, kFew) : 0);
+    o.words = o.few + (tokens <= kFewTokens ? sizeof(FewTile) / 4 * tile_cap(tokens, n, kFew) : 0);
     return o;
 }
 // Rank rows of the kernels: 16, 32, 64 or 128, the least that holds rank_max.
 inline uint32_t padded_rank(uint32_t rank_max) { return rank_max <= 16 ? 16 : rank_max <= 32 ? 32 : rank_max <= 64 ? 64 : 128; }
+
+// What every kernel knows of the batch.
+struct Batch {
+    uint32_t tokens, n, rank_max, part_stride; // part_stride: elements of one of the three parts
+    const uint32_t* plan;
+    const int32_t* ranks;  // nullptr: every adapter has rank_max
+    const float* scales;   // nullptr: 1
+};
+__device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
+    if (!b.ranks) return b.rank_max;
+    const int32_t r = __ldg(b.ranks + a);
+    return r < 0 ? 0u : min(static_cast<uint32_t>(r), b.rank_max);
+}
+
+// The decoding kernel (bs_lora_few.cu): a cluster takes up to kFew tokens of one adapter through
+// both products.
+constexpr uint32_t kFewCluster = 8, kFewThreads = 256;
+struct FewJob {
+    const uint16_t *x, *a, *b;
+    const uint8_t* base; // nullptr: 0
+    uint8_t* out;        // nullptr: h only
+    uint16_t* h;         // three parts of [tokens][R], in the plan's order
+    uint64_t x_stride, base_stride, out_stride;
+    uint32_t rows, cols, bf16, pad;
+};
+struct FewParams {
+    Batch b;
+    uint32_t split, pad; // clusters of a tile
+    FewJob job[kMaxItems];
+};
+bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s);
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

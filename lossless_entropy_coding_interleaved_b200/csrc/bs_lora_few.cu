@@ -1,0 +1,265 @@
+// bs_lora_few.cu -- the adapters' forward product for batches of few tokens, as in decoding.
+//
+//   h[t] = s_a A_a x[t],  y[t] = base[t] + B_a h[t]
+//
+// With a token or a few per adapter the product is bound by the bytes of A and B, and at the
+// smallest sizes by latency: two kernels with a trip of h through memory between them would cost
+// more than the bytes. So one cluster of 8 CTAs takes up to 8 tokens of one adapter through both
+// products: its 64 warps share the K range of A x, the CTAs exchange their sums of h (rank x 8
+// numbers each) through distributed shared memory, and the warps share the rows of B h. The
+// cluster asks for its part of B (into L2) before it starts on A.
+//
+// Weights are the matrix instructions' 16-row operand and the tokens the 8 columns of the other, so
+// weights go from global memory to registers in the order that they lie in: a sum does not depend on
+// the order of its terms, so each lane takes 16 (A) or 8 (B) contiguous bytes of a row and the tokens' side
+// is indexed to match. Nothing is staged in shared memory but h. h enters the second product as three
+// BF16 numbers (24 bits).
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "bs_lora.cuh"
+
+namespace bs {
+namespace lora {
+namespace {
+namespace cg = cooperative_groups;
+
+constexpr uint32_t kWarps = kFewThreads / 32, kSlices = kFewCluster * kWarps;
+
+__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// What a lane has of a block of 128 rows of B: words of its rows g and g + 8 of the warp's 16 (for
+// R = 16, 4 ranks of each; else 8 ranks of each 32), and base of its rows and tokens.
+template <int R>
+struct BRows {
+    static constexpr int W = R == 16 ? 2 : R / 8; // words of a row
+    uint32_t lo[W], hi[W];
+    float base[2][2]; // [row][token]
+};
+
+template <int R>
+__global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lora_few_kernel(const __grid_constant__ FewParams p) {
+    constexpr int MT = R / 16;
+    __shared__ __align__(16) float s_red[kWarps][R * 8], s_part[R * 8], s_h[R * 8]; // [rank][token]
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g = lane >> 2, q = lane & 3u;
+    const uint32_t cta = blockIdx.x % kFewCluster, part = blockIdx.x / kFewCluster % p.split, tile = blockIdx.x / kFewCluster / p.split;
+    const FewJob& job = p.job[blockIdx.y];
+    const uint32_t N = job.rows, K = job.cols, rm = p.b.rank_max;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    const FewTile* entry = reinterpret_cast<const FewTile*>(p.b.plan + o.few) + tile;
+    const uint32_t a = entry->bucket, first = entry->first, count = entry->count, tok_g = entry->token[g];
+    const uint32_t tok[2] = {entry->token[2 * q], entry->token[2 * q + 1]}; // ~0 past the count
+    if (tile >= p.b.plan[3]) return; // the whole cluster
+    if (a >= p.b.n) { // tokens without an adapter: base as it is
+        if (!job.out || (job.base == job.out && job.base_stride == job.out_stride)) return;
+        const uint32_t es = job.bf16 ? 2 : 4, pieces = N * es / 16;
+        for (uint32_t t = 0; t < count; ++t) {
+            const uint4* src = reinterpret_cast<const uint4*>(job.base + uint64_t(entry->token[t]) * job.base_stride * es);
+            uint4* dst = reinterpret_cast<uint4*>(job.out + uint64_t(entry->token[t]) * job.out_stride * es);
+            for (uint32_t i = (part * kFewCluster + cta) * kFewThreads + tid; i < pieces; i += p.split * kFewCluster * kFewThreads)
+                dst[i] = job.base ? src[i] : make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    const uint32_t rank = rank_of(p.b, a);
+    const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
+    const uint16_t* A = job.a + uint64_t(a) * rm * K;
+    const uint16_t* B = job.b + uint64_t(a) * rm * N;
+    // the rows of B h in blocks of 128, dealt out to the CTAs of the tile's clusters, 16 rows a warp
+    const uint32_t blocks = job.out ? (N + 127) / 128 : 0, b0 = part * kFewCluster + cta, deal = p.split * kFewCluster;
+    for (uint32_t b = b0; b < blocks; b += deal) {
+        const uint8_t* run = reinterpret_cast<const uint8_t*>(B + uint64_t(b) * 128 * rm);
+        const uint32_t bytes = min(128u, N - b * 128) * rm * 2;
+        for (uint32_t at = tid * 128; at < bytes; at += kFewThreads * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(run + at));
+    }
+    // ---- A x: the warp's columns, 64 at a time; lane (g, q) has row g (and g + 8) of each 16 ranks,
+    // token g, and columns 8 q .. 8 q + 7 of each half of the 64. A warp's chain of sums is K / 1024
+    // matrix instructions long.
+    const uint16_t* x = g < count ? job.x + uint64_t(tok_g) * job.x_stride : nullptr;
+    float acc[MT][4] = {};
+    for (uint32_t k0 = (cta * kWarps + warp) * 64; k0 < K; k0 += kSlices * 64) {
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half) {
+            const uint32_t k = k0 + 32 * half + 8 * q;
+            const bool on = k < K;
+            uint4 xv = make_uint4(0, 0, 0, 0);
+            if (on && x) xv = ld16(x + k);
+            uint4 lo[MT], hi[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                lo[m] = hi[m] = make_uint4(0, 0, 0, 0);
+                if (on && 16 * m + g < rank) lo[m] = ld16(A + uint64_t(16 * m + g) * K + k);
+                if (on && 16 * m + g + 8 < rank) hi[m] = ld16(A + uint64_t(16 * m + g + 8) * K + k);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t a0[4] = {lo[m].x, hi[m].x, lo[m].y, hi[m].y}, a1[4] = {lo[m].z, hi[m].z, lo[m].w, hi[m].w};
+                mma16816(acc[m], a0, xv.x, xv.y);
+                mma16816(acc[m], a1, xv.z, xv.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        *reinterpret_cast<float2*>(&s_red[warp][(16 * m + g) * 8 + 2 * q]) = make_float2(acc[m][0], acc[m][1]);
+        *reinterpret_cast<float2*>(&s_red[warp][(16 * m + g + 8) * 8 + 2 * q]) = make_float2(acc[m][2], acc[m][3]);
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < R * 8; i += kFewThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) v += s_red[w][i];
+        s_part[i] = v;
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();
+    // ranks past the adapter's are cut off: bits of this lane's pairs of the last 16 or 32
+    constexpr uint32_t kStep = R == 16 ? 16 : 32, kLane = kStep / 4; // ranks of a lane in each step
+    constexpr int W = BRows<R>::W, WS = kLane / 2;                   // words of a row, and in each step
+    const uint32_t steps = (rank + kStep - 1) / kStep;
+    uint32_t mask[WS];
+#pragma unroll
+    for (int i = 0; i < WS; ++i) {
+        const uint32_t k = (steps - 1) * kStep + kLane * q + 2 * i; // not used where there are no steps
+        mask[i] = k + 1 < rank ? ~0u : k < rank ? 0xFFFFu : 0u;
+    }
+    auto load = [&](uint32_t b) {
+        BRows<R> r;
+        const uint32_t n = b * 128 + warp * 16 + g;
+        const bool in = b < blocks;
+#pragma unroll
+        for (int m = 0; m < W / WS; ++m)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t(&d)[W] = half ? r.hi : r.lo;
+                const uint16_t* src = B + uint64_t(n + 8 * half) * rm + kStep * m + kLane * q;
+                const bool on = in && n + 8 * half < N && kStep * m + kLane * q < rank;
+                if constexpr (WS == 2) {
+                    const uint2 v = on ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+                    d[0] = v.x; d[1] = v.y;
+                } else {
+                    const uint4 v = on ? ld16(src) : make_uint4(0, 0, 0, 0);
+                    d[4 * m] = v.x; d[4 * m + 1] = v.y; d[4 * m + 2] = v.z; d[4 * m + 3] = v.w;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                r.base[half][i] = 0.f;
+                if (in && job.base && tok[i] != ~0u && n + 8 * half < N) {
+                    const uint64_t at = uint64_t(tok[i]) * job.base_stride + n + 8 * half;
+                    r.base[half][i] = job.bf16 ? __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(job.base)[at]) << 16)
+                                               : reinterpret_cast<const float*>(job.base)[at];
+                }
+            }
+        return r;
+    };
+    BRows<R> cur = load(b0); // under way while the sums of h are exchanged
+    cluster.barrier_wait();
+    for (uint32_t i = tid; i < R * 8; i += kFewThreads) {
+        float peer[kFewCluster], v = 0.f;
+#pragma unroll
+        for (uint32_t c = 0; c < kFewCluster; ++c) peer[c] = cluster.map_shared_rank(s_part, c)[i];
+#pragma unroll
+        for (uint32_t c = 0; c < kFewCluster; ++c) v += peer[c];
+        s_h[i] = (i >> 3) < rank && (i & 7u) < count ? v * scale : 0.f;
+    }
+    cluster.barrier_arrive(); // the peers' sums have been read
+    __syncthreads();
+    if (part == 0 && cta < count && tid < R / 2) { // CTA c writes token c's h
+        uint32_t lo[3], hi[3];
+        split3(s_h[2 * tid * 8 + cta], lo);
+        split3(s_h[(2 * tid + 1) * 8 + cta], hi);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(job.h) + (uint64_t(first + cta) * R) / 2 + tid;
+#pragma unroll
+        for (int t = 0; t < 3; ++t) dst[uint64_t(t) * (p.b.part_stride / 2)] = lo[t] | (hi[t] << 16);
+    }
+    // ---- B h: the token's side of each step, in the order of the lane's words
+    uint32_t hf[W][3];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        uint32_t lo[3], hi[3];
+        const uint32_t k = w / WS * kStep + kLane * q + 2 * (w % WS);
+        split3(s_h[k * 8 + g], lo);
+        split3(s_h[(k + 1) * 8 + g], hi);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) hf[w][t] = lo[t] | (hi[t] << 16);
+    }
+    for (uint32_t b = b0; b < blocks; b += deal) {
+        const BRows<R> next = load(b + deal);
+        const uint32_t n = b * 128 + warp * 16 + g;
+        float d[4] = {};
+#pragma unroll
+        for (int m = 0; m < W / WS; ++m) {
+            if (static_cast<uint32_t>(m) >= steps) break;
+            const bool last = static_cast<uint32_t>(m) + 1 == steps;
+#pragma unroll
+            for (int i = 0; i < WS; i += 2) {
+                const int w = m * WS + i;
+                const uint32_t m0 = last ? mask[i] : ~0u, m1 = last ? mask[i + 1] : ~0u;
+                const uint32_t af[4] = {cur.lo[w] & m0, cur.hi[w] & m0, cur.lo[w + 1] & m1, cur.hi[w + 1] & m1};
+#pragma unroll
+                for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (tok[i] != ~0u && n + 8 * half < N) {
+                    const uint64_t at = uint64_t(tok[i]) * job.out_stride + n + 8 * half;
+                    const float v = cur.base[half][i] + d[2 * half + i];
+                    if (job.bf16) reinterpret_cast<uint16_t*>(job.out)[at] = static_cast<uint16_t>(bf16_of(v));
+                    else reinterpret_cast<float*>(job.out)[at] = v;
+                }
+        cur = next;
+    }
+    cluster.barrier_wait();
+}
+
+template <int R>
+bs_status launch(FewParams& p, uint32_t jobs, int sms, cudaStream_t s) {
+    // Where few tiles leave SMs idle, several clusters share a tile's rows of B h, and each works out
+    // the whole of h, which costs them the same time.
+    const uint32_t tiles = tile_cap(p.b.tokens, p.b.n, kFew);
+    p.split = 1;
+    while (p.split < 4 && tiles * jobs * kFewCluster * p.split * 2 <= static_cast<uint32_t>(sms)) p.split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * p.split * kFewCluster, jobs);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kFewCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see the kernel's wait
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, lora_few_kernel<R>, p);
+    count_launch();
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? BS_OK : cuda_status(e);
+}
+
+} // namespace
+
+bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+    switch (R) {
+    case 16: return launch<16>(p, jobs, sms, s);
+    case 32: return launch<32>(p, jobs, sms, s);
+    case 64: return launch<64>(p, jobs, sms, s);
+    default: return launch<128>(p, jobs, sms, s);
+    }
+}
+
+} // namespace lora
+} // namespace bs

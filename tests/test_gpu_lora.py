@@ -237,7 +237,13 @@ def test_plan_groups_in_order(tokens, n):
             assert count[0] == count[1] == 0
             continue
         assert count[1] == len(want) and count[0] == sum(t[0] < n for t in want)
-        assert np.array_equal(w[start:start + 4 * len(want)].reshape(-1, 4), np.array(want, np.uint32).reshape(-1, 4))
+        words = 4 if size == 128 else 12
+        got = w[start:start + words * len(want)].reshape(-1, words)
+        assert np.array_equal(got[:, :4], np.array(want, np.uint32).reshape(-1, 4))
+        if size == 8:  # the tokens themselves follow, -1 behind the last
+            perm = np.concatenate([np.argsort(bucket, kind="stable"), np.zeros(8, np.int64)])
+            for row, (_, f, c, _) in zip(got, want):
+                assert np.array_equal(row[4:4 + c], perm[f:f + c]) and np.all(row[4 + c:] == 0xFFFFFFFF)
 
 
 def test_an_index_past_the_adapters_counts_as_none_and_is_reported():
