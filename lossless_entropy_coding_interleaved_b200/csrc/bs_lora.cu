@@ -797,7 +797,7 @@ extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const
                                    static_cast<const uint8_t*>(t.d_base), static_cast<uint8_t*>(t.d_y), static_cast<uint16_t*>(t.d_h),
                                    t.x_stride, t.base_stride, t.y_stride, t.rows, t.cols, t.type, 0};
             }
-            if ((st = launch_few(fp, m, R, gpu.sms, gpu.s)) != BS_OK) return st;
+            if ((st = launch_few(fp, m, R, gpu.dev, gpu.sms, gpu.s)) != BS_OK) return st;
         }
         return BS_OK;
     }

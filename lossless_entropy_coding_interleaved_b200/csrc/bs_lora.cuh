@@ -79,7 +79,7 @@ struct FewParams {
     uint32_t split, pad; // clusters of a tile
     FewJob job[kMaxItems];
 };
-bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s);
+bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int dev, int sms, cudaStream_t s);
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

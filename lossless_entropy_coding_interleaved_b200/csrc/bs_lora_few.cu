@@ -31,19 +31,39 @@ constexpr uint32_t kWarps = kFewThreads / 32, kSlices = kFewCluster * kWarps;
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
+// WORDS words from p, where `on`; what stands in d is undefined where not.
+template <int WORDS>
+__device__ __forceinline__ void load_if(uint32_t* d, const uint16_t* p, uint32_t on) {
+    if constexpr (WORDS == 2)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n @p ld.global.nc.v2.u32 {%0, %1}, [%2];\n}"
+                     : "=r"(d[0]), "=r"(d[1]) : "l"(p), "r"(on));
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "l"(p), "r"(on));
+}
+
 // What a lane has of a block of 128 rows of B: words of its rows g and g + 8 of the warp's 16 (for
-// R = 16, 4 ranks of each; else 8 ranks of each 32), and base of its rows and tokens.
+// R = 16, 4 ranks of each; else 8 ranks of each 32).
 template <int R>
 struct BRows {
     static constexpr int W = R == 16 ? 2 : R / 8; // words of a row
     uint32_t lo[W], hi[W];
-    float base[2][2]; // [row][token]
 };
+
+// B h of a CTA gathers in shared memory, up to 16 blocks of 128 rows at a time, and goes from there to
+// y with base added, token by token in whole lines: from the matrix instructions' registers it would
+// be 4 scattered numbers a lane, most of them of tokens that the tile does not have.
+constexpr uint32_t kHold = 16, kHoldRows = kHold * 128 + 4; // 4: another bank for each token
+template <int R>
+constexpr uint32_t few_smem() { return std::max<uint32_t>(kFew * kHoldRows * 4, kWarps * R * 8 * 4); }
 
 template <int R>
 __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lora_few_kernel(const __grid_constant__ FewParams p) {
     constexpr int MT = R / 16;
-    __shared__ __align__(16) float s_red[kWarps][R * 8], s_part[R * 8], s_h[R * 8]; // [rank][token]
+    extern __shared__ __align__(16) float s_dyn[];
+    __shared__ __align__(16) float s_part[R * 8], s_h[R * 8]; // [rank][token]
+    float(*s_red)[R * 8] = reinterpret_cast<float(*)[R * 8]>(s_dyn); // [warps]
+    float* s_y = s_dyn;                                              // [token][kHoldRows]
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, g = lane >> 2, q = lane & 3u;
     const uint32_t cta = blockIdx.x % kFewCluster, part = blockIdx.x / kFewCluster % p.split, tile = blockIdx.x / kFewCluster / p.split;
     const FewJob& job = p.job[blockIdx.y];
@@ -53,7 +73,6 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const FewTile* entry = reinterpret_cast<const FewTile*>(p.b.plan + o.few) + tile;
     const uint32_t a = entry->bucket, first = entry->first, count = entry->count, tok_g = entry->token[g];
-    const uint32_t tok[2] = {entry->token[2 * q], entry->token[2 * q + 1]}; // ~0 past the count
     if (tile >= p.b.plan[3]) return; // the whole cluster
     if (a >= p.b.n) { // tokens without an adapter: base as it is
         if (!job.out || (job.base == job.out && job.base_stride == job.out_stride)) return;
@@ -129,39 +148,25 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
         const uint32_t k = (steps - 1) * kStep + kLane * q + 2 * i; // not used where there are no steps
         mask[i] = k + 1 < rank ? ~0u : k < rank ? 0xFFFFu : 0u;
     }
-    auto load = [&](uint32_t b) {
-        BRows<R> r;
-        const uint32_t n = b * 128 + warp * 16 + g;
-        const bool in = b < blocks;
+    const uint16_t* rows_g = B + uint64_t(g) * rm + kLane * q;
+    // The warp's 16 rows from n0 on (n0 < N; N is a multiple of 8, so the upper 8 are all there or not,
+    // and stand for nothing where not). A lane whose ranks are all past the adapter's loads nothing:
+    // its mask is 0.
+    auto load = [&](BRows<R>& r, uint32_t n0) {
+        const uint16_t* p0 = rows_g + uint64_t(n0) * rm;
+        const uint16_t* p1 = n0 + 8 < N ? p0 + 8 * rm : p0;
 #pragma unroll
-        for (int m = 0; m < W / WS; ++m)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t(&d)[W] = half ? r.hi : r.lo;
-                const uint16_t* src = B + uint64_t(n + 8 * half) * rm + kStep * m + kLane * q;
-                const bool on = in && n + 8 * half < N && kStep * m + kLane * q < rank;
-                if constexpr (WS == 2) {
-                    const uint2 v = on ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
-                    d[0] = v.x; d[1] = v.y;
-                } else {
-                    const uint4 v = on ? ld16(src) : make_uint4(0, 0, 0, 0);
-                    d[4 * m] = v.x; d[4 * m + 1] = v.y; d[4 * m + 2] = v.z; d[4 * m + 3] = v.w;
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                r.base[half][i] = 0.f;
-                if (in && job.base && tok[i] != ~0u && n + 8 * half < N) {
-                    const uint64_t at = uint64_t(tok[i]) * job.base_stride + n + 8 * half;
-                    r.base[half][i] = job.bf16 ? __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(job.base)[at]) << 16)
-                                               : reinterpret_cast<const float*>(job.base)[at];
-                }
-            }
-        return r;
+        for (int m = 0; m < W / WS; ++m) {
+            if (static_cast<uint32_t>(m) >= steps) break;
+            const uint32_t on = kStep * m + kLane * q < rank;
+            load_if<WS>(&r.lo[WS * m], p0 + kStep * m, on);
+            load_if<WS>(&r.hi[WS * m], p1 + kStep * m, on);
+        }
     };
-    BRows<R> cur = load(b0); // under way while the sums of h are exchanged
+    BRows<R> cur, next;
+    const uint32_t first_row = b0 * 128 + warp * 16, row_deal = deal * 128;
+    const uint32_t rows_end = job.out ? N : 0;
+    if (first_row < rows_end) load(cur, first_row); // under way while the sums of h are exchanged
     cluster.barrier_wait();
     for (uint32_t i = tid; i < R * 8; i += kFewThreads) {
         float peer[kFewCluster], v = 0.f;
@@ -192,40 +197,61 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
 #pragma unroll
         for (int t = 0; t < 3; ++t) hf[w][t] = lo[t] | (hi[t] << 16);
     }
-    for (uint32_t b = b0; b < blocks; b += deal) {
-        const BRows<R> next = load(b + deal);
-        const uint32_t n = b * 128 + warp * 16 + g;
-        float d[4] = {};
+    for (uint32_t hold = first_row - warp * 16; hold < rows_end; hold += kHold * row_deal) { // the same for every warp
+        uint32_t held = 0;
+        for (uint32_t n0 = hold + warp * 16; n0 < rows_end && held < kHold; n0 += row_deal, ++held) {
+            if (n0 + row_deal < rows_end) load(next, n0 + row_deal);
+            float d[4] = {};
 #pragma unroll
-        for (int m = 0; m < W / WS; ++m) {
-            if (static_cast<uint32_t>(m) >= steps) break;
-            const bool last = static_cast<uint32_t>(m) + 1 == steps;
+            for (int m = 0; m < W / WS; ++m) {
+                if (static_cast<uint32_t>(m) >= steps) break;
+                if (static_cast<uint32_t>(m) + 1 == steps) {
 #pragma unroll
-            for (int i = 0; i < WS; i += 2) {
-                const int w = m * WS + i;
-                const uint32_t m0 = last ? mask[i] : ~0u, m1 = last ? mask[i + 1] : ~0u;
-                const uint32_t af[4] = {cur.lo[w] & m0, cur.hi[w] & m0, cur.lo[w + 1] & m1, cur.hi[w + 1] & m1};
+                    for (int i = 0; i < WS; ++i) {
+                        cur.lo[m * WS + i] &= mask[i];
+                        cur.hi[m * WS + i] &= mask[i];
+                    }
+                }
 #pragma unroll
-                for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
+                for (int w = m * WS; w < (m + 1) * WS; w += 2) {
+                    const uint32_t af[4] = {cur.lo[w], cur.hi[w], cur.lo[w + 1], cur.hi[w + 1]};
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
+                }
+            }
+            float* y = s_y + 2 * q * kHoldRows + held * 128 + warp * 16 + g;
+            if (2 * q < count) { y[0] = d[0]; y[8] = d[2]; }
+            if (2 * q + 1 < count) { y[kHoldRows] = d[1]; y[kHoldRows + 8] = d[3]; }
+            cur = next;
+        }
+        __syncthreads();
+        // 4 columns a thread: a block of 128 by a warp
+        const uint32_t left = (rows_end - hold + row_deal - 1) / row_deal, n_held = min(left, kHold);
+        for (uint32_t i = warp; i < n_held * count; i += kWarps) {
+            const uint32_t t = i / n_held, block = i % n_held, n = hold + block * row_deal + 4 * lane;
+            if (n >= N) continue;
+            const uint32_t tok = entry->token[t];
+            const float4 d = *reinterpret_cast<const float4*>(s_y + t * kHoldRows + block * 128 + 4 * lane);
+            const uint64_t from = uint64_t(tok) * job.base_stride + n, to = uint64_t(tok) * job.out_stride + n;
+            if (job.bf16) {
+                uint2 v = make_uint2(0, 0);
+                if (job.base) v = *reinterpret_cast<const uint2*>(job.base + 2 * from);
+                v.x = bf16_of(__uint_as_float(v.x << 16) + d.x) | (bf16_of(__uint_as_float(v.x & 0xFFFF0000u) + d.y) << 16);
+                v.y = bf16_of(__uint_as_float(v.y << 16) + d.z) | (bf16_of(__uint_as_float(v.y & 0xFFFF0000u) + d.w) << 16);
+                *reinterpret_cast<uint2*>(job.out + 2 * to) = v;
+            } else {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (job.base) v = *reinterpret_cast<const float4*>(job.base + 4 * from);
+                *reinterpret_cast<float4*>(job.out + 4 * to) = make_float4(v.x + d.x, v.y + d.y, v.z + d.z, v.w + d.w);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                if (tok[i] != ~0u && n + 8 * half < N) {
-                    const uint64_t at = uint64_t(tok[i]) * job.out_stride + n + 8 * half;
-                    const float v = cur.base[half][i] + d[2 * half + i];
-                    if (job.bf16) reinterpret_cast<uint16_t*>(job.out)[at] = static_cast<uint16_t>(bf16_of(v));
-                    else reinterpret_cast<float*>(job.out)[at] = v;
-                }
-        cur = next;
+        __syncthreads();
     }
     cluster.barrier_wait();
 }
 
 template <int R>
-bs_status launch(FewParams& p, uint32_t jobs, int sms, cudaStream_t s) {
+bs_status launch(FewParams& p, uint32_t jobs, int dev, int sms, cudaStream_t s) {
     // Where few tiles leave SMs idle, several clusters share a tile's rows of B h, and each works out
     // the whole of h, which costs them the same time.
     const uint32_t tiles = tile_cap(p.b.tokens, p.b.n, kFew);
@@ -234,6 +260,7 @@ bs_status launch(FewParams& p, uint32_t jobs, int sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.split * kFewCluster, jobs);
     cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = few_smem<R>();
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -244,7 +271,9 @@ bs_status launch(FewParams& p, uint32_t jobs, int sms, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lora_few_kernel<R>, p);
+    cudaError_t e = allow_smem<lora_few_kernel<R>>(dev, few_smem<R>());
+    if (e != cudaSuccess) return cuda_status(e);
+    e = cudaLaunchKernelEx(&cfg, lora_few_kernel<R>, p);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
@@ -252,12 +281,12 @@ bs_status launch(FewParams& p, uint32_t jobs, int sms, cudaStream_t s) {
 
 } // namespace
 
-bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int sms, cudaStream_t s) {
+bs_status launch_few(FewParams& p, uint32_t jobs, uint32_t R, int dev, int sms, cudaStream_t s) {
     switch (R) {
-    case 16: return launch<16>(p, jobs, sms, s);
-    case 32: return launch<32>(p, jobs, sms, s);
-    case 64: return launch<64>(p, jobs, sms, s);
-    default: return launch<128>(p, jobs, sms, s);
+    case 16: return launch<16>(p, jobs, dev, sms, s);
+    case 32: return launch<32>(p, jobs, dev, sms, s);
+    case 64: return launch<64>(p, jobs, dev, sms, s);
+    default: return launch<128>(p, jobs, dev, sms, s);
     }
 }
 
