@@ -251,19 +251,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _on(index: int, what: str, fn, *args, stream=None):
     """fn(*args, stream) with device `index` current; the stream is that device's current one by default."""
-    def go():
-        if stream is not None:
-            st = _stream(stream)
-        else:
-            st = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-        r = fn(*args, st)
-        if r != OK:
-            _check(r, what)
-    if torch.cuda.current_device() == index:
-        go()
-    else:
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            go()
+            return _on(index, what, fn, *args, stream=stream)
+    if stream is not None:
+        st = _stream(stream)
+    else:
+        st = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    r = fn(*args, st)
+    if r != OK:
+        _check(r, what)
 
 
 def _host_bytes(container) -> np.ndarray:
@@ -776,7 +773,7 @@ class LoraAdapters:
     pools) are written, or added to with accumulate; dxs[k] = dx_bases[k] + the adapters' part,
     where entries of dxs that are the same tensor receive the sum of their parts. dx_bases None: 0.
     xs and dys are bfloat16 [tokens, width], ys and dxs float32 or bfloat16, their bases of the same
-    type; rows may be strided. Beside fw_gemv and fw_gemm the outputs of those are the bases.
+    type; rows may be strided. Arguments of several projections are lists or tuples. Beside fw_gemv and fw_gemm the outputs of those are the bases.
     """
 
     def __init__(self, a, b, scales: torch.Tensor | None = None, ranks: torch.Tensor | None = None):
@@ -799,6 +796,7 @@ class LoraAdapters:
         self._index = a[0].get_device()
         self._fixed = [(x.data_ptr(), y.data_ptr(), y.shape[1], x.shape[2]) for x, y in zip(a, b)]
         self._ranks_at, self._scales_at = (t.data_ptr() if t is not None else None for t in (ranks, scales))
+        self._array = LoraItem * self._n
         self._need = (-1, 0)  # the bytes of a state for the last batch's number of tokens
 
     def state(self, tokens: int) -> list:
@@ -810,10 +808,10 @@ class LoraAdapters:
 
     def _rows(self, t, width, dtype, what, tokens):
         """(address, stride) of a [tokens, width] tensor of contiguous rows."""
-        if t.shape == (tokens, width) and t.dtype is dtype and t.get_device() == self._index:
-            s0, s1 = t.stride()
-            if tokens <= 1:
+        if t.dtype is dtype and t.shape == (tokens, width) and t.get_device() == self._index:
+            if t.is_contiguous() or tokens <= 1:
                 return t.data_ptr(), width
+            s0, s1 = t.stride()
             if s1 == 1:
                 return t.data_ptr(), s0
         raise BsError(E_ARG, "lora", f"{what}: [{tokens}, {width}] of {dtype}, rows contiguous, on the adapters' device")
@@ -822,49 +820,56 @@ class LoraAdapters:
         """(type, base, its stride, output, its stride); no output: zeros."""
         if t is None:
             return 0, 0, 0, 0, 0
-        if t.dtype not in _TYPES:
+        dt = t.dtype
+        if dt not in _TYPES:
             raise BsError(E_ARG, "lora", f"{what}: float32 or bfloat16")
-        at = self._rows(t, width, t.dtype, what, tokens)
-        from_ = at if base is t else (0, 0) if base is None else self._rows(base, width, t.dtype, what + " base", tokens)
-        return (_TYPES[t.dtype], *from_, *at)
+        p, s = self._rows(t, width, dt, what, tokens)
+        if base is t:
+            return _TYPES[dt], p, s, p, s
+        if base is None:
+            return _TYPES[dt], 0, 0, p, s
+        bp, bs = self._rows(base, width, dt, what, tokens)
+        return _TYPES[dt], bp, bs, p, s
 
     def _begin(self, plan, lists, states):
         if plan.n_adapters != self.n or plan._index != self._index:
             raise BsError(E_ARG, "lora", "the plan is of another set of adapters")
-        for v in lists + states:
-            if len(v) != self._n:
+        n = self._n
+        for v in lists:
+            if len(v) != n:
                 raise BsError(E_ARG, "lora", "one entry for each projection")
         if plan.tokens != self._need[0]:
             self._need = (plan.tokens, lib.bs_lora_state_bytes(plan.tokens, self.rank_max))
-        need = self._need[1]
-        for v in states:
-            for t in v:
-                if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != self._index:
-                    raise BsError(E_SIZE, "lora", "a state is of another batch")
-        batch = LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2])
-        return (LoraItem * self._n)(), batch
+        need, index = self._need[1], self._index
+        for t in states:
+            if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != index:
+                raise BsError(E_SIZE, "lora", "a state is of another batch")
+        return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2])
 
     def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
-        xs = list(xs)
-        state = self.state(plan.tokens) if state is None else list(state)
-        ys = [None] * self._n if ys is None else list(ys)
-        bases = ys if bases is None else list(bases)
-        items, batch = self._begin(plan, [xs, ys, bases], [state])
-        T, pack = plan.tokens, _LORA_ITEM.pack_into
+        n, T = self._n, plan.tokens
+        state = self.state(T) if state is None else state
+        ys = [None] * n if ys is None else ys
+        bases = ys if bases is None else bases
+        items, batch = self._begin(plan, (xs, ys, bases, state), state)
+        pack, last = _LORA_ITEM.pack_into, None
         for k, (a, b, rows, cols) in enumerate(self._fixed):
-            ty, base, bs_, y, ys_ = self._out(ys[k], bases[k], rows, "y", T)
-            pack(items, 160 * k, a, b, rows, cols, ty, 0, *self._rows(xs[k], cols, torch.bfloat16, "x", T), state[k].data_ptr(),
-                 base, bs_, y, ys_, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-        _on(self._index, "lora_forward", lib.bs_lora_forward, self._n, items, ctypes.byref(batch), stream=stream)
+            x = xs[k]
+            if x is not last or cols != last_cols:  # q, k and v read one x
+                xp, x_stride = self._rows(x, cols, torch.bfloat16, "x", T)
+                last, last_cols = x, cols
+            ty, bp, b_stride, y, y_stride = self._out(ys[k], bases[k], rows, "y", T)
+            pack(items, 160 * k, a, b, rows, cols, ty, 0, xp, x_stride, state[k].data_ptr(), bp, b_stride, y, y_stride,
+                 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        _on(self._index, "lora_forward", lib.bs_lora_forward, n, items, ctypes.byref(batch), stream=stream)
         return ys
 
     def backward(self, plan: LoraPlan, xs, dys, state, das, dbs, dxs=None, dx_bases=None, work=None, accumulate: bool = False,
                  stream=None):
-        xs, dys, das, dbs, state = list(xs), list(dys), list(das), list(dbs), list(state)
-        work = self.state(plan.tokens) if work is None else list(work)
-        dxs = [None] * self._n if dxs is None else list(dxs)
-        dx_bases = [None] * self._n if dx_bases is None else list(dx_bases)
-        items, batch = self._begin(plan, [xs, dys, das, dbs, dxs, dx_bases], [state, work])
+        work = self.state(plan.tokens) if work is None else work
+        dxs = [None] * self._n if dxs is None else dxs
+        dx_bases = [None] * self._n if dx_bases is None else dx_bases
+        items, batch = self._begin(plan, (xs, dys, das, dbs, dxs, dx_bases, state, work), (*state, *work))
         T, pack, bf = plan.tokens, _LORA_ITEM.pack_into, torch.bfloat16
         for k, (a, b, rows, cols) in enumerate(self._fixed):
             for t, shape in ((das[k], self.a[k].shape), (dbs[k], self.b[k].shape)):

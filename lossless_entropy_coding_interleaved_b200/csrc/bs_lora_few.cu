@@ -7,7 +7,7 @@
 // more than the bytes. So one cluster of 8 CTAs takes up to 8 tokens of one adapter through both
 // products: its 64 warps share the K range of A x, the CTAs exchange their sums of h (rank x 8
 // numbers each) through distributed shared memory, and the warps share the rows of B h. The
-// cluster asks for its part of B (into L2) before it starts on A.
+// first rows of B are on their way to registers during that exchange.
 //
 // Weights are the matrix instructions' 16-row operand and the tokens the 8 columns of the other, so
 // weights go from global memory to registers in the order that they lie in: a sum does not depend on
@@ -89,14 +89,6 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
     const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
     const uint16_t* A = job.a + uint64_t(a) * rm * K;
     const uint16_t* B = job.b + uint64_t(a) * rm * N;
-    // the rows of B h in blocks of 128, dealt out to the CTAs of the tile's clusters, 16 rows a warp
-    const uint32_t blocks = job.out ? (N + 127) / 128 : 0, b0 = part * kFewCluster + cta, deal = p.split * kFewCluster;
-    for (uint32_t b = b0; b < blocks; b += deal) {
-        const uint8_t* run = reinterpret_cast<const uint8_t*>(B + uint64_t(b) * 128 * rm);
-        const uint32_t bytes = min(128u, N - b * 128) * rm * 2;
-        for (uint32_t at = tid * 128; at < bytes; at += kFewThreads * 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(run + at));
-    }
     // ---- A x: the warp's columns, 64 at a time; lane (g, q) has row g (and g + 8) of each 16 ranks,
     // token g, and columns 8 q .. 8 q + 7 of each half of the 64. A warp's chain of sums is K / 1024
     // matrix instructions long.
@@ -163,8 +155,9 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
             load_if<WS>(&r.hi[WS * m], p1 + kStep * m, on);
         }
     };
+    // the rows of B h in blocks of 128, dealt out to the CTAs of the tile's clusters, 16 rows a warp
     BRows<R> cur, next;
-    const uint32_t first_row = b0 * 128 + warp * 16, row_deal = deal * 128;
+    const uint32_t first_row = (part * kFewCluster + cta) * 128 + warp * 16, row_deal = p.split * kFewCluster * 128;
     const uint32_t rows_end = job.out ? N : 0;
     if (first_row < rows_end) load(cur, first_row); // under way while the sums of h are exchanged
     cluster.barrier_wait();
