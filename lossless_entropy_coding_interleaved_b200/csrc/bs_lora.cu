@@ -333,25 +333,33 @@ struct ExpandJob {
 };
 struct ExpandParams {
     Batch b;
-    uint32_t blocks; // blocks of 128 columns a CTA takes
+    uint32_t blocks; // blocks of kExpandCols columns a CTA takes
     uint32_t pad;
     ExpandJob job[kMaxItems];
     ExpandSrc src[kMaxItems];
 };
+constexpr uint32_t kExpandCols = 64;
+constexpr uint32_t kStageRow = 40; // floats between the rows of a warp's 16 x 32 sums: no two of 16 lanes share a bank
 template <int R, bool WT>
-__host__ __device__ constexpr uint32_t expand_w() { return WT ? R * padded<256> : 128 * padded<2 * R>; }
+__host__ __device__ constexpr uint32_t expand_w() { return WT ? R * padded<2 * kExpandCols> : kExpandCols * padded<2 * R>; }
 template <int R, bool WT>
-constexpr uint32_t expand_smem() { return 3 * kTile * padded<2 * R> + 2 * expand_w<R, WT>(); }
+constexpr uint32_t expand_smem() {
+    return 3 * kTile * padded<2 * R> + 2 * expand_w<R, WT>() + (kTiledThreads / 32) * 16 * kStageRow * 4;
+}
 
 // WT: the weights' column index is the contiguous one (A), else the rank index is (B).
-template <int R, bool WT>
+// BF16: base and out are BF16; h then enters as its two upper parts (16 bits), whose loss is 2^-17
+// where the output's own rounding is 2^-9. FP32 outputs take all three (24 bits).
+template <int R, bool WT, bool BF16>
 __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_tok[kTile];
+    constexpr int kParts = BF16 ? 2 : 3;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp & 3u, wn = warp >> 2;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     if (blockIdx.y >= p.b.plan[1]) return;
     const ExpandJob& job = p.job[blockIdx.z];
-    const uint32_t N = job.width, blocks = (N + 127) / 128;
+    const uint32_t N = job.width, blocks = (N + kExpandCols - 1) / kExpandCols;
     const uint32_t nb0 = blockIdx.x * p.blocks, nb1 = min(nb0 + p.blocks, blocks);
     if (nb0 >= nb1) return;
     const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[blockIdx.y];
@@ -361,10 +369,11 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_ke
     const uint32_t rank = none ? 0u : rank_of(p.b, a);
     const uint32_t s0 = smem_u32(smem);
     constexpr uint32_t kPart = kTile * padded<2 * R>, kW0 = 3 * kPart, kWb = expand_w<R, WT>();
+    float* stage = reinterpret_cast<float*>(smem + kW0 + 2 * kWb) + warp * 16 * kStageRow;
     auto load_parts = [&](const ExpandSrc& s) {
         constexpr uint32_t kC = R / 8;
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
+        for (int t = 0; t < kParts; ++t)
             for (uint32_t c = tid; c < kTile * kC; c += kTiledThreads) {
                 const uint32_t r = c / kC, j = 8 * (c % kC);
                 cp_async16(s0 + t * kPart + r * padded<2 * R> + 2 * j,
@@ -373,21 +382,22 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_ke
     };
     auto load_w = [&](const ExpandSrc& s, uint32_t nb, uint32_t buf) {
         const uint16_t* w = s.w + uint64_t(a) * p.b.rank_max * N;
-        const uint32_t sb = s0 + kW0 + buf * kWb;
+        const uint32_t sb = s0 + kW0 + buf * kWb, n0 = nb * kExpandCols;
         if (!WT) {
             constexpr uint32_t kC = R / 8;
 #pragma unroll
-            for (uint32_t c = tid; c < 128 * kC; c += kTiledThreads) {
+            for (uint32_t c = tid; c < kExpandCols * kC; c += kTiledThreads) {
                 const uint32_t n = c / kC, j = 8 * (c % kC);
-                const uint32_t bytes = nb * 128 + n < N && j < rank ? min(rank - j, 8u) * 2u : 0u;
-                cp_async16(sb + n * padded<2 * R> + 2 * j, bytes ? w + uint64_t(nb * 128 + n) * p.b.rank_max + j : s.w, bytes);
+                const uint32_t bytes = n0 + n < N && j < rank ? min(rank - j, 8u) * 2u : 0u;
+                cp_async16(sb + n * padded<2 * R> + 2 * j, bytes ? w + uint64_t(n0 + n) * p.b.rank_max + j : s.w, bytes);
             }
         } else {
+            constexpr uint32_t kC = kExpandCols / 8;
 #pragma unroll
-            for (uint32_t c = tid; c < R * 16; c += kTiledThreads) {
-                const uint32_t j = c >> 4, n = nb * 128 + 8 * (c & 15u);
+            for (uint32_t c = tid; c < R * kC; c += kTiledThreads) {
+                const uint32_t j = c / kC, n = n0 + 8 * (c % kC);
                 const bool on = j < rank && n < N;
-                cp_async16(sb + j * padded<256> + 16 * (c & 15u), on ? w + uint64_t(j) * N + n : s.w, on ? 16u : 0u);
+                cp_async16(sb + j * padded<2 * kExpandCols> + 16 * (c % kC), on ? w + uint64_t(j) * N + n : s.w, on ? 16u : 0u);
             }
         }
     };
@@ -398,13 +408,31 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_ke
         load_w(p.src[job.src], nb0, 0);
         cp_async_commit();
     }
-    uint32_t tok[4]; // this thread's rows: lane / 4 + 8 i of the warp's 32
+    if (tid < kTile) s_tok[tid] = tid < count ? p.b.plan[o.perm + first + tid] : ~0u;
+    __syncthreads();
+    // Output: 4 columns (lane % 8) of rows lane / 8 + 4 i of the warp's 32, so that 8 lanes have 32
+    // columns of a row together. base of a block is loaded while the block before it is worked on.
+    const uint32_t row0 = wm * 32 + (lane >> 3), col0 = wn * 32 + 4 * (lane & 7u);
+    uint4 base[8] = {}; // BF16: .x and .y
+    auto load_base = [&](uint32_t nb) {
+        const uint32_t n = nb * kExpandCols + col0;
+        if (!job.base || n >= N) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = wm * 32 + 8 * i + (lane >> 2);
-        tok[i] = r < count ? p.b.plan[o.perm + first + r] : ~0u;
-    }
-    float acc[2][8][4] = {};
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t tok = s_tok[row0 + 4 * i];
+            if (tok == ~0u) continue;
+            const uint64_t at = uint64_t(tok) * job.base_stride + n;
+            if (BF16) {
+                const uint2 v = *reinterpret_cast<const uint2*>(job.base + 2 * at);
+                base[i].x = v.x;
+                base[i].y = v.y;
+            } else {
+                base[i] = *reinterpret_cast<const uint4*>(job.base + 4 * at);
+            }
+        }
+    };
+    load_base(nb0);
+    float acc[2][4][4] = {};
     uint32_t step = 0;
     for (uint32_t nb = nb0; nb < nb1; ++nb) {
         for (uint32_t s = 0; s < n_src; ++s, ++step) {
@@ -424,61 +452,62 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_ke
 #pragma unroll
             for (uint32_t kk = 0; kk < R / 16; ++kk) {
                 if (kk * 16 >= rank) break;
-                uint32_t bf[4][4];
+                uint32_t bf[2][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint32_t c = wn * 64 + n * 16;
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t c = wn * 32 + n * 16;
                     if (!WT) ldsm4(bf[n], sb + (c + (lane & 7u) + ((lane >> 4) << 3)) * padded<2 * R> + 16 * (2 * kk + ((lane >> 3) & 1u)));
-                    else ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<256> + 2 * (c + 8 * (lane >> 4)));
+                    else ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<2 * kExpandCols> + 2 * (c + 8 * (lane >> 4)));
                 }
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
+                for (int t = 0; t < kParts; ++t)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t af[4];
                         ldsm4(af, s0 + t * kPart + (wm * 32 + m * 16 + (lane & 15u)) * padded<2 * R> + 16 * (2 * kk + (lane >> 4)));
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
+                        for (int n = 0; n < 2; ++n) {
                             mma16816(acc[m][2 * n], af, bf[n][0], bf[n][1]);
                             mma16816(acc[m][2 * n + 1], af, bf[n][2], bf[n][3]);
                         }
                     }
             }
         }
-        const uint32_t c0 = nb * 128 + wn * 64 + 2 * (lane & 3u);
+        const uint32_t n = nb * kExpandCols + col0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (tok[i] == ~0u) continue;
-            const uint64_t bo = uint64_t(tok[i]) * job.base_stride + c0, oo = uint64_t(tok[i]) * job.out_stride + c0;
-            float2 v[8];
+        for (int m = 0; m < 2; ++m) { // 16 rows at a time through shared memory into whole rows
+            __syncwarp();
 #pragma unroll
-            for (int n = 0; n < 8; ++n) v[n] = make_float2(0.f, 0.f);
-            if (job.base) {
+            for (int c = 0; c < 4; ++c) {
+                float* d = stage + (lane >> 2) * kStageRow + 8 * c + 2 * (lane & 3u);
+                *reinterpret_cast<float2*>(d) = make_float2(acc[m][c][0], acc[m][c][1]);
+                *reinterpret_cast<float2*>(d + 8 * kStageRow) = make_float2(acc[m][c][2], acc[m][c][3]);
 #pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    if (c0 + 8 * n < N) {
-                        if (job.bf16) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(job.base + 2 * (bo + 8 * n));
-                            v[n] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-                        } else {
-                            v[n] = *reinterpret_cast<const float2*>(job.base + 4 * (bo + 8 * n));
-                        }
-                    }
+                for (int q = 0; q < 4; ++q) acc[m][c][q] = 0.f;
             }
+            __syncwarp();
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                if (c0 + 8 * n < N) {
-                    const float x = v[n].x + acc[i >> 1][n][2 * (i & 1)], y = v[n].y + acc[i >> 1][n][2 * (i & 1) + 1];
-                    if (job.bf16) *reinterpret_cast<uint32_t*>(job.out + 2 * (oo + 8 * n)) = bf16_of(x) | (bf16_of(y) << 16);
-                    else *reinterpret_cast<float2*>(job.out + 4 * (oo + 8 * n)) = make_float2(x, y);
+            for (int i = 4 * m; i < 4 * m + 4; ++i) {
+                const uint32_t tok = s_tok[row0 + 4 * i];
+                const float4 d = *reinterpret_cast<const float4*>(stage + ((lane >> 3) + 4 * (i & 3)) * kStageRow + 4 * (lane & 7u));
+                if (tok == ~0u || n >= N) continue;
+                const uint64_t at = uint64_t(tok) * job.out_stride + n;
+                const uint4 v = base[i];
+                if (BF16) {
+                    uint2 w;
+                    w.x = bf16x2_of(__uint_as_float(v.x << 16) + d.x, __uint_as_float(v.x & 0xFFFF0000u) + d.y);
+                    w.y = bf16x2_of(__uint_as_float(v.y << 16) + d.z, __uint_as_float(v.y & 0xFFFF0000u) + d.w);
+                    if (none) w = make_uint2(v.x, v.y); // as it is, NaN payloads too
+                    *reinterpret_cast<uint2*>(job.out + 2 * at) = w;
+                } else {
+                    uint4 w = make_uint4(__float_as_uint(__uint_as_float(v.x) + d.x), __float_as_uint(__uint_as_float(v.y) + d.y),
+                                         __float_as_uint(__uint_as_float(v.z) + d.z), __float_as_uint(__uint_as_float(v.w) + d.w));
+                    if (none) w = v;
+                    *reinterpret_cast<uint4*>(job.out + 4 * at) = w;
                 }
+            }
         }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
+        if (nb + 1 < nb1) load_base(nb + 1);
     }
     cp_async_wait<0>();
 }
@@ -698,21 +727,35 @@ bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, const Gpu& g
     default: return launch<lora_shrink_kernel<128, WT>>(grid, shrink_smem<128, WT>(), p.split, gpu, p);
     }
 }
-template <bool WT>
-bs_status launch_expand(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
+template <bool WT, bool BF16>
+bs_status launch_expand_of(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     uint32_t blocks = 1;
-    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
+    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + kExpandCols - 1) / kExpandCols);
     const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
-    // a CTA keeps its tokens' parts for up to 8 blocks, as long as 8 CTAs an SM are left
+    // a CTA keeps its tokens' parts for up to 16 blocks, as long as 6 CTAs an SM are left
     p.blocks = 1;
-    while (p.blocks < 8 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 8ull * gpu.sms) p.blocks *= 2;
+    while (p.blocks < 16 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 6ull * gpu.sms) p.blocks *= 2;
     const dim3 grid((blocks + p.blocks - 1) / p.blocks, cap, jobs);
     switch (R) {
-    case 16: return launch<lora_expand_kernel<16, WT>>(grid, expand_smem<16, WT>(), 1, gpu, p);
-    case 32: return launch<lora_expand_kernel<32, WT>>(grid, expand_smem<32, WT>(), 1, gpu, p);
-    case 64: return launch<lora_expand_kernel<64, WT>>(grid, expand_smem<64, WT>(), 1, gpu, p);
-    default: return launch<lora_expand_kernel<128, WT>>(grid, expand_smem<128, WT>(), 1, gpu, p);
+    case 16: return launch<lora_expand_kernel<16, WT, BF16>>(grid, expand_smem<16, WT>(), 1, gpu, p);
+    case 32: return launch<lora_expand_kernel<32, WT, BF16>>(grid, expand_smem<32, WT>(), 1, gpu, p);
+    case 64: return launch<lora_expand_kernel<64, WT, BF16>>(grid, expand_smem<64, WT>(), 1, gpu, p);
+    default: return launch<lora_expand_kernel<128, WT, BF16>>(grid, expand_smem<128, WT>(), 1, gpu, p);
     }
+}
+// The jobs of a call may be of both types: those of each go together.
+template <bool WT>
+bs_status launch_expand(const ExpandParams& all, uint32_t jobs, uint32_t R, const Gpu& gpu) {
+    ExpandParams p = all;
+    for (uint32_t type : {BS_TYPE_F32, BS_TYPE_BF16}) {
+        uint32_t n = 0;
+        for (uint32_t k = 0; k < jobs; ++k)
+            if (all.job[k].bf16 == type) p.job[n++] = all.job[k];
+        if (n == 0) continue;
+        const bs_status st = type == BS_TYPE_BF16 ? launch_expand_of<WT, true>(p, n, R, gpu) : launch_expand_of<WT, false>(p, n, R, gpu);
+        if (st != BS_OK) return st;
+    }
+    return BS_OK;
 }
 bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     uint32_t blocks = 1;

@@ -99,6 +99,11 @@ __device__ __forceinline__ uint32_t bf16_of(float f) { // to nearest, ties to ev
     asm("{\n .reg .b16 h;\n cvt.rn.bf16.f32 h, %1;\n mov.b32 %0, {h, 0};\n}" : "=r"(r) : "f"(f));
     return r;
 }
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // The three BF16 numbers whose sum is f: each takes 8 bits of what the ones before it left, 24 in
 // all, so a rank-wide FP32 intermediate goes through the BF16 tensor cores without loss. What an
 // infinity or NaN leaves is taken as 0, not as the NaN of inf - inf.
