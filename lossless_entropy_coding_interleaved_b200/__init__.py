@@ -97,7 +97,7 @@ class LoraBatch(ctypes.Structure):
     """bs_lora_batch: the batch that the items of one call share."""
     _fields_ = [("tokens", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32), ("rank_max", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("d_ranks", ctypes.c_void_p), ("d_scales", ctypes.c_void_p),
-                ("d_plan", ctypes.c_void_p)]
+                ("d_plan", ctypes.c_void_p), ("d_err", ctypes.c_void_p)]
 
 
 class AdamWItem(ctypes.Structure):
@@ -737,7 +737,9 @@ assert _LORA_ITEM.size == ctypes.sizeof(LoraItem) == 160
 class LoraPlan:
     """The routing of a batch of ``tokens`` tokens to ``n_adapters`` adapters (bs_lora_plan), in
     device memory. update(idx) sets it from an int32 CUDA tensor, an adapter per token (negative:
-    none); one plan serves every projection of the batch, and may be updated for the next batch."""
+    none); one plan serves every projection of the batch, and may be updated for the next batch.
+    ``err``, an int32 device word, gathers what the calls that use the plan report: bit 2 an index past
+    the adapters, bit 1 a wait inside a kernel that ran out (0 in a working program)."""
 
     def __init__(self, tokens: int, n_adapters: int, device="cuda"):
         if not torch.cuda.is_available():
@@ -844,7 +846,7 @@ class LoraAdapters:
         for t in states:
             if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != index:
                 raise BsError(E_SIZE, "lora", "a state is of another batch")
-        return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2])
+        return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2], plan._args[4])
 
     def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
         n, T = self._n, plan.tokens

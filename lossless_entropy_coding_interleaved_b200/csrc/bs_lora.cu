@@ -26,6 +26,7 @@
 #include <cstring>
 
 #include "bs_lora.cuh"
+#include "bs_lora_tc.cuh"
 
 namespace bs {
 namespace {
@@ -333,183 +334,276 @@ struct ExpandJob {
 };
 struct ExpandParams {
     Batch b;
-    uint32_t blocks; // blocks of kExpandCols columns a CTA takes
-    uint32_t pad;
+    uint32_t n_jobs, pad;
     ExpandJob job[kMaxItems];
     ExpandSrc src[kMaxItems];
 };
-constexpr uint32_t kExpandCols = 64;
-constexpr uint32_t kStageRow = 40; // floats between the rows of a warp's 16 x 32 sums: no two of 16 lanes share a bank
-template <int R, bool WT>
-__host__ __device__ constexpr uint32_t expand_w() { return WT ? R * padded<2 * kExpandCols> : kExpandCols * padded<2 * R>; }
-template <int R, bool WT>
+constexpr uint32_t kExpandOut = 256, kExpandLoad = 128; // threads that write and that load; a warp more issues
+constexpr uint32_t kExpandThreads = kExpandOut + kExpandLoad + 32;
+constexpr uint32_t kRowBytes = 256, kRowPitch = kRowBytes + 16; // of a block's rows of base, which become those of out
+template <bool BF16>
+constexpr uint32_t expand_cols = kRowBytes / (BF16 ? 2 : 4); // columns of a block
+template <int R>
+constexpr uint32_t atoms_of = R > 64 ? 2 : 1; // 64 ranks each
+// Shared memory: h's parts (tokens x ranks, K-major), two buffers of weights, two of base.
+template <int R, bool BF16>
+__host__ __device__ constexpr uint32_t expand_w() { return expand_cols<BF16> * 128 * atoms_of<R>; }
+template <int R, bool BF16>
 constexpr uint32_t expand_smem() {
-    return 3 * kTile * padded<2 * R> + 2 * expand_w<R, WT>() + (kTiledThreads / 32) * 16 * kStageRow * 4;
+    return 1024 + (BF16 ? 2 : 3) * 16384 * atoms_of<R> + 2 * expand_w<R, BF16>() + 2 * kTile * kRowPitch;
 }
 
+// A place in the sequence of (job, tile, block) that the CTAs share out.
+struct ExpandAt {
+    uint32_t job, tile, block;
+};
+
+// One wave of CTAs shares the blocks (128 tokens of a tile x 256 bytes of their rows) of all jobs
+// evenly, in the order job, tile, block, so that a CTA keeps a tile's h for its run of blocks. base's
+// rows come by bulk copies into shared memory, the matrix instructions' sums (128 tokens x the
+// block's columns, in tensor memory) are added there, and the rows leave by bulk copies: the threads
+// between them handle 16 bytes at a time and no addresses. (With loads and stores from the threads
+// themselves, 8192 tokens x 14336 columns took 209 us by mma.sync and 243 us by tcgen05: 20 to 33
+// instructions for each 32 numbers.)
 // WT: the weights' column index is the contiguous one (A), else the rank index is (B).
 // BF16: base and out are BF16; h then enters as its two upper parts (16 bits), whose loss is 2^-17
 // where the output's own rounding is 2^-9. FP32 outputs take all three (24 bits).
 template <int R, bool WT, bool BF16>
-__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t s_tok[kTile];
-    constexpr int kParts = BF16 ? 2 : 3;
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp & 3u, wn = warp >> 2;
+__global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_bar[10];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
+    constexpr uint32_t kTmem = 2 * kCols;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    if (blockIdx.y >= p.b.plan[1]) return;
-    const ExpandJob& job = p.job[blockIdx.z];
-    const uint32_t N = job.width, blocks = (N + kExpandCols - 1) / kExpandCols;
-    const uint32_t nb0 = blockIdx.x * p.blocks, nb1 = min(nb0 + p.blocks, blocks);
-    if (nb0 >= nb1) return;
-    const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[blockIdx.y];
-    const uint32_t a = tl.x, first = tl.y, count = tl.z;
-    const bool none = a >= p.b.n; // tokens without an adapter: base as it is
-    if (none && job.base == job.out && job.base_stride == job.out_stride) return;
-    const uint32_t rank = none ? 0u : rank_of(p.b, a);
-    const uint32_t s0 = smem_u32(smem);
-    constexpr uint32_t kPart = kTile * padded<2 * R>, kW0 = 3 * kPart, kWb = expand_w<R, WT>();
-    float* stage = reinterpret_cast<float*>(smem + kW0 + 2 * kWb) + warp * 16 * kStageRow;
-    auto load_parts = [&](const ExpandSrc& s) {
-        constexpr uint32_t kC = R / 8;
-#pragma unroll
-        for (int t = 0; t < kParts; ++t)
-            for (uint32_t c = tid; c < kTile * kC; c += kTiledThreads) {
-                const uint32_t r = c / kC, j = 8 * (c % kC);
-                cp_async16(s0 + t * kPart + r * padded<2 * R> + 2 * j,
-                           s.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < count ? first + r : first) * R + j, r < count ? 16u : 0u);
-            }
-    };
-    auto load_w = [&](const ExpandSrc& s, uint32_t nb, uint32_t buf) {
-        const uint16_t* w = s.w + uint64_t(a) * p.b.rank_max * N;
-        const uint32_t sb = s0 + kW0 + buf * kWb, n0 = nb * kExpandCols;
-        if (!WT) {
-            constexpr uint32_t kC = R / 8;
-#pragma unroll
-            for (uint32_t c = tid; c < kExpandCols * kC; c += kTiledThreads) {
-                const uint32_t n = c / kC, j = 8 * (c % kC);
-                const uint32_t bytes = n0 + n < N && j < rank ? min(rank - j, 8u) * 2u : 0u;
-                cp_async16(sb + n * padded<2 * R> + 2 * j, bytes ? w + uint64_t(n0 + n) * p.b.rank_max + j : s.w, bytes);
-            }
-        } else {
-            constexpr uint32_t kC = kExpandCols / 8;
-#pragma unroll
-            for (uint32_t c = tid; c < R * kC; c += kTiledThreads) {
-                const uint32_t j = c / kC, n = n0 + 8 * (c % kC);
-                const bool on = j < rank && n < N;
-                cp_async16(sb + j * padded<2 * kExpandCols> + 16 * (c % kC), on ? w + uint64_t(j) * N + n : s.w, on ? 16u : 0u);
-            }
-        }
-    };
-    // the steps: every block's sources, one after the other; step i's weights in buffer i % 2
-    const uint32_t n_src = none ? 0u : job.n_src, n_steps = (nb1 - nb0) * n_src;
-    if (n_steps) {
-        load_parts(p.src[job.src]);
-        load_w(p.src[job.src], nb0, 0);
-        cp_async_commit();
+    const uint32_t tiles = p.b.plan[1];
+    const uint4* tile_of = reinterpret_cast<const uint4*>(p.b.plan + o.tiles);
+    auto blocks_of = [&](uint32_t job) { return (p.job[job].width + kCols - 1) / kCols; };
+    uint64_t total = 0;
+    for (uint32_t k = 0; k < p.n_jobs; ++k) total += uint64_t(tiles) * blocks_of(k);
+    const uint64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (u0 == u1) return;
+    const uint32_t n_units = static_cast<uint32_t>(u1 - u0);
+    ExpandAt start{0, 0, 0};
+    {
+        uint64_t u = u0;
+        while (u >= uint64_t(tiles) * blocks_of(start.job)) u -= uint64_t(tiles) * blocks_of(start.job++);
+        start.tile = static_cast<uint32_t>(u / blocks_of(start.job));
+        start.block = static_cast<uint32_t>(u % blocks_of(start.job));
     }
-    if (tid < kTile) s_tok[tid] = tid < count ? p.b.plan[o.perm + first + tid] : ~0u;
-    __syncthreads();
-    // Output: 4 columns (lane % 8) of rows lane / 8 + 4 i of the warp's 32, so that 8 lanes have 32
-    // columns of a row together. base of a block is loaded while the block before it is worked on.
-    const uint32_t row0 = wm * 32 + (lane >> 3), col0 = wn * 32 + 4 * (lane & 7u);
-    uint4 base[8] = {}; // BF16: .x and .y
-    auto load_base = [&](uint32_t nb) {
-        const uint32_t n = nb * kExpandCols + col0;
-        if (!job.base || n >= N) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t tok = s_tok[row0 + 4 * i];
-            if (tok == ~0u) continue;
-            const uint64_t at = uint64_t(tok) * job.base_stride + n;
-            if (BF16) {
-                const uint2 v = *reinterpret_cast<const uint2*>(job.base + 2 * at);
-                base[i].x = v.x;
-                base[i].y = v.y;
-            } else {
-                base[i] = *reinterpret_cast<const uint4*>(job.base + 4 * at);
-            }
+    // steps to the next unit; true where the tile (or job) is another one
+    auto next = [&](ExpandAt& at) {
+        if (++at.block < blocks_of(at.job)) return false;
+        at.block = 0;
+        if (++at.tile == tiles) {
+            at.tile = 0;
+            ++at.job;
         }
+        return true;
     };
-    load_base(nb0);
-    float acc[2][4][4] = {};
-    uint32_t step = 0;
-    for (uint32_t nb = nb0; nb < nb1; ++nb) {
-        for (uint32_t s = 0; s < n_src; ++s, ++step) {
-            if (n_src > 1 && step > 0) { // another source's parts take the place of the last one's
-                __syncthreads();
-                load_parts(p.src[job.src + s]);
+    const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sH = s0, sW = sH + kParts * kPart, sRow = sW + 2 * expand_w<R, BF16>();
+    uint8_t* const rows = smem_raw + (sRow - smem_u32(smem_raw));
+    // barriers, two each: full (weights, and parts before them, have landed), empty (the matrix
+    // instructions that read them are done), d (a block's sums are complete), base (its base has
+    // landed), free (its sums and its rows' buffer have been read out)
+    const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 16, bar_d = bar_full + 32, bar_base = bar_full + 48, bar_free = bar_full + 64;
+    if (tid == 0) {
+        s_abort = 0;
+        for (uint32_t i = 0; i < 2; ++i) {
+            bar_init(bar_full + 8 * i, kExpandLoad);
+            bar_init(bar_empty + 8 * i, 1);
+            bar_init(bar_d + 8 * i, 1);
+            bar_init(bar_base + 8 * i, kExpandLoad);
+            bar_init(bar_free + 8 * i, kExpandOut);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    constexpr uint32_t kIssueWarp = (kExpandOut + kExpandLoad) / 32;
+    if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort_flag = &s_abort;
+    // What a role needs of a tile: its adapter's rank (0: base as it is), and whether nothing at all is
+    // to be done for it. Units left out take no turn of the buffers: every role counts the same ones.
+    auto rank_at = [&](const uint4& tl) { return tl.x < p.b.n ? rank_of(p.b, tl.x) : 0u; };
+    auto left_out = [&](const ExpandJob& j, uint32_t rank) { return rank == 0 && j.base == j.out && j.base_stride == j.out_stride; };
+
+    if (warp >= kExpandOut / 32 && warp < kIssueWarp) {
+        const uint32_t t0 = tid - kExpandOut; // this thread copies the block's row t0
+        constexpr uint32_t kC = R / 8;
+        uint4 tl = make_uint4(0, 0, 0, 0);
+        uint32_t rank = 0, turn = 0, step = 0; // turns of the base buffers, of the weights' buffers
+        uint64_t tok = 0;
+        bool fresh = true, parts_in = false; // another tile; its parts are in place (with one source)
+        ExpandAt at = start;
+        for (uint32_t u = 0; u < n_units; ++u) {
+            const ExpandJob& job = p.job[at.job];
+            if (fresh) {
+                tl = tile_of[at.tile];
+                rank = rank_at(tl);
+                tok = t0 < tl.z ? p.b.plan[o.perm + tl.y + t0] : 0;
+                parts_in = false;
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
-            if (step + 1 < n_steps) {
-                const uint32_t s2 = s + 1 < n_src ? s + 1 : 0;
-                load_w(p.src[job.src + s2], s2 ? nb : nb + 1, (step + 1) & 1u);
-            }
-            cp_async_commit();
-            const uint32_t sb = s0 + kW0 + (step & 1u) * kWb;
+            const uint32_t nb = at.block, n0 = nb * kCols, a = tl.x, count = tl.z;
+            if (!left_out(job, rank)) {
+                const uint32_t buf = turn & 1u;
+                if (turn >= 2 && !bar_wait(bar_free + 8 * buf, (turn / 2 - 1) & 1u, abort_flag)) break;
+                const uint32_t bytes = t0 < count && job.base ? min(kCols, job.width - n0) * es : 0u;
+                asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}"
+                             ::"r"(bar_base + 8 * buf), "r"(bytes) : "memory");
+                if (bytes)
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                 ::"r"(sRow + buf * kTile * kRowPitch + t0 * kRowPitch), "l"(job.base + (tok * job.base_stride + n0) * es),
+                                   "r"(bytes), "r"(bar_base + 8 * buf) : "memory");
+                ++turn;
+                for (uint32_t si = 0; si < (rank ? job.n_src : 0u); ++si, ++step) {
+                    const ExpandSrc& src = p.src[job.src + si];
+                    const uint32_t wb = step & 1u;
+                    if (step >= 2 && !bar_wait(bar_empty + 8 * wb, (step / 2 - 1) & 1u, abort_flag)) break;
+                    if (!parts_in) { // once what stood there has been read
+                        if (step > 0 && !bar_wait(bar_empty + 8 * (wb ^ 1u), ((step - 1) / 2) & 1u, abort_flag)) break;
 #pragma unroll
-            for (uint32_t kk = 0; kk < R / 16; ++kk) {
-                if (kk * 16 >= rank) break;
-                uint32_t bf[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint32_t c = wn * 32 + n * 16;
-                    if (!WT) ldsm4(bf[n], sb + (c + (lane & 7u) + ((lane >> 4) << 3)) * padded<2 * R> + 16 * (2 * kk + ((lane >> 3) & 1u)));
-                    else ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<2 * kExpandCols> + 2 * (c + 8 * (lane >> 4)));
-                }
-#pragma unroll
-                for (int t = 0; t < kParts; ++t)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t af[4];
-                        ldsm4(af, s0 + t * kPart + (wm * 32 + m * 16 + (lane & 15u)) * padded<2 * R> + 16 * (2 * kk + (lane >> 4)));
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            mma16816(acc[m][2 * n], af, bf[n][0], bf[n][1]);
-                            mma16816(acc[m][2 * n + 1], af, bf[n][2], bf[n][3]);
+                        for (uint32_t t = 0; t < kParts; ++t)
+                            for (uint32_t c = t0; c < count * kC; c += kExpandLoad) {
+                                const uint32_t r = c / kC, j = c % kC;
+                                cp_async16(sH + t * kPart + (j >> 3) * 16384 + sw128(r, j & 7u),
+                                           src.parts + uint64_t(t) * p.b.part_stride + uint64_t(tl.y + r) * R + 8 * j, 16u);
+                            }
+                        parts_in = job.n_src == 1;
+                    }
+                    const uint16_t* w = src.w + uint64_t(a) * p.b.rank_max * job.width;
+                    const uint32_t sb = sW + wb * expand_w<R, BF16>(), N = job.width;
+                    if (!WT) {
+#pragma unroll 4
+                        for (uint32_t c = t0; c < kCols * kC; c += kExpandLoad) {
+                            const uint32_t n = c / kC, j = c % kC;
+                            const uint32_t take = n0 + n < N && 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
+                            cp_async16(sb + (j >> 3) * (kCols * 128) + sw128(n, j & 7u), take ? w + uint64_t(n0 + n) * p.b.rank_max + 8 * j : src.w, take);
+                        }
+                    } else {
+                        constexpr uint32_t kRow = kCols / 8; // pieces of a rank's columns
+#pragma unroll 4
+                        for (uint32_t c = t0; c < R * kRow; c += kExpandLoad) {
+                            const uint32_t j = c / kRow, q = c % kRow, n = n0 + 8 * q;
+                            const bool on = j < rank && n < N;
+                            cp_async16(sb + (q >> 3) * (R * 128) + sw128(j, q & 7u), on ? w + uint64_t(j) * N + n : src.w, on ? 16u : 0u);
                         }
                     }
-            }
-        }
-        const uint32_t n = nb * kExpandCols + col0;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) { // 16 rows at a time through shared memory into whole rows
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float* d = stage + (lane >> 2) * kStageRow + 8 * c + 2 * (lane & 3u);
-                *reinterpret_cast<float2*>(d) = make_float2(acc[m][c][0], acc[m][c][1]);
-                *reinterpret_cast<float2*>(d + 8 * kStageRow) = make_float2(acc[m][c][2], acc[m][c][3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[m][c][q] = 0.f;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 4 * m; i < 4 * m + 4; ++i) {
-                const uint32_t tok = s_tok[row0 + 4 * i];
-                const float4 d = *reinterpret_cast<const float4*>(stage + ((lane >> 3) + 4 * (i & 3)) * kStageRow + 4 * (lane & 7u));
-                if (tok == ~0u || n >= N) continue;
-                const uint64_t at = uint64_t(tok) * job.out_stride + n;
-                const uint4 v = base[i];
-                if (BF16) {
-                    uint2 w;
-                    w.x = bf16x2_of(__uint_as_float(v.x << 16) + d.x, __uint_as_float(v.x & 0xFFFF0000u) + d.y);
-                    w.y = bf16x2_of(__uint_as_float(v.y << 16) + d.z, __uint_as_float(v.y & 0xFFFF0000u) + d.w);
-                    if (none) w = make_uint2(v.x, v.y); // as it is, NaN payloads too
-                    *reinterpret_cast<uint2*>(job.out + 2 * at) = w;
-                } else {
-                    uint4 w = make_uint4(__float_as_uint(__uint_as_float(v.x) + d.x), __float_as_uint(__uint_as_float(v.y) + d.y),
-                                         __float_as_uint(__uint_as_float(v.z) + d.z), __float_as_uint(__uint_as_float(v.w) + d.w));
-                    if (none) w = v;
-                    *reinterpret_cast<uint4*>(job.out + 4 * at) = w;
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_operands();
+                    bar_arrive(bar_full + 8 * wb);
                 }
             }
+            fresh = next(at);
         }
-        if (nb + 1 < nb1) load_base(nb + 1);
+        cp_async_wait<0>();
+        if (*abort_flag) { // given up: the copies that are under way must land before the CTA ends
+            volatile int own = 0;
+            for (uint32_t k = turn >= 2 ? turn - 2 : 0; k < turn; ++k) bar_wait(bar_base + 8 * (k & 1u), (k / 2) & 1u, &own);
+        }
+    } else if (tid == kIssueWarp * 32) {
+        const uint32_t idesc = idesc_of(kCols, false, WT);
+        uint32_t rank = 0, turn = 0, step = 0;
+        bool fresh = true;
+        ExpandAt at = start;
+        for (uint32_t u = 0; u < n_units; ++u) {
+            const ExpandJob& job = p.job[at.job];
+            if (fresh) rank = rank_at(tile_of[at.tile]);
+            if (!left_out(job, rank)) {
+                const uint32_t db = turn & 1u, kn = (rank + 15) / 16;
+                if (turn >= 2 && !bar_wait(bar_free + 8 * db, (turn / 2 - 1) & 1u, abort_flag)) break;
+                for (uint32_t si = 0; si < (rank ? job.n_src : 0u); ++si, ++step) {
+                    const uint32_t wb = step & 1u, w = sW + wb * expand_w<R, BF16>();
+                    if (!bar_wait(bar_full + 8 * wb, (step / 2) & 1u, abort_flag)) break;
+                    fence_after();
+                    for (uint32_t kk = 0; kk < kn; ++kk) {
+                        const uint64_t bd = WT ? mn_major(w + kk * 2048, R * 128) : k_major(w + (kk >> 2) * (kCols * 128) + (kk & 3u) * 32);
+#pragma unroll
+                        for (int t = kParts - 1; t >= 0; --t) // small parts first
+                            mma_tc(tmem + db * kCols, k_major(sH + t * kPart + (kk >> 2) * 16384 + (kk & 3u) * 32), bd, idesc,
+                                   !(si == 0 && kk == 0 && t == static_cast<int>(kParts) - 1));
+                    }
+                    commit_tc(bar_empty + 8 * wb);
+                }
+                if (rank) commit_tc(bar_d + 8 * db);
+                else bar_arrive(bar_d + 8 * db);
+                ++turn;
+            }
+            fresh = next(at);
+        }
+    } else if (warp < kExpandOut / 32) {
+        // warps w and w + 4: tokens 32 (w % 4) .. of the tile, a token each lane; w the first half of a
+        // block's row, w + 4 the second
+        const uint32_t r = (warp & 3u) * 32 + lane, half = warp >> 2;
+        constexpr uint32_t kHalf = kCols / 2;
+        uint4 tl = make_uint4(0, 0, 0, 0);
+        uint32_t rank = 0, turn = 0;
+        uint64_t tok = 0;
+        bool fresh = true;
+        ExpandAt at = start;
+        for (uint32_t u = 0; u < n_units; ++u) {
+            const ExpandJob& job = p.job[at.job];
+            if (fresh) {
+                tl = tile_of[at.tile];
+                rank = rank_at(tl);
+                tok = r < tl.z ? p.b.plan[o.perm + tl.y + r] : 0;
+            }
+            if (!left_out(job, rank)) {
+                const uint32_t buf = turn & 1u, n0 = at.block * kCols + half * kHalf;
+                uint8_t* row = rows + buf * kTile * kRowPitch + r * kRowPitch + half * (kRowBytes / 2);
+                if (!bar_wait(bar_base + 8 * buf, (turn / 2) & 1u, abort_flag)) break;
+                if (!bar_wait(bar_d + 8 * buf, (turn / 2) & 1u, abort_flag)) break;
+                fence_after();
+                if (rank || !job.base)
+#pragma unroll
+                    for (uint32_t c = 0; c < kHalf; c += 16) {
+                        uint32_t d[16] = {};
+                        if (rank) tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + buf * kCols + half * kHalf + c);
+                        uint4* at16 = reinterpret_cast<uint4*>(row + c * es);
+#pragma unroll
+                        for (uint32_t q = 0; q < es; ++q) { // 16 bytes: 8 BF16 or 4 FP32
+                            uint4 v = job.base ? at16[q] : make_uint4(0, 0, 0, 0);
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (uint32_t i = 0; i < 4; ++i) {
+                                if (BF16)
+                                    w[i] = bf16x2_of(__uint_as_float(w[i] << 16) + __uint_as_float(d[8 * (q & 1u) + 2 * i]),
+                                                     __uint_as_float(w[i] & 0xFFFF0000u) + __uint_as_float(d[8 * (q & 1u) + 2 * i + 1]));
+                                else
+                                    w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(d[4 * q + i]));
+                            }
+                            at16[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                fence_before();
+                fence_operands(); // read by the copy below
+                if (r < tl.z && n0 < job.width) {
+                    const uint32_t bytes = min(kHalf, job.width - n0) * es;
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                                 ::"l"(job.out + (tok * job.out_stride + n0) * es), "r"(smem_u32(row)), "r"(bytes) : "memory");
+                }
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                bar_arrive(bar_free + 8 * buf);
+                ++turn;
+            }
+            fresh = next(at);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
-    cp_async_wait<0>();
+    fence_before();
+    __syncthreads();
+    if (tid == 0 && s_abort && p.b.err) atomicOr(p.b.err, 2u);
+    if (warp == kIssueWarp) {
+        __syncwarp();
+        tmem_free(tmem, kTmem);
+    }
 }
 
 // ---------------------------------------------------------------- outer
@@ -652,7 +746,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bs_status check_batch(const bs_lora_batch* b) {
     if (!b || b->tokens > kMaxTokens || b->n_adapters < 1 || b->n_adapters > kMaxAdapters || b->reserved) return BS_E_ARG;
     if (b->rank_max < 8 || b->rank_max > kMaxRank || b->rank_max % 8) return BS_E_ARG;
-    if (!b->d_plan || !aligned(b->d_plan, 16) || !aligned(b->d_ranks, 4) || !aligned(b->d_scales, 4)) return BS_E_ARG;
+    if (!b->d_plan || !aligned(b->d_plan, 16) || !aligned(b->d_ranks, 4) || !aligned(b->d_scales, 4) || !aligned(b->d_err, 4)) return BS_E_ARG;
     return BS_OK;
 }
 bs_status check_item(const bs_lora_item& t) {
@@ -676,19 +770,20 @@ Batch batch_of(const bs_lora_batch& b) {
     o.plan = static_cast<const uint32_t*>(b.d_plan);
     o.ranks = b.d_ranks;
     o.scales = b.d_scales;
+    o.err = b.d_err;
     return o;
 }
 struct Gpu {
     int dev = 0, sms = 148;
     cudaStream_t s = nullptr;
 };
-template <auto FN, typename Params>
+template <auto FN, uint32_t THREADS = kTiledThreads, typename Params>
 bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, const Params& p) {
     cudaError_t e = allow_smem<FN>(gpu.dev, smem);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kTiledThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = gpu.s;
     cudaLaunchAttribute attr[1];
@@ -729,18 +824,16 @@ bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, const Gpu& g
 }
 template <bool WT, bool BF16>
 bs_status launch_expand_of(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
-    uint32_t blocks = 1;
-    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + kExpandCols - 1) / kExpandCols);
-    const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
-    // a CTA keeps its tokens' parts for up to 16 blocks, as long as 6 CTAs an SM are left
-    p.blocks = 1;
-    while (p.blocks < 16 && uint64_t((p.b.tokens + kTile - 1) / kTile) * jobs * (blocks / (2 * p.blocks)) >= 6ull * gpu.sms) p.blocks *= 2;
-    const dim3 grid((blocks + p.blocks - 1) / p.blocks, cap, jobs);
+    p.n_jobs = jobs;
+    uint64_t units = 0; // at most: the plan, on the device, knows the tiles
+    for (uint32_t k = 0; k < jobs; ++k)
+        units += uint64_t(tile_cap(p.b.tokens, p.b.n, kTile)) * ((p.job[k].width + expand_cols<BF16> - 1) / expand_cols<BF16>);
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(units, gpu.sms)));
     switch (R) {
-    case 16: return launch<lora_expand_kernel<16, WT, BF16>>(grid, expand_smem<16, WT>(), 1, gpu, p);
-    case 32: return launch<lora_expand_kernel<32, WT, BF16>>(grid, expand_smem<32, WT>(), 1, gpu, p);
-    case 64: return launch<lora_expand_kernel<64, WT, BF16>>(grid, expand_smem<64, WT>(), 1, gpu, p);
-    default: return launch<lora_expand_kernel<128, WT, BF16>>(grid, expand_smem<128, WT>(), 1, gpu, p);
+    case 16: return launch<lora_expand_kernel<16, WT, BF16>, kExpandThreads>(grid, expand_smem<16, BF16>(), 1, gpu, p);
+    case 32: return launch<lora_expand_kernel<32, WT, BF16>, kExpandThreads>(grid, expand_smem<32, BF16>(), 1, gpu, p);
+    case 64: return launch<lora_expand_kernel<64, WT, BF16>, kExpandThreads>(grid, expand_smem<64, BF16>(), 1, gpu, p);
+    default: return launch<lora_expand_kernel<128, WT, BF16>, kExpandThreads>(grid, expand_smem<128, BF16>(), 1, gpu, p);
     }
 }
 // The jobs of a call may be of both types: those of each go together.

@@ -56,6 +56,7 @@ struct Batch {
     const uint32_t* plan;
     const int32_t* ranks;  // nullptr: every adapter has rank_max
     const float* scales;   // nullptr: 1
+    uint32_t* err;         // nullptr, or a word whose bit 1 says that a wait inside a kernel ran out
 };
 __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
     if (!b.ranks) return b.rank_max;
