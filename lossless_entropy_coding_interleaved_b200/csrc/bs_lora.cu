@@ -338,19 +338,25 @@ struct ExpandParams {
     ExpandJob job[kMaxItems];
     ExpandSrc src[kMaxItems];
 };
-constexpr uint32_t kExpandOut = 256, kExpandLoad = 128; // threads that write and that load; a warp more issues
-constexpr uint32_t kExpandThreads = kExpandOut + kExpandLoad + 32;
+// threads that write and that load; a warp more issues
+constexpr uint32_t kExpandOut = 256, kExpandLoad = 128, kExpandThreads = kExpandOut + kExpandLoad + 32;
 constexpr uint32_t kRowBytes = 256, kRowPitch = kRowBytes + 16; // of a block's rows of base, which become those of out
 template <bool BF16>
 constexpr uint32_t expand_cols = kRowBytes / (BF16 ? 2 : 4); // columns of a block
 template <int R>
 constexpr uint32_t atoms_of = R > 64 ? 2 : 1; // 64 ranks each
-// Shared memory: h's parts (tokens x ranks, K-major), two buffers of weights, two of base.
+// Buffers of base and of sums: as many as fit beside the operands, of which rank 128 has twice the bytes.
+template <int R>
+constexpr uint32_t expand_bufs = R > 64 ? 2 : 4;
+// Sources that stand beside each other in an operand's 64 (or 128) ranks.
+template <int R>
+constexpr uint32_t group_of = R >= 64 ? 1 : 64 / R;
+// Shared memory: h's parts (tokens x ranks, K-major), two buffers of weights, then those of base.
 template <int R, bool BF16>
 __host__ __device__ constexpr uint32_t expand_w() { return expand_cols<BF16> * 128 * atoms_of<R>; }
 template <int R, bool BF16>
 constexpr uint32_t expand_smem() {
-    return 1024 + (BF16 ? 2 : 3) * 16384 * atoms_of<R> + 2 * expand_w<R, BF16>() + 2 * kTile * kRowPitch;
+    return 1024 + (BF16 ? 2 : 3) * 16384 * atoms_of<R> + 2 * expand_w<R, BF16>() + expand_bufs<R> * kTile * kRowPitch;
 }
 
 // A place in the sequence of (job, tile, block) that the CTAs share out.
@@ -360,22 +366,23 @@ struct ExpandAt {
 
 // One wave of CTAs shares the blocks (128 tokens of a tile x 256 bytes of their rows) of all jobs
 // evenly, in the order job, tile, block, so that a CTA keeps a tile's h for its run of blocks. base's
-// rows come by bulk copies into shared memory, the matrix instructions' sums (128 tokens x the
-// block's columns, in tensor memory) are added there, and the rows leave by bulk copies: the threads
-// between them handle 16 bytes at a time and no addresses. (With loads and stores from the threads
-// themselves, 8192 tokens x 14336 columns took 209 us by mma.sync and 243 us by tcgen05: 20 to 33
-// instructions for each 32 numbers.)
+// rows are copied to shared memory some blocks ahead, the matrix instructions' sums (128 tokens x the
+// block's columns, in tensor memory) are added to them there, and they leave in lines of 128 bytes.
+// 8192 tokens x 14336 columns, BF16, rank 64: 91 us. Before: 209 us by mma.sync with the sums
+// going to memory from its registers, 243 us from tensor memory number by number (20 to 33
+// instructions for each 32 of them), 143 us with a bulk copy for each row's 256 or 128 bytes, which
+// the copy engine takes 14 cycles each for.
 // WT: the weights' column index is the contiguous one (A), else the rank index is (B).
 // BF16: base and out are BF16; h then enters as its two upper parts (16 bits), whose loss is 2^-17
 // where the output's own rounding is 2^-9. FP32 outputs take all three (24 bits).
 template <int R, bool WT, bool BF16>
 __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_bar[10];
+    __shared__ __align__(8) uint64_t s_bar[4 + 3 * expand_bufs<R>];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
-    constexpr uint32_t kTmem = 2 * kCols;
+    constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t tiles = p.b.plan[1];
@@ -406,15 +413,18 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sH = s0, sW = sH + kParts * kPart, sRow = sW + 2 * expand_w<R, BF16>();
     uint8_t* const rows = smem_raw + (sRow - smem_u32(smem_raw));
-    // barriers, two each: full (weights, and parts before them, have landed), empty (the matrix
-    // instructions that read them are done), d (a block's sums are complete), base (its base has
-    // landed), free (its sums and its rows' buffer have been read out)
-    const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 16, bar_d = bar_full + 32, bar_base = bar_full + 48, bar_free = bar_full + 64;
+    // barriers: full[2] (weights, and parts before them, have landed), empty[2] (the matrix instructions
+    // that read them are done); for each buffer d (a block's sums are complete), base (its base has
+    // landed), free (its sums and its rows have been read out)
+    const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 16, bar_d = bar_full + 32, bar_base = bar_d + 8 * kBufs,
+                   bar_free = bar_base + 8 * kBufs;
     if (tid == 0) {
         s_abort = 0;
         for (uint32_t i = 0; i < 2; ++i) {
             bar_init(bar_full + 8 * i, kExpandLoad);
             bar_init(bar_empty + 8 * i, 1);
+        }
+        for (uint32_t i = 0; i < kBufs; ++i) {
             bar_init(bar_d + 8 * i, 1);
             bar_init(bar_base + 8 * i, kExpandLoad);
             bar_init(bar_free + 8 * i, kExpandOut);
@@ -434,56 +444,81 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     auto left_out = [&](const ExpandJob& j, uint32_t rank) { return rank == 0 && j.base == j.out && j.base_stride == j.out_stride; };
 
     if (warp >= kExpandOut / 32 && warp < kIssueWarp) {
-        const uint32_t t0 = tid - kExpandOut; // this thread copies the block's row t0
+        // base: piece t0 % 16 of the rows t0 / 16 + 8 i; weights and parts likewise by pieces of 16 bytes
+        const uint32_t t0 = tid - kExpandOut, piece = t0 & 15u;
         constexpr uint32_t kC = R / 8;
         uint4 tl = make_uint4(0, 0, 0, 0);
-        uint32_t rank = 0, turn = 0, step = 0; // turns of the base buffers, of the weights' buffers
-        uint64_t tok = 0;
-        bool fresh = true, parts_in = false; // another tile; its parts are in place (with one source)
+        uint32_t rank = 0, turn = 0, step = 0, pending = ~0u; // pending: the weights' buffer that is being filled
+        uint64_t row[16] = {};
+        bool fresh = true, parts_in = false, ok = true; // another tile; the parts in place are those of all sources
         ExpandAt at = start;
-        for (uint32_t u = 0; u < n_units; ++u) {
+        auto filled = [&]() { // all but the copies queued last have landed
+            if (pending == ~0u) return;
+            fence_operands();
+            bar_arrive(bar_full + 8 * pending);
+            pending = ~0u;
+        };
+        for (uint32_t u = 0; u < n_units && ok; ++u) {
             const ExpandJob& job = p.job[at.job];
             if (fresh) {
                 tl = tile_of[at.tile];
                 rank = rank_at(tl);
-                tok = t0 < tl.z ? p.b.plan[o.perm + tl.y + t0] : 0;
                 parts_in = false;
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) {
+                    const uint32_t r = (t0 >> 4) + 8 * i;
+                    row[i] = r < tl.z ? p.b.plan[o.perm + tl.y + r] * job.base_stride : ~0ull;
+                }
             }
-            const uint32_t nb = at.block, n0 = nb * kCols, a = tl.x, count = tl.z;
+            const uint32_t n0 = at.block * kCols, N = job.width, count = tl.z, sources = rank ? job.n_src : 0u;
             if (!left_out(job, rank)) {
-                const uint32_t buf = turn & 1u;
-                if (turn >= 2 && !bar_wait(bar_free + 8 * buf, (turn / 2 - 1) & 1u, abort_flag)) break;
-                const uint32_t bytes = t0 < count && job.base ? min(kCols, job.width - n0) * es : 0u;
-                asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}"
-                             ::"r"(bar_base + 8 * buf), "r"(bytes) : "memory");
-                if (bytes)
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                 ::"r"(sRow + buf * kTile * kRowPitch + t0 * kRowPitch), "l"(job.base + (tok * job.base_stride + n0) * es),
-                                   "r"(bytes), "r"(bar_base + 8 * buf) : "memory");
+                const uint32_t buf = turn % kBufs, n = n0 + piece * (16 / es);
+                // The wait below is for the turn kBufs (2 or more) before this one. A turn with weights tells
+                // of those of the turn before it, so that one is never held up by this thread; a turn
+                // without any has to tell here.
+                if (sources == 0) {
+                    cp_async_wait<0>();
+                    filled();
+                }
+                if (turn >= kBufs && !bar_wait(bar_free + 8 * buf, (turn / kBufs - 1) & 1u, abort_flag)) break;
+                if (job.base && n < N) {
+                    const uint32_t dst = sRow + (buf * kTile + (t0 >> 4)) * kRowPitch + 16 * piece;
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i)
+                        cp_async16_if(row[i] != ~0ull, dst + 8 * i * kRowPitch, job.base + (row[i] + n) * es, 16u);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_base + 8 * buf) : "memory");
                 ++turn;
-                for (uint32_t si = 0; si < (rank ? job.n_src : 0u); ++si, ++step) {
-                    const ExpandSrc& src = p.src[job.src + si];
-                    const uint32_t wb = step & 1u;
-                    if (step >= 2 && !bar_wait(bar_empty + 8 * wb, (step / 2 - 1) & 1u, abort_flag)) break;
-                    if (!parts_in) { // once what stood there has been read
-                        if (step > 0 && !bar_wait(bar_empty + 8 * (wb ^ 1u), ((step - 1) / 2) & 1u, abort_flag)) break;
+            }
+            for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) { // a group of sources at a time
+                const uint32_t wb = step & 1u, sb = sW + wb * expand_w<R, BF16>(), g1 = min(g0 + kGroup, sources);
+                if (step >= 2 && !bar_wait(bar_empty + 8 * wb, (step / 2 - 1) & 1u, abort_flag)) { ok = false; break; }
+                if (!parts_in) { // once what stood there has been read
+                    if (step > 0) {
+                        cp_async_wait<0>();
+                        filled();
+                        if (!bar_wait(bar_empty + 8 * (wb ^ 1u), ((step - 1) / 2) & 1u, abort_flag)) { ok = false; break; }
+                    }
+                    for (uint32_t g = g0; g < g1; ++g)
 #pragma unroll
                         for (uint32_t t = 0; t < kParts; ++t)
                             for (uint32_t c = t0; c < count * kC; c += kExpandLoad) {
-                                const uint32_t r = c / kC, j = c % kC;
-                                cp_async16(sH + t * kPart + (j >> 3) * 16384 + sw128(r, j & 7u),
-                                           src.parts + uint64_t(t) * p.b.part_stride + uint64_t(tl.y + r) * R + 8 * j, 16u);
+                                const uint32_t r = c / kC, j = c % kC, at_j = (g - g0) * kC + j;
+                                cp_async16(sH + t * kPart + (at_j >> 3) * 16384 + sw128(r, at_j & 7u),
+                                           p.src[job.src + g].parts + uint64_t(t) * p.b.part_stride + uint64_t(tl.y + r) * R + 8 * j, 16u);
                             }
-                        parts_in = job.n_src == 1;
-                    }
-                    const uint16_t* w = src.w + uint64_t(a) * p.b.rank_max * job.width;
-                    const uint32_t sb = sW + wb * expand_w<R, BF16>(), N = job.width;
+                    parts_in = sources <= kGroup;
+                }
+                for (uint32_t g = g0; g < g1; ++g) {
+                    const ExpandSrc& src = p.src[job.src + g];
+                    const uint16_t* w = src.w + uint64_t(tl.x) * p.b.rank_max * N;
                     if (!WT) {
 #pragma unroll 4
                         for (uint32_t c = t0; c < kCols * kC; c += kExpandLoad) {
-                            const uint32_t n = c / kC, j = c % kC;
+                            const uint32_t n = c / kC, j = c % kC, at_j = (g - g0) * kC + j;
                             const uint32_t take = n0 + n < N && 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
-                            cp_async16(sb + (j >> 3) * (kCols * 128) + sw128(n, j & 7u), take ? w + uint64_t(n0 + n) * p.b.rank_max + 8 * j : src.w, take);
+                            cp_async16(sb + (at_j >> 3) * (kCols * 128) + sw128(n, at_j & 7u),
+                                       take ? w + uint64_t(n0 + n) * p.b.rank_max + 8 * j : src.w, take);
                         }
                     } else {
                         constexpr uint32_t kRow = kCols / 8; // pieces of a rank's columns
@@ -491,44 +526,43 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                         for (uint32_t c = t0; c < R * kRow; c += kExpandLoad) {
                             const uint32_t j = c / kRow, q = c % kRow, n = n0 + 8 * q;
                             const bool on = j < rank && n < N;
-                            cp_async16(sb + (q >> 3) * (R * 128) + sw128(j, q & 7u), on ? w + uint64_t(j) * N + n : src.w, on ? 16u : 0u);
+                            cp_async16(sb + (q >> 3) * (kGroup * R * 128) + sw128((g - g0) * R + j, q & 7u), on ? w + uint64_t(j) * N + n : src.w, on ? 16u : 0u);
                         }
                     }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    fence_operands();
-                    bar_arrive(bar_full + 8 * wb);
                 }
+                cp_async_commit();
+                if (pending != ~0u) cp_async_wait<1>();
+                filled();
+                pending = wb;
             }
             fresh = next(at);
         }
         cp_async_wait<0>();
-        if (*abort_flag) { // given up: the copies that are under way must land before the CTA ends
-            volatile int own = 0;
-            for (uint32_t k = turn >= 2 ? turn - 2 : 0; k < turn; ++k) bar_wait(bar_base + 8 * (k & 1u), (k / 2) & 1u, &own);
-        }
+        filled();
     } else if (tid == kIssueWarp * 32) {
         const uint32_t idesc = idesc_of(kCols, false, WT);
         uint32_t rank = 0, turn = 0, step = 0;
-        bool fresh = true;
+        bool fresh = true, ok = true;
         ExpandAt at = start;
-        for (uint32_t u = 0; u < n_units; ++u) {
+        for (uint32_t u = 0; u < n_units && ok; ++u) {
             const ExpandJob& job = p.job[at.job];
             if (fresh) rank = rank_at(tile_of[at.tile]);
             if (!left_out(job, rank)) {
-                const uint32_t db = turn & 1u, kn = (rank + 15) / 16;
-                if (turn >= 2 && !bar_wait(bar_free + 8 * db, (turn / 2 - 1) & 1u, abort_flag)) break;
-                for (uint32_t si = 0; si < (rank ? job.n_src : 0u); ++si, ++step) {
+                const uint32_t db = turn % kBufs, kn = (rank + 15) / 16, sources = rank ? job.n_src : 0u;
+                if (turn >= kBufs && !bar_wait(bar_free + 8 * db, (turn / kBufs - 1) & 1u, abort_flag)) break;
+                for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) {
                     const uint32_t wb = step & 1u, w = sW + wb * expand_w<R, BF16>();
-                    if (!bar_wait(bar_full + 8 * wb, (step / 2) & 1u, abort_flag)) break;
+                    if (!bar_wait(bar_full + 8 * wb, (step / 2) & 1u, abort_flag)) { ok = false; break; }
                     fence_after();
-                    for (uint32_t kk = 0; kk < kn; ++kk) {
-                        const uint64_t bd = WT ? mn_major(w + kk * 2048, R * 128) : k_major(w + (kk >> 2) * (kCols * 128) + (kk & 3u) * 32);
+                    for (uint32_t g = g0; g < min(g0 + kGroup, sources); ++g)
+                        for (uint32_t k1 = 0; k1 < kn; ++k1) {
+                            const uint32_t kk = (g - g0) * (R / 16) + k1;
+                            const uint64_t bd = WT ? mn_major(w + kk * 2048, kGroup * R * 128) : k_major(w + (kk >> 2) * (kCols * 128) + (kk & 3u) * 32);
 #pragma unroll
-                        for (int t = kParts - 1; t >= 0; --t) // small parts first
-                            mma_tc(tmem + db * kCols, k_major(sH + t * kPart + (kk >> 2) * 16384 + (kk & 3u) * 32), bd, idesc,
-                                   !(si == 0 && kk == 0 && t == static_cast<int>(kParts) - 1));
-                    }
+                            for (int t = kParts - 1; t >= 0; --t) // small parts first
+                                mma_tc(tmem + db * kCols, k_major(sH + t * kPart + (kk >> 2) * 16384 + (kk & 3u) * 32), bd, idesc,
+                                       !(g == 0 && k1 == 0 && t == static_cast<int>(kParts) - 1));
+                        }
                     commit_tc(bar_empty + 8 * wb);
                 }
                 if (rank) commit_tc(bar_d + 8 * db);
@@ -538,13 +572,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             fresh = next(at);
         }
     } else if (warp < kExpandOut / 32) {
-        // warps w and w + 4: tokens 32 (w % 4) .. of the tile, a token each lane; w the first half of a
-        // block's row, w + 4 the second
-        const uint32_t r = (warp & 3u) * 32 + lane, half = warp >> 2;
+        // warps w and w + 4: tokens 32 (w % 4) .. of the tile, w the first half of a block's rows, w + 4
+        // the second. A lane adds a token's sums to its row; then 8 lanes write 128 bytes of a row.
+        const uint32_t r0 = (warp & 3u) * 32, half = warp >> 2;
         constexpr uint32_t kHalf = kCols / 2;
         uint4 tl = make_uint4(0, 0, 0, 0);
         uint32_t rank = 0, turn = 0;
-        uint64_t tok = 0;
+        uint64_t row[8] = {}; // of the rows r0 + lane / 8 + 4 i
         bool fresh = true;
         ExpandAt at = start;
         for (uint32_t u = 0; u < n_units; ++u) {
@@ -552,20 +586,24 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             if (fresh) {
                 tl = tile_of[at.tile];
                 rank = rank_at(tl);
-                tok = r < tl.z ? p.b.plan[o.perm + tl.y + r] : 0;
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) {
+                    const uint32_t r = r0 + (lane >> 3) + 4 * i;
+                    row[i] = r < tl.z ? p.b.plan[o.perm + tl.y + r] * job.out_stride : ~0ull;
+                }
             }
             if (!left_out(job, rank)) {
-                const uint32_t buf = turn & 1u, n0 = at.block * kCols + half * kHalf;
-                uint8_t* row = rows + buf * kTile * kRowPitch + r * kRowPitch + half * (kRowBytes / 2);
-                if (!bar_wait(bar_base + 8 * buf, (turn / 2) & 1u, abort_flag)) break;
-                if (!bar_wait(bar_d + 8 * buf, (turn / 2) & 1u, abort_flag)) break;
+                const uint32_t buf = turn % kBufs, n = at.block * kCols + half * kHalf + (lane & 7u) * (16 / es);
+                uint8_t* mine = rows + (buf * kTile + r0) * kRowPitch + half * (kRowBytes / 2);
+                if (!bar_wait(bar_base + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
+                if (!bar_wait(bar_d + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
                 fence_after();
                 if (rank || !job.base)
 #pragma unroll
                     for (uint32_t c = 0; c < kHalf; c += 16) {
                         uint32_t d[16] = {};
-                        if (rank) tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + buf * kCols + half * kHalf + c);
-                        uint4* at16 = reinterpret_cast<uint4*>(row + c * es);
+                        if (rank) tmem_ld16(d, tmem + (r0 << 16) + buf * kCols + half * kHalf + c);
+                        uint4* at16 = reinterpret_cast<uint4*>(mine + lane * kRowPitch + c * es);
 #pragma unroll
                         for (uint32_t q = 0; q < es; ++q) { // 16 bytes: 8 BF16 or 4 FP32
                             uint4 v = job.base ? at16[q] : make_uint4(0, 0, 0, 0);
@@ -582,20 +620,20 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                         }
                     }
                 fence_before();
-                fence_operands(); // read by the copy below
-                if (r < tl.z && n0 < job.width) {
-                    const uint32_t bytes = min(kHalf, job.width - n0) * es;
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                                 ::"l"(job.out + (tok * job.out_stride + n0) * es), "r"(smem_u32(row)), "r"(bytes) : "memory");
+                __syncwarp();
+                if (n < job.width) {
+                    const uint8_t* from = mine + (lane >> 3) * kRowPitch + (lane & 7u) * 16;
+                    uint8_t* to = job.out + uint64_t(n) * es;
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i)
+                        if (row[i] != ~0ull) *reinterpret_cast<uint4*>(to + row[i] * es) = *reinterpret_cast<const uint4*>(from + 4 * i * kRowPitch);
                 }
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
                 bar_arrive(bar_free + 8 * buf);
                 ++turn;
             }
             fresh = next(at);
         }
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     fence_before();
     __syncthreads();

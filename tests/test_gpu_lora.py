@@ -100,6 +100,7 @@ def check_forward(c, dt, in_place=False, y_pad=0, base=True):
     state = c.set.state(c.T)
     c.set.forward(c.plan, c.xd, ys, bases=None if in_place else based if base else [None] * len(ys), state=state)
     torch.cuda.synchronize()
+    assert int(c.plan.err) & 2 == 0  # no wait ran out
     for k in range(len(c.projs)):
         x, a, b = c.f64(k)
         want, h = L.forward(x, c.idx, a, b, c.scales, c.ranks, base_np[k].astype(np.float64))
@@ -130,6 +131,7 @@ def check_backward(c, dt, state, dx=True, base=True, accumulate=False):
     c.set.backward(c.plan, c.xd, dyd, state, das, dbs, dxs=dxs if dx else None, dx_bases=dxd if base and dx else None,
                    accumulate=accumulate)
     torch.cuda.synchronize()
+    assert int(c.plan.err) & 2 == 0
     want_dx = [v.astype(np.float64) for v in dxb]
     tol_dx = [np.abs(v).astype(np.float64) * 4 * U for v in dxb]
     for k in range(n):
@@ -175,6 +177,10 @@ SIZES = [  # tokens, adapters, rank_max, projections, route, ranks
     (1025, 7, 128, [(136, 144)], "mixed", [128, 127, 64, 65, 3]),
     (64, 5, 16, [(4096, 3584)], "none", None),
     (200, 6, 16, [(136, 2056)], "one", None),
+    # many blocks a CTA, the last tiles without an adapter (a run of blocks with nothing to multiply)
+    (700, 2, 16, [(14336, 64)], "runs", None),
+    (400, 3, 128, [(8200, 72)], "runs", [100, 0, 128]),
+    (257, 2, 16, [(64, 8200), (72, 8200), (80, 8200), (64, 8200), (72, 8200)], "runs", None),
 ]
 
 
