@@ -160,11 +160,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
 constexpr uint32_t kPlanSmem = 220 * 1024;
 
 // ---------------------------------------------------------------- what the tiled kernels share
-constexpr int kTiledThreads = 256;
-// Rows in shared memory are padded by 16 bytes, so that the 8 rows of an 8 x 8 matrix lie in
-// different banks for every rank.
-template <int BYTES>
-constexpr uint32_t padded = BYTES + 16;
+template <int R>
+constexpr uint32_t atoms_of = R > 64 ? 2 : 1; // 64 ranks each
 
 struct ShrinkJob {
     const uint16_t* src; // [tokens][stride]: x or dy
@@ -180,20 +177,30 @@ struct ShrinkParams {
     ShrinkJob job[kMaxItems];
 };
 
-constexpr int kShrinkStages = 3;
+// Threads that add up, that load; a warp more issues. 4 stages of 64 of the summed index: x (128 tokens
+// x 64, K-major) and the weights (R x 64 K-major, or 64 x R MN-major).
+constexpr uint32_t kShrinkLoad = 128, kShrinkStages = 4;
+template <int R>
+constexpr uint32_t shrink_out = R > 64 ? 256 : 128; // rank 128: two threads a token, 64 ranks each
+template <int R>
+constexpr uint32_t shrink_threads = shrink_out<R> + kShrinkLoad + 32;
 template <int R, bool WT>
-__host__ __device__ constexpr uint32_t shrink_stage() { return kTile * padded<128> + (WT ? 64 * padded<2 * R> : R * padded<128>); }
+__host__ __device__ constexpr uint32_t shrink_stage() { return 16384 + (WT ? 8192 * atoms_of<R> : R * 128); }
 template <int R, bool WT>
 constexpr uint32_t shrink_smem() {
-    return std::max<uint32_t>(kShrinkStages * shrink_stage<R, WT>(), kTile * (R + 4) * 4);
+    return 1024 + std::max<uint32_t>(kShrinkStages * shrink_stage<R, WT>(), kTile * (R + 4) * 4);
 }
+constexpr uint32_t kFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
 
 // WT: the weights' rank index is the contiguous one (B), else the summed index is (A).
 template <int R, bool WT>
-__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int WN = R == 16 ? 1 : 2, WM = 8 / WN, MT = 8 / WM, NT = R / WN / 8; // warps, 16-token and 8-rank tiles of a warp
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp % WM, wn = warp / WM;
+__global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_bar[2 * kShrinkStages + 4];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    constexpr uint32_t kTmem = R <= 16 ? 32 : 2 * R, S = kShrinkStages, kShrinkOut = shrink_out<R>, kRanks = R > 64 ? 64 : R;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     if (tile >= p.b.plan[0]) return; // the whole cluster
@@ -201,99 +208,120 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_shrink_ke
     const ShrinkJob& job = p.job[blockIdx.y];
     const uint32_t a = tl.x, first = tl.y, count = tl.z, rank = rank_of(p.b, a), K = job.width;
     const uint32_t steps = (K + 63) / 64, per = (steps + p.split - 1) / p.split;
-    const uint32_t k_begin = min(part * per, steps), k_end = min(k_begin + per, steps);
-    // this thread's pieces: x rows tid / 8 + 32 i, 16 bytes at 8 (tid % 8) of the step's 64 columns
-    const uint32_t chunk = tid & 7u;
-    const uint16_t* xrow[4];
-    bool live[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = (tid >> 3) + 32 * i;
-        live[i] = r < count;
-        xrow[i] = live[i] ? job.src + uint64_t(p.b.plan[o.perm + first + r]) * job.stride : job.src;
-    }
-    const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
-    const uint32_t s0 = smem_u32(smem);
-    constexpr uint32_t kStage = shrink_stage<R, WT>(), kW = kTile * padded<128>;
-    auto load = [&](uint32_t step) {
-        const uint32_t k = step * 64, sb = s0 + (step - k_begin) % kShrinkStages * kStage;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool on = live[i] && k + 8 * chunk < K;
-            cp_async16(sb + ((tid >> 3) + 32 * i) * padded<128> + 16 * chunk, on ? xrow[i] + k + 8 * chunk : job.src, on ? 16u : 0u);
+    const uint32_t k_begin = min(part * per, steps), n_steps = min(k_begin + per, steps) - k_begin;
+    const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    constexpr uint32_t kStage = shrink_stage<R, WT>();
+    // barriers: full[S] (a stage has landed), empty[S] (its matrix instructions are done), d[2] (a
+    // chain's sums are complete), free[2] (they have been added up)
+    const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 8 * S, bar_d = bar_empty + 8 * S, bar_free = bar_d + 16;
+    if (tid == 0) {
+        s_abort = 0;
+        for (uint32_t i = 0; i < S; ++i) {
+            bar_init(bar_full + 8 * i, kShrinkLoad);
+            bar_init(bar_empty + 8 * i, 1);
         }
-        if (!WT) {
-#pragma unroll
-            for (uint32_t c = tid; c < R * 8; c += kTiledThreads) {
-                const uint32_t j = c >> 3, kc = k + 8 * (c & 7u);
-                const bool on = j < rank && kc < K;
-                cp_async16(sb + kW + j * padded<128> + 16 * (c & 7u), on ? w + uint64_t(j) * K + kc : job.w, on ? 16u : 0u);
-            }
-        } else {
-            constexpr uint32_t kC = R / 8; // pieces of a row
-#pragma unroll
-            for (uint32_t c = tid; c < 64 * kC; c += kTiledThreads) {
-                const uint32_t kr = c / kC, j = 8 * (c % kC);
-                const uint32_t bytes = k + kr < K && j < rank ? min(rank - j, 8u) * 2u : 0u;
-                cp_async16(sb + kW + kr * padded<2 * R> + 2 * j, bytes ? w + uint64_t(k + kr) * p.b.rank_max + j : job.w, bytes);
-            }
+        for (uint32_t i = 0; i < 2; ++i) {
+            bar_init(bar_d + 8 * i, 1);
+            bar_init(bar_free + 8 * i, kShrinkOut);
         }
-    };
-    float sum[MT][NT][4] = {}, acc[MT][NT][4] = {};
-    for (uint32_t s = k_begin; s < k_begin + kShrinkStages - 1; ++s) {
-        if (s < k_end) load(s);
-        cp_async_commit();
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (uint32_t s = k_begin; s < k_end; ++s) {
-        cp_async_wait<kShrinkStages - 2>();
-        __syncthreads();
-        if (s + kShrinkStages - 1 < k_end) load(s + kShrinkStages - 1);
-        cp_async_commit();
-        const uint32_t sb = s0 + (s - k_begin) % kShrinkStages * kStage;
+    constexpr uint32_t kIssueWarp = (kShrinkOut + kShrinkLoad) / 32;
+    if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort_flag = &s_abort;
+    float* red = reinterpret_cast<float*>(smem_raw + (s0 - smem_u32(smem_raw))); // [128][R + 4], over the stages at the end
+
+    if (warp >= kShrinkOut / 32 && warp < kIssueWarp) {
+        // piece t0 % 8 of the rows t0 / 8 + 16 i of x; rows past the tokens stand for nothing
+        const uint32_t t0 = tid - kShrinkOut, chunk = t0 & 7u;
+        uint64_t row[8];
 #pragma unroll
-        for (uint32_t kk = 0; kk < 4; ++kk) {
-            uint32_t af[MT][4];
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t r = (t0 >> 3) + 16 * i;
+            row[i] = r < count ? p.b.plan[o.perm + first + r] * job.stride : ~0ull;
+        }
+        const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
+        auto landed = [&](uint32_t s) {
+            fence_operands();
+            bar_arrive(bar_full + 8 * (s % S));
+        };
+        uint32_t s = 0;
+        for (; s < n_steps; ++s) {
+            if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
+            const uint32_t k = (k_begin + s) * 64, sb = s0 + s % S * kStage, sw = sb + 16384, kx = k + 8 * chunk;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                ldsm4(af[m], sb + (wm * MT * 16 + m * 16 + (lane & 15u)) * padded<128> + 16 * (2 * kk + (lane >> 4)));
+            for (uint32_t i = 0; i < 8; ++i)
+                cp_async16_if(row[i] != ~0ull, sb + sw128((t0 >> 3) + 16 * i, chunk), kx < K ? job.src + row[i] + kx : job.src, kx < K ? 16u : 0u);
+            if (!WT) {
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t bf[4];
-                const uint32_t j = wn * NT * 8 + n * 8;
-                if (!WT) ldsm4(bf, sb + kW + (j + (lane & 7u) + ((lane >> 4) << 3)) * padded<128> + 16 * (2 * kk + ((lane >> 3) & 1u)));
-                else ldsm4t(bf, sb + kW + (kk * 16 + (lane & 15u)) * padded<2 * R> + 2 * (j + 8 * (lane >> 4)));
+                for (uint32_t c = t0; c < R * 8; c += kShrinkLoad) {
+                    const uint32_t j = c >> 3, kc = k + 8 * (c & 7u);
+                    const bool on = j < rank && kc < K;
+                    cp_async16(sw + sw128(j, c & 7u), on ? w + uint64_t(j) * K + kc : job.w, on ? 16u : 0u);
+                }
+            } else {
+                constexpr uint32_t kC = R / 8; // pieces of a row
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma16816(acc[m][n], af[m], bf[0], bf[1]);
-                    mma16816(acc[m][n + 1], af[m], bf[2], bf[3]);
+                for (uint32_t c = t0; c < 64 * kC; c += kShrinkLoad) {
+                    const uint32_t kr = c / kC, j = c % kC;
+                    const uint32_t bytes = k + kr < K && 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
+                    cp_async16(sw + (j >> 3) * 8192 + sw128(kr, j & 7u), bytes ? w + uint64_t(k + kr) * p.b.rank_max + 8 * j : job.w, bytes);
                 }
             }
+            cp_async_commit();
+            if (s >= 2) { // three stages under way, the oldest has landed
+                cp_async_wait<2>();
+                landed(s - 2);
+            }
         }
-        if (((s - k_begin) & 3u) == 3u || s + 1 == k_end) { // 16 matrix instructions long
+        cp_async_wait<0>();
+        if (s == n_steps)
+            for (uint32_t l = n_steps > 2 ? n_steps - 2 : 0; l < n_steps; ++l) landed(l);
+    } else if (tid == kIssueWarp * 32) {
+        const uint32_t idesc = idesc_of(R, false, WT);
+        for (uint32_t s = 0; s < n_steps; ++s) {
+            const uint32_t chain = s / kFlush, db = chain & 1u;
+            if (s % kFlush == 0 && chain >= 2 && !bar_wait(bar_free + 8 * db, (chain / 2 - 1) & 1u, abort_flag)) break;
+            if (!bar_wait(bar_full + 8 * (s % S), (s / S) & 1u, abort_flag)) break;
+            fence_after();
+            const uint32_t x = s0 + s % S * kStage, w = x + 16384;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) { sum[m][n][q] += acc[m][n][q]; acc[m][n][q] = 0.f; }
+            for (uint32_t kk = 0; kk < 4; ++kk)
+                mma_tc(tmem + db * R, k_major(x + kk * 32), WT ? mn_major(w + kk * 2048, 8192) : k_major(w + kk * 32), idesc, !(s % kFlush == 0 && kk == 0));
+            commit_tc(bar_empty + 8 * (s % S));
+            if (s % kFlush == kFlush - 1 || s + 1 == n_steps) commit_tc(bar_d + 8 * db);
         }
+    } else if (warp < kShrinkOut / 32) {
+        const uint32_t chains = (n_steps + kFlush - 1) / kFlush, j0 = (warp >> 2) * kRanks;
+        float sum[kRanks] = {}; // of token 32 (warp % 4) + lane
+        for (uint32_t c = 0; c < chains; ++c) {
+            if (!bar_wait(bar_d + 8 * (c & 1u), (c / 2) & 1u, abort_flag)) break;
+            fence_after();
+#pragma unroll
+            for (uint32_t j = 0; j < kRanks; j += 16) {
+                uint32_t d[16];
+                tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + (c & 1u) * R + j0 + j);
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
+            }
+            fence_before();
+            bar_arrive(bar_free + 8 * (c & 1u));
+        }
+        // every stage has been read: their place holds the sums from here on
+#pragma unroll
+        for (uint32_t j = 0; j < kRanks; j += 4)
+            *reinterpret_cast<float4*>(red + ((warp & 3u) * 32 + lane) * (R + 4) + j0 + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
     }
-    cp_async_wait<0>();
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(smem); // [128][R + 4]
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t r = wm * MT * 16 + m * 16 + (lane >> 2), c = wn * NT * 8 + n * 8 + 2 * (lane & 3u);
-            *reinterpret_cast<float2*>(red + r * (R + 4) + c) = make_float2(sum[m][n][0], sum[m][n][1]);
-            *reinterpret_cast<float2*>(red + (r + 8) * (R + 4) + c) = make_float2(sum[m][n][2], sum[m][n][3]);
-        }
+    fence_before();
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
     const uint32_t rows = kTile / p.split; // rows that this CTA adds up and writes
-    for (uint32_t i = tid; i < rows * (R / 8); i += kTiledThreads) {
+    for (uint32_t i = tid; i < rows * (R / 8); i += shrink_threads<R>) {
         const uint32_t r = part * rows + i / (R / 8), c = 8 * (i % (R / 8));
         if (r >= count) continue;
         float v[8] = {};
@@ -317,6 +345,11 @@ __global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_shrink_ke
             *reinterpret_cast<uint4*>(dst + uint64_t(t) * p.b.part_stride) = make_uint4(w3[t][0], w3[t][1], w3[t][2], w3[t][3]);
     }
     cluster.sync(); // the peers may still read this CTA's sums
+    if (tid == 0 && s_abort && p.b.err) atomicOr(p.b.err, 2u);
+    if (warp == kIssueWarp) {
+        __syncwarp();
+        tmem_free(tmem, kTmem);
+    }
 }
 
 // ---------------------------------------------------------------- expand
@@ -343,8 +376,6 @@ constexpr uint32_t kExpandOut = 256, kExpandLoad = 128, kExpandThreads = kExpand
 constexpr uint32_t kRowBytes = 256, kRowPitch = kRowBytes + 16; // of a block's rows of base, which become those of out
 template <bool BF16>
 constexpr uint32_t expand_cols = kRowBytes / (BF16 ? 2 : 4); // columns of a block
-template <int R>
-constexpr uint32_t atoms_of = R > 64 ? 2 : 1; // 64 ranks each
 // Buffers of base and of sums: as many as fit beside the operands, of which rank 128 has twice the bytes.
 template <int R>
 constexpr uint32_t expand_bufs = R > 64 ? 2 : 4;
@@ -658,124 +689,175 @@ struct OuterParams {
     uint32_t accumulate; // add to out, adapters without tokens left as they are
     OuterJob job[2 * kMaxItems];
 };
-constexpr int kOuterStages = 3;
-constexpr uint32_t kOuterTok = 32; // tokens of a step
+// Threads that add up, that load; a warp more issues. A stage holds 64 tokens: their columns (MN-major)
+// and the three parts of their ranks (MN-major). 256 columns a CTA, a thread each; rank 128: 128
+// columns, two threads each, 64 ranks a thread.
+constexpr uint32_t kOuterOut = 256, kOuterLoad = 128, kOuterThreads = kOuterOut + kOuterLoad + 32, kOuterTok = 64, kOuterStages = 3;
 template <int R>
-__host__ __device__ constexpr uint32_t outer_stage() { return kOuterTok * padded<256> + 3 * kOuterTok * padded<2 * R>; }
+constexpr uint32_t outer_cols = R > 64 ? 128 : 256;
 template <int R>
-constexpr uint32_t outer_smem() { return std::max<uint32_t>(kOuterStages * outer_stage<R>(), R * 132 * 4); }
+__host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 3 * 8192 * atoms_of<R>; }
+template <int R>
+constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(kOuterStages * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
+constexpr uint32_t kOuterFlush = 2; // stages whose sums stay in tensor memory: chains of 24 matrix instructions
 
 template <int R>
-__global__ void __launch_bounds__(kTiledThreads, R <= 64 ? 2 : 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int WM = R == 16 ? 1 : R / 32, WN = 8 / WM, MT = R / WM / 16, NT = 16 / WN; // warps, 16-rank and 8-column tiles
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, wm = warp % WM, wn = warp / WM;
-    const uint32_t part = blockIdx.x % p.split, c0 = blockIdx.x / p.split * 128, a = blockIdx.y;
+__global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kTmem = 2 * kHalves * R; // 64 .. 256
+    constexpr uint32_t kStage = outer_stage<R>(), kPart = 8192 * atoms_of<R>, kRanks = R > 64 ? 64 : R;
+    __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    const uint32_t part = blockIdx.x % p.split, c0 = blockIdx.x / p.split * kOuterCols, a = blockIdx.y;
     const OuterJob& job = p.job[blockIdx.z];
     if (c0 >= job.width) return; // the whole cluster
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t t_begin = p.b.plan[o.begin + a], t_end = p.b.plan[o.begin + a + 1];
-    if (p.accumulate && t_begin == t_end) return;
+    const uint32_t rm = p.b.rank_max, cols = min(kOuterCols, job.width - c0);
+    float* out = job.out + uint64_t(a) * rm * job.width;
+    if (t_begin == t_end) { // no tokens: zero, or as it is
+        if (p.accumulate) return;
+        if (!job.transposed) {
+            for (uint32_t i = part * kOuterThreads + tid; i < rm * (cols / 4); i += p.split * kOuterThreads)
+                *reinterpret_cast<float4*>(out + uint64_t(i / (cols / 4)) * job.width + c0 + 4 * (i % (cols / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            float4* d = reinterpret_cast<float4*>(out + uint64_t(c0) * rm);
+            for (uint32_t i = part * kOuterThreads + tid; i < cols * rm / 4; i += p.split * kOuterThreads) d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
     const uint32_t steps = (t_end - t_begin + kOuterTok - 1) / kOuterTok, per = (steps + p.split - 1) / p.split;
-    const uint32_t s_begin = min(part * per, steps), s_end = min(s_begin + per, steps);
-    const uint32_t s0 = smem_u32(smem);
-    constexpr uint32_t kStage = outer_stage<R>(), kP = kOuterTok * padded<256>, kPart = kOuterTok * padded<2 * R>;
-    auto load = [&](uint32_t s) {
-        const uint32_t t0 = t_begin + s * kOuterTok, sb = s0 + (s - s_begin) % kOuterStages * kStage;
-#pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) { // 32 rows of 16 pieces
-            const uint32_t r = (tid >> 4) + 16 * i, c = c0 + 8 * (tid & 15u);
-            const bool on = t0 + r < t_end && c < job.width;
-            cp_async16(sb + r * padded<256> + 16 * (tid & 15u), on ? job.src + uint64_t(p.b.plan[o.perm + t0 + r]) * job.stride + c : job.src,
-                       on ? 16u : 0u);
+    const uint32_t s_begin = min(part * per, steps), n_steps = min(s_begin + per, steps) - s_begin;
+    const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 8 * S, bar_d = bar_empty + 8 * S, bar_free = bar_d + 16; // as in shrink
+    if (tid == 0) {
+        s_abort = 0;
+        for (uint32_t i = 0; i < S; ++i) {
+            bar_init(bar_full + 8 * i, kOuterLoad);
+            bar_init(bar_empty + 8 * i, 1);
         }
-        constexpr uint32_t kC = R / 8;
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-#pragma unroll
-            for (uint32_t c = tid; c < kOuterTok * kC; c += kTiledThreads) {
-                const uint32_t r = c / kC, j = 8 * (c % kC);
-                const bool on = t0 + r < t_end;
-                cp_async16(sb + kP + t * kPart + r * padded<2 * R> + 2 * j,
-                           job.parts + uint64_t(t) * p.b.part_stride + uint64_t(on ? t0 + r : t_begin) * R + j, on ? 16u : 0u);
-            }
-    };
-    float sum[MT][NT][4] = {}, acc[MT][NT][4] = {};
-    for (uint32_t s = s_begin; s < s_begin + kOuterStages - 1; ++s) {
-        if (s < s_end) load(s);
-        cp_async_commit();
+        for (uint32_t i = 0; i < 2; ++i) {
+            bar_init(bar_d + 8 * i, 1);
+            bar_init(bar_free + 8 * i, kOuterOut);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (uint32_t s = s_begin; s < s_end; ++s) {
-        cp_async_wait<kOuterStages - 2>();
-        __syncthreads();
-        if (s + kOuterStages - 1 < s_end) load(s + kOuterStages - 1);
-        cp_async_commit();
-        const uint32_t sb = s0 + (s - s_begin) % kOuterStages * kStage;
-#pragma unroll
-        for (uint32_t kk = 0; kk < kOuterTok / 16; ++kk) {
-            uint32_t bf[NT / 2][4];
-#pragma unroll
-            for (int n = 0; n < NT / 2; ++n)
-                ldsm4t(bf[n], sb + (kk * 16 + (lane & 15u)) * padded<256> + 2 * (wn * NT * 8 + n * 16 + 8 * (lane >> 4)));
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t af[4]; // the transpose of [tokens][ranks]: (ranks lo, tokens lo), (hi, lo), (lo, hi), (hi, hi)
-                    ldsm4t(af, sb + kP + t * kPart + (kk * 16 + (lane & 7u) + ((lane >> 4) << 3)) * padded<2 * R> +
-                                   2 * ((wm * MT + m) * 16 + 8 * ((lane >> 3) & 1u)));
-#pragma unroll
-                    for (int n = 0; n < NT / 2; ++n) {
-                        mma16816(acc[m][2 * n], af, bf[n][0], bf[n][1]);
-                        mma16816(acc[m][2 * n + 1], af, bf[n][2], bf[n][3]);
-                    }
-                }
-        }
-        if (((s - s_begin) & 3u) == 3u || s + 1 == s_end) { // 24 matrix instructions long
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) { sum[m][n][q] += acc[m][n][q]; acc[m][n][q] = 0.f; }
-        }
-    }
-    cp_async_wait<0>();
+    constexpr uint32_t kIssueWarp = (kOuterOut + kOuterLoad) / 32;
+    if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    fence_before();
     __syncthreads();
-    float* red = reinterpret_cast<float*>(smem); // [R][132]
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort_flag = &s_abort;
+    float* red = reinterpret_cast<float*>(smem_raw + (s0 - smem_u32(smem_raw))); // [256][R + 4], over the stages at the end
+
+    if (warp >= kOuterOut / 32 && warp < kIssueWarp) {
+        // columns: 16-byte pieces, of every 4th (8th) token; pieces past the width stand for nothing, tokens
+        // past the last are 0 on both sides
+        constexpr uint32_t kPieces = kOuterCols / 8, kEvery = kOuterLoad / kPieces, kRows = kOuterTok / kEvery;
+        const uint32_t t0 = tid - kOuterOut, piece = t0 % kPieces, r0 = t0 / kPieces;
+        const bool in = 8 * piece < cols;
+        constexpr uint32_t kC = R / 8;
+        auto landed = [&](uint32_t s) {
+            fence_operands();
+            bar_arrive(bar_full + 8 * (s % S));
+        };
+        uint32_t s = 0;
+        for (; s < n_steps; ++s) {
+            const uint32_t first = t_begin + (s_begin + s) * kOuterTok, left = t_end - first;
+            uint64_t row[kRows];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+            for (uint32_t i = 0; i < kRows; ++i) {
+                const uint32_t r = r0 + kEvery * i;
+                row[i] = r < left ? p.b.plan[o.perm + first + r] * job.stride : ~0ull;
+            }
+            if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
+            const uint32_t sb = s0 + s % S * kStage, sg = sb + kOuterCols * 128;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t j = (wm * MT + m) * 16 + (lane >> 2), c = (wn * NT + n) * 8 + 2 * (lane & 3u);
-            *reinterpret_cast<float2*>(red + j * 132 + c) = make_float2(sum[m][n][0], sum[m][n][1]);
-            *reinterpret_cast<float2*>(red + (j + 8) * 132 + c) = make_float2(sum[m][n][2], sum[m][n][3]);
+            for (uint32_t i = 0; i < kRows; ++i) {
+                const bool on = row[i] != ~0ull;
+                cp_async16_if(in, sb + (piece >> 3) * 8192 + sw128(r0 + kEvery * i, piece & 7u), on ? job.src + row[i] + c0 + 8 * piece : job.src, on ? 16u : 0u);
+            }
+#pragma unroll
+            for (uint32_t t = 0; t < 3; ++t)
+#pragma unroll
+                for (uint32_t c = t0; c < kOuterTok * kC; c += kOuterLoad) {
+                    const uint32_t r = c / kC, j = c % kC;
+                    cp_async16(sg + t * kPart + (j >> 3) * 8192 + sw128(r, j & 7u),
+                               job.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < left ? first + r : t_begin) * R + 8 * j, r < left ? 16u : 0u);
+                }
+            cp_async_commit();
+            if (s >= 1) { // two stages under way, the older has landed
+                cp_async_wait<1>();
+                landed(s - 1);
+            }
         }
+        cp_async_wait<0>();
+        if (s == n_steps && n_steps) landed(n_steps - 1);
+    } else if (tid == kIssueWarp * 32) {
+        const uint32_t idesc = idesc_of(R, true, true);
+        for (uint32_t s = 0; s < n_steps; ++s) {
+            const uint32_t chain = s / kOuterFlush, db = chain & 1u;
+            if (s % kOuterFlush == 0 && chain >= 2 && !bar_wait(bar_free + 8 * db, (chain / 2 - 1) & 1u, abort_flag)) break;
+            if (!bar_wait(bar_full + 8 * (s % S), (s / S) & 1u, abort_flag)) break;
+            fence_after();
+            const uint32_t x = s0 + s % S * kStage, g = x + kOuterCols * 128;
+#pragma unroll
+            for (uint32_t kk = 0; kk < kOuterTok / 16; ++kk)
+#pragma unroll
+                for (int t = 2; t >= 0; --t) // small parts first
+#pragma unroll
+                    for (uint32_t h = 0; h < kHalves; ++h)
+                        mma_tc(tmem + (kHalves * db + h) * R, mn_major(x + h * 16384 + kk * 2048, 8192), mn_major(g + t * kPart + kk * 2048, 8192), idesc,
+                               !(s % kOuterFlush == 0 && kk == 0 && t == 2));
+            commit_tc(bar_empty + 8 * (s % S));
+            if (s % kOuterFlush == kOuterFlush - 1 || s + 1 == n_steps) commit_tc(bar_d + 8 * db);
+        }
+    } else if (warp < kOuterOut / 32) {
+        // column 32 (warp % 4) + lane of a half; warps 4 to 7: the other half, or the other ranks
+        const uint32_t chains = (n_steps + kOuterFlush - 1) / kOuterFlush, up = warp >> 2;
+        const uint32_t h = kHalves == 2 ? up : 0, j0 = kHalves == 2 ? 0 : up * kRanks;
+        float sum[kRanks] = {};
+        for (uint32_t c = 0; c < chains; ++c) {
+            if (!bar_wait(bar_d + 8 * (c & 1u), (c / 2) & 1u, abort_flag)) break;
+            fence_after();
+#pragma unroll
+            for (uint32_t j = 0; j < kRanks; j += 16) {
+                uint32_t d[16];
+                tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + (kHalves * (c & 1u) + h) * R + j0 + j);
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
+            }
+            fence_before();
+            bar_arrive(bar_free + 8 * (c & 1u));
+        }
+        // every stage has been read: their place holds the sums from here on
+#pragma unroll
+        for (uint32_t j = 0; j < kRanks; j += 4)
+            *reinterpret_cast<float4*>(red + (h * 128 + (warp & 3u) * 32 + lane) * (R + 4) + j0 + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+    }
+    fence_before();
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const uint32_t rm = p.b.rank_max, cols = min(128u, job.width - c0);
-    float* out = job.out + uint64_t(a) * rm * job.width;
-    if (!job.transposed) { // rows j = part, part + split, ..: 128 columns, one a thread
-        for (uint32_t i = tid; i < (rm - part + p.split - 1) / p.split * 128; i += kTiledThreads) {
-            const uint32_t j = part + (i >> 7) * p.split, c = i & 127u;
-            if (c >= cols) continue;
-            float v = 0.f;
-            for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[j * 132 + c];
-            float* d = out + uint64_t(j) * job.width + c0 + c;
-            *d = p.accumulate ? *d + v : v;
-        }
-    } else { // columns c = 128 part / split ..: rm ranks of each, contiguous
-        const uint32_t each = 128 / p.split;
-        for (uint32_t i = tid; i < each * rm; i += kTiledThreads) {
-            const uint32_t c = part * each + i / rm, j = i % rm;
-            if (c >= cols) continue;
-            float v = 0.f;
-            for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[j * 132 + c];
-            float* d = out + uint64_t(c0 + c) * rm + j;
-            *d = p.accumulate ? *d + v : v;
-        }
+    // columns part * 256 / split ..: the parts of all CTAs added up
+    const uint32_t each = kOuterCols / p.split;
+    for (uint32_t i = tid; i < each * rm; i += kOuterThreads) {
+        // neighbouring threads write neighbouring numbers: columns of a rank (dA) or ranks of a column (dB)
+        const uint32_t c = part * each + (job.transposed ? i / rm : i % each), j = job.transposed ? i % rm : i / each;
+        if (c >= cols) continue;
+        float v = 0.f;
+        for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[c * (R + 4) + j];
+        float* d = job.transposed ? out + uint64_t(c0 + c) * rm + j : out + uint64_t(j) * job.width + c0 + c;
+        *d = p.accumulate ? *d + v : v;
     }
     cluster.sync(); // the peers may still read this CTA's sums
+    if (tid == 0 && s_abort && p.b.err) atomicOr(p.b.err, 2u);
+    if (warp == kIssueWarp) {
+        __syncwarp();
+        tmem_free(tmem, kTmem);
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -815,7 +897,7 @@ struct Gpu {
     int dev = 0, sms = 148;
     cudaStream_t s = nullptr;
 };
-template <auto FN, uint32_t THREADS = kTiledThreads, typename Params>
+template <auto FN, uint32_t THREADS, typename Params>
 bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, const Params& p) {
     cudaError_t e = allow_smem<FN>(gpu.dev, smem);
     if (e != cudaSuccess) return cuda_status(e);
@@ -839,10 +921,11 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
 // Whether a batch goes through the decoding kernel.
 bool few_tokens(uint32_t tokens, uint32_t n) { return tokens <= 128 || (tokens <= kFewTokens && tokens <= 4 * n); }
 
-// CTAs of a cluster that share a sum: the least power of two up to 8 that fills the GPU
-uint32_t split_for(uint64_t ctas, uint32_t steps, int sms) {
+// CTAs of a cluster that share a sum: the most of 1, 2, 4, 8 that leave each CTA 4 steps and fit into
+// `slots` CTAs at a time.
+uint32_t split_for(uint64_t ctas, uint32_t steps, uint64_t slots) {
     uint32_t c = 1;
-    while (c < 8 && ctas * c < 2u * static_cast<uint32_t>(sms) && steps >= 4 * c) c *= 2;
+    while (c < 8 && ctas * c * 2 <= slots && steps >= 8 * c) c *= 2;
     return c;
 }
 
@@ -851,13 +934,13 @@ bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, const Gpu& g
     uint32_t steps = ~0u;
     for (uint32_t k = 0; k < jobs; ++k) steps = std::min(steps, (p.job[k].width + 63) / 64);
     const uint32_t cap = tile_cap(p.b.tokens, p.b.n, kTile);
-    p.split = split_for(uint64_t(std::min(cap, (p.b.tokens + kTile - 1) / kTile)) * jobs, steps, gpu.sms);
+    p.split = split_for(uint64_t(std::min(cap, (p.b.tokens + kTile - 1) / kTile)) * jobs, steps, uint64_t(gpu.sms) * (R <= 64 ? 2 : 1));
     const dim3 grid(cap * p.split, jobs);
     switch (R) {
-    case 16: return launch<lora_shrink_kernel<16, WT>>(grid, shrink_smem<16, WT>(), p.split, gpu, p);
-    case 32: return launch<lora_shrink_kernel<32, WT>>(grid, shrink_smem<32, WT>(), p.split, gpu, p);
-    case 64: return launch<lora_shrink_kernel<64, WT>>(grid, shrink_smem<64, WT>(), p.split, gpu, p);
-    default: return launch<lora_shrink_kernel<128, WT>>(grid, shrink_smem<128, WT>(), p.split, gpu, p);
+    case 16: return launch<lora_shrink_kernel<16, WT>, shrink_threads<16>>(grid, shrink_smem<16, WT>(), p.split, gpu, p);
+    case 32: return launch<lora_shrink_kernel<32, WT>, shrink_threads<32>>(grid, shrink_smem<32, WT>(), p.split, gpu, p);
+    case 64: return launch<lora_shrink_kernel<64, WT>, shrink_threads<64>>(grid, shrink_smem<64, WT>(), p.split, gpu, p);
+    default: return launch<lora_shrink_kernel<128, WT>, shrink_threads<128>>(grid, shrink_smem<128, WT>(), p.split, gpu, p);
     }
 }
 template <bool WT, bool BF16>
@@ -889,15 +972,21 @@ bs_status launch_expand(const ExpandParams& all, uint32_t jobs, uint32_t R, cons
     return BS_OK;
 }
 bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
+    const uint32_t cols = R > 64 ? outer_cols<128> : outer_cols<64>;
     uint32_t blocks = 1;
-    for (uint32_t k = 0; k < jobs; ++k) blocks = std::max(blocks, (p.job[k].width + 127) / 128);
-    p.split = split_for(uint64_t(blocks) * jobs * p.b.n, p.b.tokens / p.b.n / kOuterTok, gpu.sms);
+    uint64_t ctas = 0;
+    for (uint32_t k = 0; k < jobs; ++k) {
+        blocks = std::max(blocks, (p.job[k].width + cols - 1) / cols);
+        ctas += (p.job[k].width + cols - 1) / cols;
+    }
+    // two to four waves: adapters have uneven numbers of tokens
+    p.split = split_for(ctas * p.b.n, p.b.tokens / p.b.n / kOuterTok, 4ull * gpu.sms);
     const dim3 grid(blocks * p.split, p.b.n, jobs);
     switch (R) {
-    case 16: return launch<lora_outer_kernel<16>>(grid, outer_smem<16>(), p.split, gpu, p);
-    case 32: return launch<lora_outer_kernel<32>>(grid, outer_smem<32>(), p.split, gpu, p);
-    case 64: return launch<lora_outer_kernel<64>>(grid, outer_smem<64>(), p.split, gpu, p);
-    default: return launch<lora_outer_kernel<128>>(grid, outer_smem<128>(), p.split, gpu, p);
+    case 16: return launch<lora_outer_kernel<16>, kOuterThreads>(grid, outer_smem<16>(), p.split, gpu, p);
+    case 32: return launch<lora_outer_kernel<32>, kOuterThreads>(grid, outer_smem<32>(), p.split, gpu, p);
+    case 64: return launch<lora_outer_kernel<64>, kOuterThreads>(grid, outer_smem<64>(), p.split, gpu, p);
+    default: return launch<lora_outer_kernel<128>, kOuterThreads>(grid, outer_smem<128>(), p.split, gpu, p);
     }
 }
 
