@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     constexpr uint32_t kTmem = R <= 16 ? 32 : 2 * R, S = kShrinkStages, kShrinkOut = shrink_out<R>, kRanks = R > 64 ? 64 : R;
+    after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     __shared__ int s_abort;
     constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
     constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
+    after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t tiles = p.b.plan[1];
@@ -690,25 +692,31 @@ struct OuterParams {
     OuterJob job[2 * kMaxItems];
 };
 // Threads that add up, that load; a warp more issues. A stage holds 64 tokens: their columns (MN-major)
-// and the three parts of their ranks (MN-major). 256 columns a CTA, a thread each; rank 128: 128
-// columns, two threads each, 64 ranks a thread.
-constexpr uint32_t kOuterOut = 256, kOuterLoad = 128, kOuterThreads = kOuterOut + kOuterLoad + 32, kOuterTok = 64, kOuterStages = 3;
+// and the three parts of their ranks side by side (MN-major). Up to rank 32: 128 columns a CTA, a
+// thread each, and 2 or 3 CTAs an SM, since batches of few tokens per adapter are all latency; rank
+// 64: 256 columns; rank 128: 128 columns, two threads each, 64 ranks a thread.
 template <int R>
-constexpr uint32_t outer_cols = R > 64 ? 128 : 256;
+constexpr uint32_t outer_out = R > 32 ? 256 : 128;
 template <int R>
-__host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 3 * 8192 * atoms_of<R>; }
+constexpr uint32_t outer_cols = R == 64 ? 256 : 128;
+constexpr uint32_t kOuterLoad = 128, kOuterTok = 64, kOuterStages = 3;
+template <int R>
+constexpr uint32_t outer_threads = outer_out<R> + kOuterLoad + 32;
+template <int R>
+__host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 8192 * ((3 * R + 63) / 64); }
 template <int R>
 constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(kOuterStages * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
 constexpr uint32_t kOuterFlush = 2; // stages whose sums stay in tensor memory: chains of 24 matrix instructions
 
 template <int R>
-__global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
+__global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kTmem = 2 * kHalves * R; // 64 .. 256
-    constexpr uint32_t kStage = outer_stage<R>(), kPart = 8192 * atoms_of<R>, kRanks = R > 64 ? 64 : R;
+    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kTmem = 2 * kHalves * R; // 32 .. 256
+    constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t part = blockIdx.x % p.split, c0 = blockIdx.x / p.split * kOuterCols, a = blockIdx.y;
     const OuterJob& job = p.job[blockIdx.z];
@@ -764,28 +772,35 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const __gr
             fence_operands();
             bar_arrive(bar_full + 8 * (s % S));
         };
-        uint32_t s = 0;
-        for (; s < n_steps; ++s) {
-            const uint32_t first = t_begin + (s_begin + s) * kOuterTok, left = t_end - first;
-            uint64_t row[kRows];
+        uint32_t s = 0, tok[kRows]; // of the step's tokens; the next step's are fetched a step ahead
+        auto fetch = [&](uint32_t step) {
+            const uint32_t first = t_begin + (s_begin + step) * kOuterTok;
 #pragma unroll
             for (uint32_t i = 0; i < kRows; ++i) {
-                const uint32_t r = r0 + kEvery * i;
-                row[i] = r < left ? p.b.plan[o.perm + first + r] * job.stride : ~0ull;
+                const uint32_t at = first + r0 + kEvery * i;
+                tok[i] = step < n_steps && at < t_end ? p.b.plan[o.perm + at] : ~0u;
             }
+        };
+        fetch(0);
+        for (; s < n_steps; ++s) {
+            const uint32_t first = t_begin + (s_begin + s) * kOuterTok, left = t_end - first;
+            uint32_t now[kRows];
+#pragma unroll
+            for (uint32_t i = 0; i < kRows; ++i) now[i] = tok[i];
+            fetch(s + 1);
             if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
             const uint32_t sb = s0 + s % S * kStage, sg = sb + kOuterCols * 128;
 #pragma unroll
             for (uint32_t i = 0; i < kRows; ++i) {
-                const bool on = row[i] != ~0ull;
-                cp_async16_if(in, sb + (piece >> 3) * 8192 + sw128(r0 + kEvery * i, piece & 7u), on ? job.src + row[i] + c0 + 8 * piece : job.src, on ? 16u : 0u);
+                const bool on = now[i] != ~0u;
+                cp_async16_if(in, sb + (piece >> 3) * 8192 + sw128(r0 + kEvery * i, piece & 7u), on ? job.src + now[i] * job.stride + c0 + 8 * piece : job.src, on ? 16u : 0u);
             }
 #pragma unroll
             for (uint32_t t = 0; t < 3; ++t)
 #pragma unroll
                 for (uint32_t c = t0; c < kOuterTok * kC; c += kOuterLoad) {
-                    const uint32_t r = c / kC, j = c % kC;
-                    cp_async16(sg + t * kPart + (j >> 3) * 8192 + sw128(r, j & 7u),
+                    const uint32_t r = c / kC, j = c % kC, q = t * kC + j;
+                    cp_async16(sg + (q >> 3) * 8192 + sw128(r, q & 7u),
                                job.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < left ? first + r : t_begin) * R + 8 * j, r < left ? 16u : 0u);
                 }
             cp_async_commit();
@@ -810,14 +825,14 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const __gr
                 for (int t = 2; t >= 0; --t) // small parts first
 #pragma unroll
                     for (uint32_t h = 0; h < kHalves; ++h)
-                        mma_tc(tmem + (kHalves * db + h) * R, mn_major(x + h * 16384 + kk * 2048, 8192), mn_major(g + t * kPart + kk * 2048, 8192), idesc,
+                        mma_tc(tmem + (kHalves * db + h) * R, mn_major(x + h * 16384 + kk * 2048, 8192), mn_major(g + t * R / 64 * 8192 + t * R % 64 * 2 + kk * 2048, 8192), idesc,
                                !(s % kOuterFlush == 0 && kk == 0 && t == 2));
             commit_tc(bar_empty + 8 * (s % S));
             if (s % kOuterFlush == kOuterFlush - 1 || s + 1 == n_steps) commit_tc(bar_d + 8 * db);
         }
     } else if (warp < kOuterOut / 32) {
         // column 32 (warp % 4) + lane of a half; warps 4 to 7: the other half, or the other ranks
-        const uint32_t chains = (n_steps + kOuterFlush - 1) / kOuterFlush, up = warp >> 2;
+        const uint32_t chains = (n_steps + kOuterFlush - 1) / kOuterFlush, up = warp >> 2; // up: 0 with 128 threads
         const uint32_t h = kHalves == 2 ? up : 0, j0 = kHalves == 2 ? 0 : up * kRanks;
         float sum[kRanks] = {};
         for (uint32_t c = 0; c < chains; ++c) {
@@ -841,16 +856,28 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const __gr
     fence_before();
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    // columns part * 256 / split ..: the parts of all CTAs added up
-    const uint32_t each = kOuterCols / p.split;
-    for (uint32_t i = tid; i < each * rm; i += kOuterThreads) {
-        // neighbouring threads write neighbouring numbers: columns of a rank (dA) or ranks of a column (dB)
-        const uint32_t c = part * each + (job.transposed ? i / rm : i % each), j = job.transposed ? i % rm : i / each;
+    // columns part * cols / split ..: the parts of all CTAs added up, 4 ranks of a column at a time
+    const uint32_t each = kOuterCols / p.split, quads = rm / 4;
+    for (uint32_t i = tid; i < each * quads; i += kOuterThreads) {
+        // neighbouring threads have neighbouring columns (dA), or neighbouring ranks of a column (dB)
+        const uint32_t c = part * each + (job.transposed ? i / quads : i % each), j = 4 * (job.transposed ? i % quads : i / each);
         if (c >= cols) continue;
-        float v = 0.f;
-        for (uint32_t q = 0; q < p.split; ++q) v += cluster.map_shared_rank(red, q)[c * (R + 4) + j];
-        float* d = job.transposed ? out + uint64_t(c0 + c) * rm + j : out + uint64_t(j) * job.width + c0 + c;
-        *d = p.accumulate ? *d + v : v;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (uint32_t q = 0; q < p.split; ++q) {
+            const float4 u = *reinterpret_cast<const float4*>(cluster.map_shared_rank(red, q) + c * (R + 4) + j);
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        if (job.transposed) {
+            float4* d = reinterpret_cast<float4*>(out + uint64_t(c0 + c) * rm + j);
+            if (p.accumulate) { const float4 u = *d; v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w); }
+            *d = v;
+        } else {
+            float* d = out + uint64_t(j) * job.width + c0 + c;
+            const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q, d += job.width) *d = p.accumulate ? *d + w[q] : w[q];
+        }
     }
     cluster.sync(); // the peers may still read this CTA's sums
     if (tid == 0 && s_abort && p.b.err) atomicOr(p.b.err, 2u);
@@ -906,13 +933,15 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = gpu.s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see after_kernel_before
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, FN, p);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
@@ -972,21 +1001,20 @@ bs_status launch_expand(const ExpandParams& all, uint32_t jobs, uint32_t R, cons
     return BS_OK;
 }
 bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
-    const uint32_t cols = R > 64 ? outer_cols<128> : outer_cols<64>;
+    const uint32_t cols = R == 64 ? outer_cols<64> : outer_cols<128>;
     uint32_t blocks = 1;
     uint64_t ctas = 0;
     for (uint32_t k = 0; k < jobs; ++k) {
         blocks = std::max(blocks, (p.job[k].width + cols - 1) / cols);
         ctas += (p.job[k].width + cols - 1) / cols;
     }
-    // two to four waves: adapters have uneven numbers of tokens
-    p.split = split_for(ctas * p.b.n, p.b.tokens / p.b.n / kOuterTok, 4ull * gpu.sms);
+    p.split = split_for(ctas * p.b.n, p.b.tokens / p.b.n / kOuterTok, 2ull * gpu.sms);
     const dim3 grid(blocks * p.split, p.b.n, jobs);
     switch (R) {
-    case 16: return launch<lora_outer_kernel<16>, kOuterThreads>(grid, outer_smem<16>(), p.split, gpu, p);
-    case 32: return launch<lora_outer_kernel<32>, kOuterThreads>(grid, outer_smem<32>(), p.split, gpu, p);
-    case 64: return launch<lora_outer_kernel<64>, kOuterThreads>(grid, outer_smem<64>(), p.split, gpu, p);
-    default: return launch<lora_outer_kernel<128>, kOuterThreads>(grid, outer_smem<128>(), p.split, gpu, p);
+    case 16: return launch<lora_outer_kernel<16>, outer_threads<16>>(grid, outer_smem<16>(), p.split, gpu, p);
+    case 32: return launch<lora_outer_kernel<32>, outer_threads<32>>(grid, outer_smem<32>(), p.split, gpu, p);
+    case 64: return launch<lora_outer_kernel<64>, outer_threads<64>>(grid, outer_smem<64>(), p.split, gpu, p);
+    default: return launch<lora_outer_kernel<128>, outer_threads<128>>(grid, outer_smem<128>(), p.split, gpu, p);
     }
 }
 

@@ -64,6 +64,14 @@ __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
     return r < 0 ? 0u : min(static_cast<uint32_t>(r), b.rank_max);
 }
 
+// Programmatic dependent launch: the next kernel of the stream may be scheduled once every CTA of this
+// one has started, and takes over the SMs that it leaves; this one goes on when the kernels before it
+// have completed and what they wrote is visible. Nothing global is read or written before.
+__device__ __forceinline__ void after_kernel_before() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The decoding kernel (bs_lora_few.cu): a cluster takes up to kFew tokens of one adapter through
 // both products.
 constexpr uint32_t kFewCluster = 8, kFewThreads = 256;
