@@ -110,6 +110,34 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
         __syncthreads();
     }
     const PlanAt o = plan_at(tokens, n);
+    // the adapters by falling number of tokens, in classes of its upper three bits (order inside a class
+    // is as it comes: it only decides which CTAs start first)
+    constexpr uint32_t kClasses = 8 * 21;
+    __shared__ uint32_t s_class[kClasses];
+    auto class_of = [&](uint32_t a) {
+        const uint32_t c = (a + 1 < nb ? first[a + 1] : s_carry[0]) - first[a], lg = c ? 31u - __clz(c) : 0u;
+        return kClasses - 1 - (c ? lg * 8 + ((lg >= 3 ? c >> (lg - 3) : c << (3 - lg)) & 7u) : 0u);
+    };
+    for (uint32_t i = tid; i < kClasses; i += blockDim.x) s_class[i] = 0;
+    __syncthreads();
+    for (uint32_t a = tid; a < n; a += blockDim.x) atomicAdd(&s_class[class_of(a)], 1u);
+    __syncthreads();
+    if (warp == 0) { // classes to first places
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < kClasses; i += 32) {
+            const uint32_t c = i + lane < kClasses ? s_class[i + lane] : 0;
+            uint32_t u = c;
+#pragma unroll
+            for (uint32_t d = 1; d < 32; d <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, u, d);
+                if (lane >= d) u += up;
+            }
+            if (i + lane < kClasses) s_class[i + lane] = before + u - c;
+            before += __shfl_sync(0xFFFFFFFFu, u, 31);
+        }
+    }
+    __syncthreads();
+    for (uint32_t a = tid; a < n; a += blockDim.x) plan[o.order + atomicAdd(&s_class[class_of(a)], 1u)] = a;
     if (tid == 0) {
         first[nb] = s_carry[0];
         t128[nb] = s_carry[1];
@@ -706,22 +734,34 @@ template <int R>
 __host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 8192 * ((3 * R + 63) / 64); }
 template <int R>
 constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(kOuterStages * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
-constexpr uint32_t kOuterFlush = 2; // stages whose sums stay in tensor memory: chains of 24 matrix instructions
+constexpr uint32_t kOuterFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
+// Sums in tensor memory: 128 columns x the 3 parts' ranks, beside each other (one matrix instruction
+// reads the columns once for all parts; one for each part read them three times, and 8192 tokens at
+// rank 64 took 135 us, bound by shared memory, against OUTER_US). Up to rank 32 two of them take turns;
+// rank 64 has one for each 128 of its 256 columns, which are added up two stages apart, so that one
+// half's matrix instructions go on meanwhile; rank 128 has one.
+template <int R>
+constexpr uint32_t outer_accs = R > 64 ? 1 : 2;
 
 template <int R>
 __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kTmem = 2 * kHalves * R; // 32 .. 256
+    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kAccs = outer_accs<R>, kWide = 3 * R;
+    constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512; // at least kAccs * kWide, a power of two
     constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    const uint32_t part = blockIdx.x % p.split, c0 = blockIdx.x / p.split * kOuterCols, a = blockIdx.y;
-    const OuterJob& job = p.job[blockIdx.z];
-    if (c0 >= job.width) return; // the whole cluster
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    // all jobs' blocks of columns for the adapter with the most tokens first, then the next: the last
+    // CTAs to start are the shortest
+    const uint32_t part = blockIdx.x % p.split, a = p.b.plan[o.order + blockIdx.y];
+    uint32_t block = blockIdx.x / p.split, k = 0;
+    while (block >= (p.job[k].width + kOuterCols - 1) / kOuterCols) block -= (p.job[k++].width + kOuterCols - 1) / kOuterCols;
+    const OuterJob& job = p.job[k];
+    const uint32_t c0 = block * kOuterCols;
     const uint32_t t_begin = p.b.plan[o.begin + a], t_end = p.b.plan[o.begin + a + 1];
     const uint32_t rm = p.b.rank_max, cols = min(kOuterCols, job.width - c0);
     float* out = job.out + uint64_t(a) * rm * job.width;
@@ -748,7 +788,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
         }
         for (uint32_t i = 0; i < 2; ++i) {
             bar_init(bar_d + 8 * i, 1);
-            bar_init(bar_free + 8 * i, kOuterOut);
+            bar_init(bar_free + 8 * i, R > 64 ? 256 : 128);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -812,43 +852,54 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
         cp_async_wait<0>();
         if (s == n_steps && n_steps) landed(n_steps - 1);
     } else if (tid == kIssueWarp * 32) {
-        const uint32_t idesc = idesc_of(R, true, true);
+        constexpr uint32_t kN = kWide > 192 ? 192 : kWide;
+        const uint32_t idesc = idesc_of(kN, true, true);
         for (uint32_t s = 0; s < n_steps; ++s) {
-            const uint32_t chain = s / kOuterFlush, db = chain & 1u;
-            if (s % kOuterFlush == 0 && chain >= 2 && !bar_wait(bar_free + 8 * db, (chain / 2 - 1) & 1u, abort_flag)) break;
             if (!bar_wait(bar_full + 8 * (s % S), (s / S) & 1u, abort_flag)) break;
             fence_after();
             const uint32_t x = s0 + s % S * kStage, g = x + kOuterCols * 128;
+            bool ok = true;
 #pragma unroll
-            for (uint32_t kk = 0; kk < kOuterTok / 16; ++kk)
+            for (uint32_t i = 0; i < kHalves; ++i) {
+                // the half that begins a chain goes second: its sums may still be being added up
+                const uint32_t h = kHalves == 2 && s % kOuterFlush == 0 ? 1 - i : i, at = s + 2 * h;
+                const uint32_t chain = at / kOuterFlush, acc = kHalves == 2 ? h : chain % kAccs, use = kHalves == 2 ? chain : chain / kAccs;
+                const bool begins = s == 0 || at % kOuterFlush == 0;
+                if (begins && use >= 1 && !bar_wait(bar_free + 8 * acc, (use - 1) & 1u, abort_flag)) { ok = false; break; }
 #pragma unroll
-                for (int t = 2; t >= 0; --t) // small parts first
+                for (uint32_t kk = 0; kk < kOuterTok / 16; ++kk)
 #pragma unroll
-                    for (uint32_t h = 0; h < kHalves; ++h)
-                        mma_tc(tmem + (kHalves * db + h) * R, mn_major(x + h * 16384 + kk * 2048, 8192), mn_major(g + t * R / 64 * 8192 + t * R % 64 * 2 + kk * 2048, 8192), idesc,
-                               !(s % kOuterFlush == 0 && kk == 0 && t == 2));
+                    for (uint32_t n = 0; n < kWide / kN; ++n)
+                        mma_tc(tmem + acc * kWide + n * kN, mn_major(x + h * 16384 + kk * 2048, 8192), mn_major(g + n * (kN / 64) * 8192 + kk * 2048, 8192),
+                               idesc, !(begins && kk == 0));
+                if (at % kOuterFlush == kOuterFlush - 1 || s + 1 == n_steps) commit_tc(bar_d + 8 * acc);
+            }
+            if (!ok) break;
             commit_tc(bar_empty + 8 * (s % S));
-            if (s % kOuterFlush == kOuterFlush - 1 || s + 1 == n_steps) commit_tc(bar_d + 8 * db);
         }
     } else if (warp < kOuterOut / 32) {
         // column 32 (warp % 4) + lane of a half; warps 4 to 7: the other half, or the other ranks
-        const uint32_t chains = (n_steps + kOuterFlush - 1) / kOuterFlush, up = warp >> 2; // up: 0 with 128 threads
-        const uint32_t h = kHalves == 2 ? up : 0, j0 = kHalves == 2 ? 0 : up * kRanks;
+        const uint32_t up = warp >> 2, h = kHalves == 2 ? up : 0, j0 = R > 64 ? up * kRanks : 0; // up: 0 with 128 threads
+        const uint32_t chains = n_steps ? (n_steps - 1 + 2 * h) / kOuterFlush + 1 : 0;
         float sum[kRanks] = {};
         for (uint32_t c = 0; c < chains; ++c) {
-            if (!bar_wait(bar_d + 8 * (c & 1u), (c / 2) & 1u, abort_flag)) break;
+            const uint32_t acc = kHalves == 2 ? h : c % kAccs, use = kHalves == 2 ? c : c / kAccs;
+            if (!bar_wait(bar_d + 8 * acc, use & 1u, abort_flag)) break;
             fence_after();
 #pragma unroll
-            for (uint32_t j = 0; j < kRanks; j += 16) {
-                uint32_t d[16];
-                tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + (kHalves * (c & 1u) + h) * R + j0 + j);
+            for (uint32_t j = 0; j < kRanks; j += 16)
 #pragma unroll
-                for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
-            }
+                for (int part = 2; part >= 0; --part) { // small parts first
+                    uint32_t d[16];
+                    tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + acc * kWide + part * R + j0 + j);
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
+                }
             fence_before();
-            bar_arrive(bar_free + 8 * (c & 1u));
+            bar_arrive(bar_free + 8 * acc);
         }
-        // every stage has been read: their place holds the sums from here on
+        // once all of their matrix instructions are done, the stages' place holds the sums
+        asm volatile("bar.sync 1, %0;" ::"n"(kOuterOut) : "memory");
 #pragma unroll
         for (uint32_t j = 0; j < kRanks; j += 4)
             *reinterpret_cast<float4*>(red + (h * 128 + (warp & 3u) * 32 + lane) * (R + 4) + j0 + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
@@ -1002,14 +1053,10 @@ bs_status launch_expand(const ExpandParams& all, uint32_t jobs, uint32_t R, cons
 }
 bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     const uint32_t cols = R == 64 ? outer_cols<64> : outer_cols<128>;
-    uint32_t blocks = 1;
-    uint64_t ctas = 0;
-    for (uint32_t k = 0; k < jobs; ++k) {
-        blocks = std::max(blocks, (p.job[k].width + cols - 1) / cols);
-        ctas += (p.job[k].width + cols - 1) / cols;
-    }
-    p.split = split_for(ctas * p.b.n, p.b.tokens / p.b.n / kOuterTok, 2ull * gpu.sms);
-    const dim3 grid(blocks * p.split, p.b.n, jobs);
+    uint32_t ctas = 0;
+    for (uint32_t k = 0; k < jobs; ++k) ctas += (p.job[k].width + cols - 1) / cols;
+    p.split = split_for(uint64_t(ctas) * p.b.n, p.b.tokens / p.b.n / kOuterTok, 2ull * gpu.sms);
+    const dim3 grid(ctas * p.split, p.b.n);
     switch (R) {
     case 16: return launch<lora_outer_kernel<16>, outer_threads<16>>(grid, outer_smem<16>(), p.split, gpu, p);
     case 32: return launch<lora_outer_kernel<32>, outer_threads<32>>(grid, outer_smem<32>(), p.split, gpu, p);

@@ -24,6 +24,7 @@ constexpr int kMaxItems = 16;     // projections of one launch
 //   [0] tiles of kTile tokens that have an adapter, [1] all tiles of kTile (those without an
 //   adapter follow), [2] and [3] the same for kFew (0 above kFewTokens), [4] tokens, [5] adapters
 //   begin[n_adapters + 2]: the first place of each bucket, then the end
+//   order[n_adapters]: the adapters, those with the most tokens first (about)
 //   perm[tokens]: the token at each place
 //   tiles: (bucket, first place, tokens, 0) each
 //   tiles of kFew: the same, and the tokens themselves
@@ -31,7 +32,7 @@ struct FewTile {
     uint32_t bucket, first, count, pad, token[kFew]; // token: ~0 past the count
 };
 struct PlanAt {
-    uint64_t begin, perm, tiles, few, words;
+    uint64_t begin, order, perm, tiles, few, words;
 };
 __host__ __device__ inline uint32_t tile_cap(uint32_t tokens, uint32_t n, uint32_t size) {
     const uint32_t most = tokens / size + n + 1; // every bucket ends in a part-filled tile
@@ -41,7 +42,8 @@ __host__ __device__ inline PlanAt plan_at(uint32_t tokens, uint32_t n) {
     PlanAt o;
     auto up4 = [](uint64_t v) { return (v + 3) & ~uint64_t(3); };
     o.begin = 16;
-    o.perm = o.begin + up4(n + 2);
+    o.order = o.begin + up4(n + 2);
+    o.perm = o.order + up4(n);
     o.tiles = o.perm + up4(tokens);
     o.few = o.tiles + 4ull * tile_cap(tokens, n, kTile);
     o.words = o.few + (tokens <= kFewTokens ? sizeof(FewTile) / 4 * tile_cap(tokens, n, kFew) : 0);

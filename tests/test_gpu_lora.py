@@ -235,6 +235,10 @@ def test_plan_groups_in_order(tokens, n):
     bucket = np.where(idx < 0, n, idx)
     assert np.array_equal(begin, np.concatenate([[0], np.cumsum(np.bincount(bucket, minlength=n + 1))]))
     at = 16 + up4(n + 2)
+    order, count = w[at:at + n], np.bincount(bucket, minlength=n + 1)[:n]
+    assert np.array_equal(np.sort(order), np.arange(n))  # every adapter once, the ones with most tokens first:
+    assert np.all(count[order][1:] * 8 <= count[order][:-1] * 9 + 8)  # none after one an eighth smaller
+    at += up4(n)
     assert np.array_equal(w[at:at + tokens], np.argsort(bucket, kind="stable"))
     assert int(plan.err) == 0
     for size, count, start in ((128, w[:2], at + up4(tokens)), (8, w[2:4], at + up4(tokens) + 4 * min(tokens, tokens // 128 + n + 1))):
