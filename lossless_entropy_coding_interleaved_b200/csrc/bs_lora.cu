@@ -274,12 +274,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
             row[i] = r < count ? p.b.plan[o.perm + first + r] * job.stride : ~0ull;
         }
         const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
-        auto landed = [&](uint32_t s) {
-            fence_operands();
-            bar_arrive(bar_full + 8 * (s % S));
-        };
-        uint32_t s = 0;
-        for (; s < n_steps; ++s) {
+        for (uint32_t s = 0; s < n_steps; ++s) {
             if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
             const uint32_t k = (k_begin + s) * 64, sb = s0 + s % S * kStage, sw = sb + 16384, kx = k + 8 * chunk;
 #pragma unroll
@@ -301,21 +296,16 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
                     cp_async16(sw + (j >> 3) * 8192 + sw128(kr, j & 7u), bytes ? w + uint64_t(k + kr) * p.b.rank_max + 8 * j : job.w, bytes);
                 }
             }
-            cp_async_commit();
-            if (s >= 2) { // three stages under way, the oldest has landed
-                cp_async_wait<2>();
-                landed(s - 2);
-            }
+            bar_arrive_copies(bar_full + 8 * (s % S));
         }
         cp_async_wait<0>();
-        if (s == n_steps)
-            for (uint32_t l = n_steps > 2 ? n_steps - 2 : 0; l < n_steps; ++l) landed(l);
     } else if (tid == kIssueWarp * 32) {
         const uint32_t idesc = idesc_of(R, false, WT);
         for (uint32_t s = 0; s < n_steps; ++s) {
             const uint32_t chain = s / kFlush, db = chain & 1u;
             if (s % kFlush == 0 && chain >= 2 && !bar_wait(bar_free + 8 * db, (chain / 2 - 1) & 1u, abort_flag)) break;
             if (!bar_wait(bar_full + 8 * (s % S), (s / S) & 1u, abort_flag)) break;
+            fence_operands(); // the copies, before the tensor cores read them
             fence_after();
             const uint32_t x = s0 + s % S * kStage, w = x + 16384;
 #pragma unroll
@@ -509,16 +499,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         const uint32_t t0 = tid - kExpandOut, piece = t0 & 15u;
         constexpr uint32_t kC = R / 8;
         uint4 tl = make_uint4(0, 0, 0, 0);
-        uint32_t rank = 0, turn = 0, step = 0, pending = ~0u; // pending: the weights' buffer that is being filled
+        uint32_t rank = 0, turn = 0, step = 0;
         uint64_t row[16] = {};
         bool fresh = true, parts_in = false, ok = true; // another tile; the parts in place are those of all sources
         ExpandAt at = start;
-        auto filled = [&]() { // all but the copies queued last have landed
-            if (pending == ~0u) return;
-            fence_operands();
-            bar_arrive(bar_full + 8 * pending);
-            pending = ~0u;
-        };
         for (uint32_t u = 0; u < n_units && ok; ++u) {
             const ExpandJob& job = p.job[at.job];
             if (fresh) {
@@ -534,13 +518,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             const uint32_t n0 = at.block * kCols, N = job.width, count = tl.z, sources = rank ? job.n_src : 0u;
             if (!left_out(job, rank)) {
                 const uint32_t buf = turn % kBufs, n = n0 + piece * (16 / es);
-                // The wait below is for the turn kBufs (2 or more) before this one. A turn with weights tells
-                // of those of the turn before it, so that one is never held up by this thread; a turn
-                // without any has to tell here.
-                if (sources == 0) {
-                    cp_async_wait<0>();
-                    filled();
-                }
                 if (turn >= kBufs && !bar_wait(bar_free + 8 * buf, (turn / kBufs - 1) & 1u, abort_flag)) break;
                 if (job.base && n < N) {
                     const uint32_t dst = sRow + (buf * kTile + (t0 >> 4)) * kRowPitch + 16 * piece;
@@ -548,18 +525,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                     for (uint32_t i = 0; i < 16; ++i)
                         cp_async16_if(row[i] != ~0ull, dst + 8 * i * kRowPitch, job.base + (row[i] + n) * es, 16u);
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_base + 8 * buf) : "memory");
+                bar_arrive_copies(bar_base + 8 * buf);
                 ++turn;
             }
             for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) { // a group of sources at a time
                 const uint32_t wb = step & 1u, sb = sW + wb * expand_w<R, BF16>(), g1 = min(g0 + kGroup, sources);
                 if (step >= 2 && !bar_wait(bar_empty + 8 * wb, (step / 2 - 1) & 1u, abort_flag)) { ok = false; break; }
                 if (!parts_in) { // once what stood there has been read
-                    if (step > 0) {
-                        cp_async_wait<0>();
-                        filled();
-                        if (!bar_wait(bar_empty + 8 * (wb ^ 1u), ((step - 1) / 2) & 1u, abort_flag)) { ok = false; break; }
-                    }
+                    if (step > 0 && !bar_wait(bar_empty + 8 * (wb ^ 1u), ((step - 1) / 2) & 1u, abort_flag)) { ok = false; break; }
                     for (uint32_t g = g0; g < g1; ++g)
 #pragma unroll
                         for (uint32_t t = 0; t < kParts; ++t)
@@ -591,15 +564,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                         }
                     }
                 }
-                cp_async_commit();
-                if (pending != ~0u) cp_async_wait<1>();
-                filled();
-                pending = wb;
+                bar_arrive_copies(bar_full + 8 * wb);
             }
             fresh = next(at);
         }
         cp_async_wait<0>();
-        filled();
     } else if (tid == kIssueWarp * 32) {
         const uint32_t idesc = idesc_of(kCols, false, WT);
         uint32_t rank = 0, turn = 0, step = 0;
@@ -614,6 +583,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) {
                     const uint32_t wb = step & 1u, w = sW + wb * expand_w<R, BF16>();
                     if (!bar_wait(bar_full + 8 * wb, (step / 2) & 1u, abort_flag)) { ok = false; break; }
+                    fence_operands(); // the copies, before the tensor cores read them
                     fence_after();
                     for (uint32_t g = g0; g < min(g0 + kGroup, sources); ++g)
                         for (uint32_t k1 = 0; k1 < kn; ++k1) {
@@ -808,11 +778,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
         const uint32_t t0 = tid - kOuterOut, piece = t0 % kPieces, r0 = t0 / kPieces;
         const bool in = 8 * piece < cols;
         constexpr uint32_t kC = R / 8;
-        auto landed = [&](uint32_t s) {
-            fence_operands();
-            bar_arrive(bar_full + 8 * (s % S));
-        };
-        uint32_t s = 0, tok[kRows]; // of the step's tokens; the next step's are fetched a step ahead
+        uint32_t tok[kRows]; // of the step's tokens; the next step's are fetched a step ahead
         auto fetch = [&](uint32_t step) {
             const uint32_t first = t_begin + (s_begin + step) * kOuterTok;
 #pragma unroll
@@ -822,7 +788,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
             }
         };
         fetch(0);
-        for (; s < n_steps; ++s) {
+        for (uint32_t s = 0; s < n_steps; ++s) {
             const uint32_t first = t_begin + (s_begin + s) * kOuterTok, left = t_end - first;
             uint32_t now[kRows];
 #pragma unroll
@@ -843,19 +809,15 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
                     cp_async16(sg + (q >> 3) * 8192 + sw128(r, q & 7u),
                                job.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < left ? first + r : t_begin) * R + 8 * j, r < left ? 16u : 0u);
                 }
-            cp_async_commit();
-            if (s >= 1) { // two stages under way, the older has landed
-                cp_async_wait<1>();
-                landed(s - 1);
-            }
+            bar_arrive_copies(bar_full + 8 * (s % S));
         }
         cp_async_wait<0>();
-        if (s == n_steps && n_steps) landed(n_steps - 1);
     } else if (tid == kIssueWarp * 32) {
         constexpr uint32_t kN = kWide > 192 ? 192 : kWide;
         const uint32_t idesc = idesc_of(kN, true, true);
         for (uint32_t s = 0; s < n_steps; ++s) {
             if (!bar_wait(bar_full + 8 * (s % S), (s / S) & 1u, abort_flag)) break;
+            fence_operands(); // the copies, before the tensor cores read them
             fence_after();
             const uint32_t x = s0 + s % S * kStage, g = x + kOuterCols * 128;
             bool ok = true;

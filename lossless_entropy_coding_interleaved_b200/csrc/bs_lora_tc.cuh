@@ -42,6 +42,10 @@ __device__ __forceinline__ void bar_init(uint32_t addr, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t addr) {
     asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(addr) : "memory");
 }
+// An arrival that takes effect once all of this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void bar_arrive_copies(uint32_t addr) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(addr) : "memory");
+}
 // Waits for the end of the barrier's phase of this parity. Gives up, sets the CTA's abort flag and
 // returns false after about a second, or soon after another thread has given up.
 __device__ __forceinline__ bool bar_wait(uint32_t addr, uint32_t parity, volatile int* abort_flag) {
