@@ -267,33 +267,35 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     if (warp >= kShrinkOut / 32 && warp < kIssueWarp) {
         // piece t0 % 8 of the rows t0 / 8 + 16 i of x; rows past the tokens stand for nothing
         const uint32_t t0 = tid - kShrinkOut, chunk = t0 & 7u;
-        uint64_t row[8];
+        const uint16_t* row[8];
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {
             const uint32_t r = (t0 >> 3) + 16 * i;
-            row[i] = r < count ? p.b.plan[o.perm + first + r] * job.stride : ~0ull;
+            row[i] = r < count ? job.src + p.b.plan[o.perm + first + r] * job.stride : nullptr;
         }
         const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
         for (uint32_t s = 0; s < n_steps; ++s) {
             if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
             const uint32_t k = (k_begin + s) * 64, sb = s0 + s % S * kStage, sw = sb + 16384, kx = k + 8 * chunk;
+            // rows t0 / 8 + 16 i of x and of A (their swizzle is the same for every i)
+            const uint32_t in = kx < K ? 16u : 0u, dst = sb + sw128(t0 >> 3, chunk);
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i)
-                cp_async16_if(row[i] != ~0ull, sb + sw128((t0 >> 3) + 16 * i, chunk), kx < K ? job.src + row[i] + kx : job.src, kx < K ? 16u : 0u);
+            for (uint32_t i = 0; i < 8; ++i) cp_async16_if(row[i] != nullptr, dst + 2048 * i, in ? row[i] + kx : job.src, in);
             if (!WT) {
 #pragma unroll
-                for (uint32_t c = t0; c < R * 8; c += kShrinkLoad) {
-                    const uint32_t j = c >> 3, kc = k + 8 * (c & 7u);
-                    const bool on = j < rank && kc < K;
-                    cp_async16(sw + sw128(j, c & 7u), on ? w + uint64_t(j) * K + kc : job.w, on ? 16u : 0u);
+                for (uint32_t i = 0; i < (R + 15) / 16; ++i) {
+                    const uint32_t j = (t0 >> 3) + 16 * i;
+                    const uint32_t on = j < rank ? in : 0u;
+                    cp_async16(sw + sw128(t0 >> 3, chunk) + 2048 * i, on ? w + uint64_t(j) * K + kx : job.w, on);
                 }
             } else {
-                constexpr uint32_t kC = R / 8; // pieces of a row
+                constexpr uint32_t kC = R / 8, kEvery = kShrinkLoad / kC; // pieces of a row; piece j of every kEvery-th row
+                const uint32_t j = t0 % kC, take = 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
+                const uint16_t* from = w + uint64_t(k + t0 / kC) * p.b.rank_max + 8 * j;
 #pragma unroll
-                for (uint32_t c = t0; c < 64 * kC; c += kShrinkLoad) {
-                    const uint32_t kr = c / kC, j = c % kC;
-                    const uint32_t bytes = k + kr < K && 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
-                    cp_async16(sw + (j >> 3) * 8192 + sw128(kr, j & 7u), bytes ? w + uint64_t(k + kr) * p.b.rank_max + 8 * j : job.w, bytes);
+                for (uint32_t i = 0; i < 64 / kEvery; ++i) {
+                    const uint32_t on = k + t0 / kC + kEvery * i < K ? take : 0u;
+                    cp_async16(sw + (j >> 3) * 8192 + sw128(t0 / kC + kEvery * i, j & 7u), on ? from + uint64_t(kEvery * i) * p.b.rank_max : job.w, on);
                 }
             }
             bar_arrive_copies(bar_full + 8 * (s % S));
@@ -546,13 +548,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 for (uint32_t g = g0; g < g1; ++g) {
                     const ExpandSrc& src = p.src[job.src + g];
                     const uint16_t* w = src.w + uint64_t(tl.x) * p.b.rank_max * N;
-                    if (!WT) {
+                    if (!WT) { // piece j of the ranks, every kExpandLoad / kC-th column
+                        const uint32_t j = t0 % kC, n = n0 + t0 / kC, at_j = (g - g0) * kC + j;
+                        const uint32_t take = 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u, dst = sb + (at_j >> 3) * (kCols * 128);
+                        const uint16_t* from = take ? w + uint64_t(n) * p.b.rank_max + 8 * j : src.w;
+                        const uint64_t hop = take ? uint64_t(kExpandLoad / kC) * p.b.rank_max : 0;
 #pragma unroll 4
-                        for (uint32_t c = t0; c < kCols * kC; c += kExpandLoad) {
-                            const uint32_t n = c / kC, j = c % kC, at_j = (g - g0) * kC + j;
-                            const uint32_t take = n0 + n < N && 8 * j < rank ? min(rank - 8 * j, 8u) * 2u : 0u;
-                            cp_async16(sb + (at_j >> 3) * (kCols * 128) + sw128(n, at_j & 7u),
-                                       take ? w + uint64_t(n0 + n) * p.b.rank_max + 8 * j : src.w, take);
+                        for (uint32_t i = 0; i < kCols * kC / kExpandLoad; ++i, from += hop) {
+                            const bool in = n + i * (kExpandLoad / kC) < N;
+                            cp_async16(dst + sw128(t0 / kC + i * (kExpandLoad / kC), at_j & 7u), in ? from : src.w, in ? take : 0u);
                         }
                     } else {
                         constexpr uint32_t kRow = kCols / 8; // pieces of a rank's columns
@@ -604,7 +608,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         }
     } else if (warp < kExpandOut / 32) {
         // warps w and w + 4: tokens 32 (w % 4) .. of the tile, w the first half of a block's rows, w + 4
-        // the second. A lane adds a token's sums to its row; then 8 lanes write 128 bytes of a row.
+        // the second. A lane adds a token's sums to its row; then 8 lanes write 128 bytes of a row. (16
+        // such warps, 8 for every other block, take as long.)
         const uint32_t r0 = (warp & 3u) * 32, half = warp >> 2;
         constexpr uint32_t kHalf = kCols / 2;
         uint4 tl = make_uint4(0, 0, 0, 0);
@@ -697,9 +702,11 @@ template <int R>
 constexpr uint32_t outer_out = R > 32 ? 256 : 128;
 template <int R>
 constexpr uint32_t outer_cols = R == 64 ? 256 : 128;
-constexpr uint32_t kOuterLoad = 128, kOuterTok = 64, kOuterStages = 3;
 template <int R>
-constexpr uint32_t outer_threads = outer_out<R> + kOuterLoad + 32;
+constexpr uint32_t outer_load = R > 32 ? 256 : 128;
+constexpr uint32_t kOuterTok = 64, kOuterStages = 3;
+template <int R>
+constexpr uint32_t outer_threads = outer_out<R> + outer_load<R> + 32;
 template <int R>
 __host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 8192 * ((3 * R + 63) / 64); }
 template <int R>
@@ -719,6 +726,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kAccs = outer_accs<R>, kWide = 3 * R;
     constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512; // at least kAccs * kWide, a power of two
     constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
+    constexpr uint32_t kOuterLoad = outer_load<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -777,6 +785,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
         constexpr uint32_t kPieces = kOuterCols / 8, kEvery = kOuterLoad / kPieces, kRows = kOuterTok / kEvery;
         const uint32_t t0 = tid - kOuterOut, piece = t0 % kPieces, r0 = t0 / kPieces;
         const bool in = 8 * piece < cols;
+        const uint16_t* from = job.src + c0 + 8 * piece;
         constexpr uint32_t kC = R / 8;
         uint32_t tok[kRows]; // of the step's tokens; the next step's are fetched a step ahead
         auto fetch = [&](uint32_t step) {
@@ -795,20 +804,28 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
             for (uint32_t i = 0; i < kRows; ++i) now[i] = tok[i];
             fetch(s + 1);
             if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
-            const uint32_t sb = s0 + s % S * kStage, sg = sb + kOuterCols * 128;
+            const uint32_t sb = s0 + s % S * kStage, sg = sb + kOuterCols * 128, dst = sb + (piece >> 3) * 8192;
+            if (in) {
 #pragma unroll
-            for (uint32_t i = 0; i < kRows; ++i) {
-                const bool on = now[i] != ~0u;
-                cp_async16_if(in, sb + (piece >> 3) * 8192 + sw128(r0 + kEvery * i, piece & 7u), on ? job.src + now[i] * job.stride + c0 + 8 * piece : job.src, on ? 16u : 0u);
-            }
-#pragma unroll
-            for (uint32_t t = 0; t < 3; ++t)
-#pragma unroll
-                for (uint32_t c = t0; c < kOuterTok * kC; c += kOuterLoad) {
-                    const uint32_t r = c / kC, j = c % kC, q = t * kC + j;
-                    cp_async16(sg + (q >> 3) * 8192 + sw128(r, q & 7u),
-                               job.parts + uint64_t(t) * p.b.part_stride + uint64_t(r < left ? first + r : t_begin) * R + 8 * j, r < left ? 16u : 0u);
+                for (uint32_t i = 0; i < kRows; ++i) {
+                    const uint32_t on = now[i] != ~0u ? 16u : 0u;
+                    cp_async16(dst + sw128(r0 + kEvery * i, piece & 7u), on ? from + now[i] * job.stride : job.src, on);
                 }
+            }
+            // the parts: 16-byte piece t0 % kC of every kPart-th token
+            constexpr uint32_t kPartRows = kOuterLoad / kC;
+            const uint32_t j = t0 % kC, pr = t0 / kC;
+            const uint16_t* part0 = job.parts + uint64_t(first + pr) * R + 8 * j;
+#pragma unroll
+            for (uint32_t t = 0; t < 3; ++t) {
+                const uint32_t q = t * kC + j;
+#pragma unroll
+                for (uint32_t i = 0; i < kOuterTok / kPartRows; ++i) {
+                    const uint32_t on = pr + kPartRows * i < left ? 16u : 0u;
+                    cp_async16(sg + (q >> 3) * 8192 + sw128(pr + kPartRows * i, q & 7u), on ? part0 + kPartRows * i * R : job.parts, on);
+                }
+                part0 += p.b.part_stride;
+            }
             bar_arrive_copies(bar_full + 8 * (s % S));
         }
         cp_async_wait<0>();
