@@ -57,12 +57,19 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
         bad |= a >= static_cast<int32_t>(n);
         return a < 0 || a >= static_cast<int32_t>(n) ? n : static_cast<uint32_t>(a);
     };
+    constexpr int kAhead = 8; // rows of 32 tokens whose loads are under way together
     if (warp < warps)
-        for (uint32_t t = b0; t < b1; t += 32) {
-            const uint32_t a = t + lane < b1 ? bucket(t + lane) : nb;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-            if (a < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a] += __popc(same);
-            __syncwarp();
+        for (uint32_t t0 = b0; t0 < b1; t0 += 32 * kAhead) {
+            uint32_t a[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) a[i] = t0 + 32 * i + lane < b1 ? bucket(t0 + 32 * i + lane) : nb;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (t0 + 32 * i >= b1) break;
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a[i]);
+                if (a[i] < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a[i]] += __popc(same);
+                __syncwarp();
+            }
         }
     if (bad && err) atomicOr(err, 4u);
     __syncthreads();
@@ -153,15 +160,21 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     __syncthreads();
     for (uint32_t a = tid; a <= nb; a += blockDim.x) plan[o.begin + a] = first[a];
     if (warp < warps)
-        for (uint32_t t = b0; t < b1; t += 32) {
-            const uint32_t a = t + lane < b1 ? bucket(t + lane) : nb;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-            uint32_t at = 0;
-            if (a < nb) at = first[a] + hist[warp * nb + a] + __popc(same & lanemask_lt());
-            __syncwarp();
-            if (a < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a] += __popc(same);
-            __syncwarp();
-            if (a < nb) plan[o.perm + at] = t + lane;
+        for (uint32_t t0 = b0; t0 < b1; t0 += 32 * kAhead) {
+            uint32_t a[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) a[i] = t0 + 32 * i + lane < b1 ? bucket(t0 + 32 * i + lane) : nb;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (t0 + 32 * i >= b1) break;
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a[i]);
+                uint32_t at = 0;
+                if (a[i] < nb) at = first[a[i]] + hist[warp * nb + a[i]] + __popc(same & lanemask_lt());
+                __syncwarp();
+                if (a[i] < nb && (same & lanemask_lt()) == 0) hist[warp * nb + a[i]] += __popc(same);
+                __syncwarp();
+                if (a[i] < nb) plan[o.perm + at] = t0 + 32 * i + lane;
+            }
         }
     auto tile_at = [&](const uint32_t* tb, uint32_t size, uint32_t i) {
         uint32_t lo = 0, hi = nb - 1; // the last bucket whose first tile is at or before i
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     __shared__ int s_abort;
     constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
     constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
-    after_kernel_before();
+    after_kernel_before<false>();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t tiles = p.b.plan[1];
@@ -692,6 +705,10 @@ struct OuterParams {
     Batch b;
     uint32_t split;
     uint32_t accumulate; // add to out, adapters without tokens left as they are
+    // The kernel before this one is the expand product of the same call. It lets this one start when all
+    // of its CTAs have seen the kernel before it (shrink, whose g is needed here) complete, so nothing
+    // has to be waited for; its own completion is, at the end.
+    uint32_t beside_expand, pad;
     OuterJob job[2 * kMaxItems];
 };
 // Threads that add up, that load; a warp more issues. A stage holds 64 tokens: their columns (MN-major)
@@ -730,7 +747,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    after_kernel_before();
+    if (!p.beside_expand) after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     // all jobs' blocks of columns for the adapter with the most tokens first, then the next: the last
@@ -744,7 +761,10 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     const uint32_t rm = p.b.rank_max, cols = min(kOuterCols, job.width - c0);
     float* out = job.out + uint64_t(a) * rm * job.width;
     if (t_begin == t_end) { // no tokens: zero, or as it is
-        if (p.accumulate) return;
+        if (p.accumulate) {
+            if (p.beside_expand) kernels_before_done();
+            return;
+        }
         if (!job.transposed) {
             for (uint32_t i = part * kOuterThreads + tid; i < rm * (cols / 4); i += p.split * kOuterThreads)
                 *reinterpret_cast<float4*>(out + uint64_t(i / (cols / 4)) * job.width + c0 + 4 * (i % (cols / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -752,6 +772,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
             float4* d = reinterpret_cast<float4*>(out + uint64_t(c0) * rm);
             for (uint32_t i = part * kOuterThreads + tid; i < cols * rm / 4; i += p.split * kOuterThreads) d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        if (p.beside_expand) kernels_before_done();
         return;
     }
     const uint32_t steps = (t_end - t_begin + kOuterTok - 1) / kOuterTok, per = (steps + p.split - 1) / p.split;
@@ -915,6 +936,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
         __syncwarp();
         tmem_free(tmem, kTmem);
     }
+    if (p.beside_expand) kernels_before_done();
 }
 
 // ---------------------------------------------------------------- host
@@ -1197,6 +1219,7 @@ extern "C" bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, cons
             if ((st = launch_shrink<true>(sp, m, R, gpu)) != BS_OK) return st;
             if (outs && (st = launch_expand<true>(ep, outs, R, gpu)) != BS_OK) return st;
         }
+        op.beside_expand = batch->tokens && outs;
         if ((st = launch_outer(op, 2 * m, R, gpu)) != BS_OK) return st;
     }
     return BS_OK;

@@ -69,9 +69,14 @@ __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
 // Programmatic dependent launch: the next kernel of the stream may be scheduled once every CTA of this
 // one has started, and takes over the SMs that it leaves; this one goes on when the kernels before it
 // have completed and what they wrote is visible. Nothing global is read or written before.
+// EARLY false: the next kernel is let go only after that wait, so that it knows the kernels before this
+// one complete without a wait of its own.
+__device__ __forceinline__ void kernels_before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <bool EARLY = true>
 __device__ __forceinline__ void after_kernel_before() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (EARLY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    kernels_before_done();
+    if (!EARLY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // The decoding kernel (bs_lora_few.cu): a cluster takes up to kFew tokens of one adapter through
