@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
         }
     }
     __syncthreads();
-    for (uint32_t a = tid; a < n; a += blockDim.x) plan[o.order + atomicAdd(&s_class[class_of(a)], 1u)] = a;
+    for (uint32_t a = tid; a < n; a += blockDim.x)
+        reinterpret_cast<uint4*>(plan + o.order)[atomicAdd(&s_class[class_of(a)], 1u)] = make_uint4(a, first[a], a + 1 < nb ? first[a + 1] : s_carry[0], 0);
     if (tid == 0) {
         first[nb] = s_carry[0];
         t128[nb] = s_carry[1];
@@ -241,16 +242,8 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     constexpr uint32_t kTmem = R <= 16 ? 32 : 2 * R, S = kShrinkStages, kShrinkOut = shrink_out<R>, kRanks = R > 64 ? 64 : R;
-    after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;
-    const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    if (tile >= p.b.plan[0]) return; // the whole cluster
-    const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[tile];
-    const ShrinkJob& job = p.job[blockIdx.y];
-    const uint32_t a = tl.x, first = tl.y, count = tl.z, rank = rank_of(p.b, a), K = job.width;
-    const uint32_t steps = (K + 63) / 64, per = (steps + p.split - 1) / p.split;
-    const uint32_t k_begin = min(part * per, steps), n_steps = min(k_begin + per, steps) - k_begin;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     constexpr uint32_t kStage = shrink_stage<R, WT>();
     // barriers: full[S] (a stage has landed), empty[S] (its matrix instructions are done), d[2] (a
@@ -270,22 +263,36 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     }
     constexpr uint32_t kIssueWarp = (kShrinkOut + kShrinkLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    after_kernel_before(); // the above goes on beside the end of the kernel before
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    const uint32_t tiles = p.b.plan[0];
+    const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[tile];
+    const ShrinkJob& job = p.job[blockIdx.y];
+    const uint32_t a = tl.x, first = tl.y, count = tl.z, K = job.width;
+    const uint32_t steps = (K + 63) / 64, per = (steps + p.split - 1) / p.split;
+    const uint32_t k_begin = min(part * per, steps), n_steps = min(k_begin + per, steps) - k_begin;
+    const uint16_t* row[8] = {}; // of the loading threads: piece t0 % 8 of the rows t0 / 8 + 16 i of x
+    if (tile < tiles && warp >= kShrinkOut / 32 && warp < kIssueWarp) {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t r = ((tid - kShrinkOut) >> 3) + 16 * i;
+            row[i] = r < count ? job.src + p.b.plan[o.perm + first + r] * job.stride : nullptr;
+        }
+    }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
+    if (tile >= tiles) { // the whole cluster
+        if (warp == kIssueWarp) tmem_free(tmem, kTmem);
+        return;
+    }
+    const uint32_t rank = rank_of(p.b, a);
     volatile int* abort_flag = &s_abort;
     float* red = reinterpret_cast<float*>(smem_raw + (s0 - smem_u32(smem_raw))); // [128][R + 4], over the stages at the end
 
     if (warp >= kShrinkOut / 32 && warp < kIssueWarp) {
-        // piece t0 % 8 of the rows t0 / 8 + 16 i of x; rows past the tokens stand for nothing
-        const uint32_t t0 = tid - kShrinkOut, chunk = t0 & 7u;
-        const uint16_t* row[8];
-#pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) {
-            const uint32_t r = (t0 >> 3) + 16 * i;
-            row[i] = r < count ? job.src + p.b.plan[o.perm + first + r] * job.stride : nullptr;
-        }
+        const uint32_t t0 = tid - kShrinkOut, chunk = t0 & 7u; // rows past the tokens stand for nothing
         const uint16_t* w = job.w + uint64_t(a) * p.b.rank_max * K;
         for (uint32_t s = 0; s < n_steps; ++s) {
             if (s >= S && !bar_wait(bar_empty + 8 * (s % S), (s / S - 1) & 1u, abort_flag)) break;
@@ -448,34 +455,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     __shared__ int s_abort;
     constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
     constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
-    after_kernel_before<false>();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    const uint32_t tiles = p.b.plan[1];
-    const uint4* tile_of = reinterpret_cast<const uint4*>(p.b.plan + o.tiles);
-    auto blocks_of = [&](uint32_t job) { return (p.job[job].width + kCols - 1) / kCols; };
-    uint64_t total = 0;
-    for (uint32_t k = 0; k < p.n_jobs; ++k) total += uint64_t(tiles) * blocks_of(k);
-    const uint64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
-    if (u0 == u1) return;
-    const uint32_t n_units = static_cast<uint32_t>(u1 - u0);
-    ExpandAt start{0, 0, 0};
-    {
-        uint64_t u = u0;
-        while (u >= uint64_t(tiles) * blocks_of(start.job)) u -= uint64_t(tiles) * blocks_of(start.job++);
-        start.tile = static_cast<uint32_t>(u / blocks_of(start.job));
-        start.block = static_cast<uint32_t>(u % blocks_of(start.job));
-    }
-    // steps to the next unit; true where the tile (or job) is another one
-    auto next = [&](ExpandAt& at) {
-        if (++at.block < blocks_of(at.job)) return false;
-        at.block = 0;
-        if (++at.tile == tiles) {
-            at.tile = 0;
-            ++at.job;
-        }
-        return true;
-    };
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sH = s0, sW = sH + kParts * kPart, sRow = sW + 2 * expand_w<R, BF16>();
     uint8_t* const rows = smem_raw + (sRow - smem_u32(smem_raw));
@@ -499,6 +479,32 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     }
     constexpr uint32_t kIssueWarp = (kExpandOut + kExpandLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    after_kernel_before<false>(); // the above goes on beside the end of the kernel before
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    const uint32_t tiles = p.b.plan[1];
+    const uint4* tile_of = reinterpret_cast<const uint4*>(p.b.plan + o.tiles);
+    auto blocks_of = [&](uint32_t job) { return (p.job[job].width + kCols - 1) / kCols; };
+    uint64_t total = 0;
+    for (uint32_t k = 0; k < p.n_jobs; ++k) total += uint64_t(tiles) * blocks_of(k);
+    const uint64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t n_units = static_cast<uint32_t>(u1 - u0);
+    ExpandAt start{0, 0, 0};
+    if (n_units) {
+        uint64_t u = u0;
+        while (u >= uint64_t(tiles) * blocks_of(start.job)) u -= uint64_t(tiles) * blocks_of(start.job++);
+        start.tile = static_cast<uint32_t>(u / blocks_of(start.job));
+        start.block = static_cast<uint32_t>(u % blocks_of(start.job));
+    }
+    // steps to the next unit; true where the tile (or job) is another one
+    auto next = [&](ExpandAt& at) {
+        if (++at.block < blocks_of(at.job)) return false;
+        at.block = 0;
+        if (++at.tile == tiles) {
+            at.tile = 0;
+            ++at.job;
+        }
+        return true;
+    };
     fence_before();
     __syncthreads();
     fence_after();
@@ -747,36 +753,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    if (!p.beside_expand) after_kernel_before();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-    const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    // all jobs' blocks of columns for the adapter with the most tokens first, then the next: the last
-    // CTAs to start are the shortest
-    const uint32_t part = blockIdx.x % p.split, a = p.b.plan[o.order + blockIdx.y];
-    uint32_t block = blockIdx.x / p.split, k = 0;
-    while (block >= (p.job[k].width + kOuterCols - 1) / kOuterCols) block -= (p.job[k++].width + kOuterCols - 1) / kOuterCols;
-    const OuterJob& job = p.job[k];
-    const uint32_t c0 = block * kOuterCols;
-    const uint32_t t_begin = p.b.plan[o.begin + a], t_end = p.b.plan[o.begin + a + 1];
-    const uint32_t rm = p.b.rank_max, cols = min(kOuterCols, job.width - c0);
-    float* out = job.out + uint64_t(a) * rm * job.width;
-    if (t_begin == t_end) { // no tokens: zero, or as it is
-        if (p.accumulate) {
-            if (p.beside_expand) kernels_before_done();
-            return;
-        }
-        if (!job.transposed) {
-            for (uint32_t i = part * kOuterThreads + tid; i < rm * (cols / 4); i += p.split * kOuterThreads)
-                *reinterpret_cast<float4*>(out + uint64_t(i / (cols / 4)) * job.width + c0 + 4 * (i % (cols / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
-        } else {
-            float4* d = reinterpret_cast<float4*>(out + uint64_t(c0) * rm);
-            for (uint32_t i = part * kOuterThreads + tid; i < cols * rm / 4; i += p.split * kOuterThreads) d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (p.beside_expand) kernels_before_done();
-        return;
-    }
-    const uint32_t steps = (t_end - t_begin + kOuterTok - 1) / kOuterTok, per = (steps + p.split - 1) / p.split;
-    const uint32_t s_begin = min(part * per, steps), n_steps = min(s_begin + per, steps) - s_begin;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bar_full = smem_u32(s_bar), bar_empty = bar_full + 8 * S, bar_d = bar_empty + 8 * S, bar_free = bar_d + 16; // as in shrink
     if (tid == 0) {
@@ -793,10 +770,41 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     }
     constexpr uint32_t kIssueWarp = (kOuterOut + kOuterLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
+    if (!p.beside_expand) after_kernel_before(); // the above goes on beside the end of the kernel before
+    const PlanAt o = plan_at(p.b.tokens, p.b.n);
+    const uint4 entry = reinterpret_cast<const uint4*>(p.b.plan + o.order)[blockIdx.y];
+    // all jobs' blocks of columns for the adapter with the most tokens first, then the next: the last
+    // CTAs to start are the shortest
+    const uint32_t part = blockIdx.x % p.split, a = entry.x;
+    uint32_t block = blockIdx.x / p.split, k = 0;
+    while (block >= (p.job[k].width + kOuterCols - 1) / kOuterCols) block -= (p.job[k++].width + kOuterCols - 1) / kOuterCols;
+    const OuterJob& job = p.job[k];
+    const uint32_t c0 = block * kOuterCols;
+    const uint32_t t_begin = entry.y, t_end = entry.z;
+    const uint32_t rm = p.b.rank_max, cols = min(kOuterCols, job.width - c0);
+    float* out = job.out + uint64_t(a) * rm * job.width;
+    const uint32_t steps = (t_end - t_begin + kOuterTok - 1) / kOuterTok, per = (steps + p.split - 1) / p.split;
+    const uint32_t s_begin = min(part * per, steps), n_steps = min(s_begin + per, steps) - s_begin;
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
+    if (t_begin == t_end) { // no tokens: zero, or as it is
+        if (warp == kIssueWarp) tmem_free(tmem, kTmem);
+        if (p.accumulate) {
+            if (p.beside_expand) kernels_before_done();
+            return;
+        }
+        if (!job.transposed) {
+            for (uint32_t i = part * kOuterThreads + tid; i < rm * (cols / 4); i += p.split * kOuterThreads)
+                *reinterpret_cast<float4*>(out + uint64_t(i / (cols / 4)) * job.width + c0 + 4 * (i % (cols / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            float4* d = reinterpret_cast<float4*>(out + uint64_t(c0) * rm);
+            for (uint32_t i = part * kOuterThreads + tid; i < cols * rm / 4; i += p.split * kOuterThreads) d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (p.beside_expand) kernels_before_done();
+        return;
+    }
     volatile int* abort_flag = &s_abort;
     float* red = reinterpret_cast<float*>(smem_raw + (s0 - smem_u32(smem_raw))); // [256][R + 4], over the stages at the end
 

@@ -24,7 +24,7 @@ constexpr int kMaxItems = 16;     // projections of one launch
 //   [0] tiles of kTile tokens that have an adapter, [1] all tiles of kTile (those without an
 //   adapter follow), [2] and [3] the same for kFew (0 above kFewTokens), [4] tokens, [5] adapters
 //   begin[n_adapters + 2]: the first place of each bucket, then the end
-//   order[n_adapters]: the adapters, those with the most tokens first (about)
+//   order: (adapter, first place, end, 0) of each adapter, those with the most tokens first (about)
 //   perm[tokens]: the token at each place
 //   tiles: (bucket, first place, tokens, 0) each
 //   tiles of kFew: the same, and the tokens themselves
@@ -43,7 +43,7 @@ __host__ __device__ inline PlanAt plan_at(uint32_t tokens, uint32_t n) {
     auto up4 = [](uint64_t v) { return (v + 3) & ~uint64_t(3); };
     o.begin = 16;
     o.order = o.begin + up4(n + 2);
-    o.perm = o.order + up4(n);
+    o.perm = o.order + 4ull * n;
     o.tiles = o.perm + up4(tokens);
     o.few = o.tiles + 4ull * tile_cap(tokens, n, kTile);
     o.words = o.few + (tokens <= kFewTokens ? sizeof(FewTile) / 4 * tile_cap(tokens, n, kFew) : 0);

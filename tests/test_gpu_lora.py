@@ -235,10 +235,12 @@ def test_plan_groups_in_order(tokens, n):
     bucket = np.where(idx < 0, n, idx)
     assert np.array_equal(begin, np.concatenate([[0], np.cumsum(np.bincount(bucket, minlength=n + 1))]))
     at = 16 + up4(n + 2)
-    order, count = w[at:at + n], np.bincount(bucket, minlength=n + 1)[:n]
+    rows, count = w[at:at + 4 * n].reshape(n, 4), np.bincount(bucket, minlength=n + 1)[:n]
+    order = rows[:, 0]
+    assert np.array_equal(rows[:, 1], begin[order]) and np.array_equal(rows[:, 2], begin[order + 1]) and not rows[:, 3].any()
     assert np.array_equal(np.sort(order), np.arange(n))  # every adapter once, the ones with most tokens first:
     assert np.all(count[order][1:] * 8 <= count[order][:-1] * 9 + 8)  # none after one an eighth smaller
-    at += up4(n)
+    at += 4 * n
     assert np.array_equal(w[at:at + tokens], np.argsort(bucket, kind="stable"))
     assert int(plan.err) == 0
     for size, count, start in ((128, w[:2], at + up4(tokens)), (8, w[2:4], at + up4(tokens) + 4 * min(tokens, tokens // 128 + n + 1))):
