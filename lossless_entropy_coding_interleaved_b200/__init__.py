@@ -688,24 +688,38 @@ def _fw_products(products, max_batch):
     return n, arr, batch or 1
 
 
-def fw_gemm(products, err: torch.Tensor, stream=None):
+def _with_adapters(products, adapters, stream):
+    """Adds each token's adapter to the products' outputs: adapters is (LoraAdapters, LoraPlan) or
+    (LoraAdapters, LoraPlan, state), the adapters' projections being the products in order."""
+    who, plan = adapters[:2]
+    two = lambda t: t.view(1, -1) if t.dim() == 1 else t  # noqa: E731
+    who.forward(plan, [two(p[4].view(torch.bfloat16)) for p in products], [two(p[5]) for p in products],
+                state=adapters[2] if len(adapters) > 2 else None, stream=stream)
+
+
+def fw_gemm(products, err: torch.Tensor, stream=None, adapters=None):
     """bs_fw_gemm: as fw_gemv, on the tensor cores, for any batch (rows a multiple of 128):
     products is a sequence of (fw, info, rows, cols, x [batch, cols] BF16, y [batch, rows] float32).
-    err: a zeroed int32 CUDA tensor of one element. Enqueued on the stream."""
+    err: a zeroed int32 CUDA tensor of one element. adapters: as fw_gemv's. Enqueued on the stream."""
     n, arr, batch = _fw_products(products, None)
     assert err.is_cuda and err.dtype == torch.int32 and err.numel() >= 1
     with torch.cuda.device(err.device):
         _check(lib.bs_fw_gemm(n, arr, batch, err.data_ptr(), _stream(stream)), "fw_gemm")
+    if adapters is not None:
+        _with_adapters(products, adapters, stream)
     return [p[5] for p in products]
 
 
-def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = False):
+def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = False, adapters=None):
     """bs_fw_gemv: products is a sequence of (fw, info, rows, cols, x, y) with fw the layout of
     W (rows x cols), x a BF16 CUDA tensor [batch, cols] (or [cols]) and y a float32 CUDA
     tensor [batch, rows] (or [rows]); every x has the same batch (1..8). err: a zeroed int32
     CUDA tensor of one element. Enqueued on the stream. layouts_resident: BS_FW_LAYOUTS_RESIDENT,
     a statement that no work in flight on the stream writes the layouts (resident weights), so
-    that their copies may start before the preceding kernel has finished."""
+    that their copies may start before the preceding kernel has finished. adapters: low-rank adapters
+    beside the products, (LoraAdapters, LoraPlan) or (LoraAdapters, LoraPlan, state), whose projections
+    are the products in order and whose tokens are the batch; their part is added to every y
+    (bs_lora_forward), and the state that a backward pass needs is left in state."""
     n = len(products)
     arr = (FwGemvItem * max(n, 1))()
     batch = None
@@ -724,6 +738,8 @@ def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = F
     with torch.cuda.device(err.device):
         _check(lib.bs_fw_gemv(n, arr, batch or 1, FW_LAYOUTS_RESIDENT if layouts_resident else 0, err.data_ptr(),
                               _stream(stream)), "fw_gemv")
+    if adapters is not None:
+        _with_adapters(products, adapters, stream)
     return [p[5] for p in products]
 
 
@@ -775,7 +791,8 @@ class LoraAdapters:
     pools) are written, or added to with accumulate; dxs[k] = dx_bases[k] + the adapters' part,
     where entries of dxs that are the same tensor receive the sum of their parts. dx_bases None: 0.
     xs and dys are bfloat16 [tokens, width], ys and dxs float32 or bfloat16, their bases of the same
-    type; rows may be strided. Arguments of several projections are lists or tuples. Beside fw_gemv and fw_gemm the outputs of those are the bases.
+    type; rows may be strided. Arguments of several projections are lists or tuples. Beside a coded
+    projection, fw_gemv and fw_gemm take the adapters with the product (their ``adapters``).
     """
 
     def __init__(self, a, b, scales: torch.Tensor | None = None, ranks: torch.Tensor | None = None):
@@ -972,7 +989,7 @@ class AdamW:
             it.d_m_scale, it.d_v_scale = ptr(self.exp_avg_scale, k), ptr(self.exp_avg_sq_scale, k)
             it.n, it.param_type, it.grad_type = sizes[k], _TYPES[self.params[k].dtype], _TYPES[self.grads[k].dtype]
             it.weight_decay = decay[k]
-        self._n, self._sizes, self._index = n, sizes, self.params[0].get_device()
+        self._n, self._sizes, self._index, self._pointers = n, sizes, self.params[0].get_device(), ctypes.c_void_p * n
         self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
         self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
@@ -1035,10 +1052,14 @@ class AdamW:
         if self.bits == 32:
             return self.exp_avg, self.exp_avg_sq
         ms, vs = ([torch.empty(k, dtype=torch.float32, device=self.device) for k in self._sizes] if t is None else list(t) for t in (ms, vs))
+        index, f32, at = self._index, torch.float32, []
         for ts in (ms, vs):
-            if len(ts) != self._n or any(t.numel() != k or t.dtype is not torch.float32 or t.get_device() != self._index or
-                                         not t.is_contiguous() for t, k in zip(ts, self._sizes)):
-                raise BsError(E_ARG, "adamw", "read_states: a contiguous float32 tensor of each parameter's size")
-        pm, pv = ((ctypes.c_void_p * self._n)(*[t.data_ptr() or None for t in ts]) for ts in (ms, vs))
+            if len(ts) != self._n:
+                raise BsError(E_ARG, "adamw", "read_states: one tensor for each parameter")
+            for t, k in zip(ts, self._sizes):
+                if t.numel() != k or t.dtype is not f32 or t.get_device() != index or not t.is_contiguous():
+                    raise BsError(E_ARG, "adamw", "read_states: a contiguous float32 tensor of each parameter's size")
+                at.append(t.data_ptr())
+        pm, pv = self._pointers(*at[:self._n]), self._pointers(*at[self._n:])
         _on(self._index, "adamw_read_states", lib.bs_adamw_read_states, self._n, self._items, pm, pv, stream=stream)
         return ms, vs
