@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     extern __shared__ uint32_t sm[];
     __shared__ uint32_t s_scan[3][32], s_carry[3];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, nb = n + 1; // buckets
+    after_kernel_before();
     uint32_t* hist = sm;                    // [warps][nb]
     uint32_t* first = hist + warps * nb;    // [nb + 1] first place of each bucket
     uint32_t* t128 = first + nb + 1;        // [nb + 1] first tile of each bucket
@@ -1108,9 +1109,19 @@ extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_
     if (e != cudaSuccess) return cuda_status(e);
     // a thread for each token or bucket; a small block passes its barriers sooner (the scan needs 3 warps)
     const uint32_t threads = std::min(1024u, std::max(128u, (std::max(tokens, nb) + 31) & ~31u));
-    lora_plan_kernel<<<1, threads, smem, static_cast<cudaStream_t>(stream)>>>(d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see after_kernel_before
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, lora_plan_kernel, d_idx, tokens, n_adapters, static_cast<uint32_t*>(d_plan), warps, d_err);
     count_launch();
-    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
 }
 

@@ -50,6 +50,12 @@ struct BRows {
     uint32_t lo[W], hi[W];
 };
 
+// Blocks of rows whose loads a warp has under way while it works on one. At rank 64, 3 CTAs an SM with
+// one block ahead take 41 us for 37 tokens over 24 adapters (14336 rows, twice); 2 CTAs with 4 ahead
+// take 46, since clusters of 8 then leave slots of their group of SMs empty.
+template <int R>
+constexpr uint32_t kAhead = R > 32 ? 1 : 4;
+
 // B h of a CTA gathers in shared memory, up to 16 blocks of 128 rows at a time, and goes from there to
 // y with base added, token by token in whole lines: from the matrix instructions' registers it would
 // be 4 scattered numbers a lane, most of them of tokens that the tile does not have.
@@ -155,10 +161,12 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
         }
     };
     // the rows of B h in blocks of 128, dealt out to the CTAs of the tile's clusters, 16 rows a warp
-    BRows<R> cur, next;
+    BRows<R> ring[kAhead<R>];
     const uint32_t first_row = (part * kFewCluster + cta) * 128 + warp * 16, row_deal = p.split * kFewCluster * 128;
     const uint32_t rows_end = job.out ? N : 0;
-    if (first_row < rows_end) load(cur, first_row); // under way while the sums of h are exchanged
+#pragma unroll
+    for (uint32_t d = 0; d < kAhead<R>; ++d) // under way while the sums of h are exchanged
+        if (first_row + d * row_deal < rows_end) load(ring[d], first_row + d * row_deal);
     cluster.barrier_wait();
     for (uint32_t i = tid; i < R * 8; i += kFewThreads) {
         float peer[kFewCluster], v = 0.f;
@@ -190,32 +198,35 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
         for (int t = 0; t < 3; ++t) hf[w][t] = lo[t] | (hi[t] << 16);
     }
     for (uint32_t hold = first_row - warp * 16; hold < rows_end; hold += kHold * row_deal) { // the same for every warp
-        uint32_t held = 0;
-        for (uint32_t n0 = hold + warp * 16; n0 < rows_end && held < kHold; n0 += row_deal, ++held) {
-            if (n0 + row_deal < rows_end) load(next, n0 + row_deal);
-            float d[4] = {};
+        for (uint32_t held = 0; held < kHold; held += kAhead<R>)
 #pragma unroll
-            for (int m = 0; m < W / WS; ++m) {
-                if (static_cast<uint32_t>(m) >= steps) break;
-                if (static_cast<uint32_t>(m) + 1 == steps) {
+            for (uint32_t r = 0; r < kAhead<R>; ++r) {
+                const uint32_t n0 = hold + warp * 16 + (held + r) * row_deal;
+                if (n0 >= rows_end) break;
+                BRows<R>& cur = ring[r];
+                float d[4] = {};
 #pragma unroll
-                    for (int i = 0; i < WS; ++i) {
-                        cur.lo[m * WS + i] &= mask[i];
-                        cur.hi[m * WS + i] &= mask[i];
+                for (int m = 0; m < W / WS; ++m) {
+                    if (static_cast<uint32_t>(m) >= steps) break;
+                    if (static_cast<uint32_t>(m) + 1 == steps) {
+#pragma unroll
+                        for (int i = 0; i < WS; ++i) {
+                            cur.lo[m * WS + i] &= mask[i];
+                            cur.hi[m * WS + i] &= mask[i];
+                        }
+                    }
+#pragma unroll
+                    for (int w = m * WS; w < (m + 1) * WS; w += 2) {
+                        const uint32_t af[4] = {cur.lo[w], cur.hi[w], cur.lo[w + 1], cur.hi[w + 1]};
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
                     }
                 }
-#pragma unroll
-                for (int w = m * WS; w < (m + 1) * WS; w += 2) {
-                    const uint32_t af[4] = {cur.lo[w], cur.hi[w], cur.lo[w + 1], cur.hi[w + 1]};
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
-                }
+                if (n0 + kAhead<R> * row_deal < rows_end) load(cur, n0 + kAhead<R> * row_deal);
+                float* y = s_y + 2 * q * kHoldRows + (held + r) * 128 + warp * 16 + g;
+                if (2 * q < count) { y[0] = d[0]; y[8] = d[2]; }
+                if (2 * q + 1 < count) { y[kHoldRows] = d[1]; y[kHoldRows + 8] = d[3]; }
             }
-            float* y = s_y + 2 * q * kHoldRows + held * 128 + warp * 16 + g;
-            if (2 * q < count) { y[0] = d[0]; y[8] = d[2]; }
-            if (2 * q + 1 < count) { y[kHoldRows] = d[1]; y[kHoldRows + 8] = d[3]; }
-            cur = next;
-        }
         __syncthreads();
         // 4 columns a thread: a block of 128 by a warp
         const uint32_t left = (rows_end - hold + row_deal - 1) / row_deal, n_held = min(left, kHold);
