@@ -501,8 +501,10 @@ typedef struct {
     const int32_t* d_ranks;      /* NULL (rank_max for all), or one for each adapter, 0..rank_max */
     const float* d_scales;       /* NULL (1 for all), or one for each adapter */
     const void* d_plan;
-    uint32_t* d_err;             /* NULL, or a device word the caller zeroes before and reads after: bit 1 (value 2)
-                                  * means that a wait inside a kernel ran out (its outputs are then incomplete) */
+    size_t plan_bytes;           /* size of its buffer, at least bs_lora_plan_bytes(tokens, n_adapters) */
+    uint32_t* d_err;             /* NULL, or a device word the caller zeroes before and reads after. Bit 1 (value 2):
+                                  * a wait inside a kernel ran out, its outputs are incomplete. Bit 3 (value 8): the plan
+                                  * is of another batch (tokens or n_adapters differ), nothing was computed. */
 } bs_lora_batch;
 
 /* One projection. Strides are in elements from one token to the next, at least the row's length.

@@ -97,7 +97,7 @@ class LoraBatch(ctypes.Structure):
     """bs_lora_batch: the batch that the items of one call share."""
     _fields_ = [("tokens", ctypes.c_uint32), ("n_adapters", ctypes.c_uint32), ("rank_max", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("d_ranks", ctypes.c_void_p), ("d_scales", ctypes.c_void_p),
-                ("d_plan", ctypes.c_void_p), ("d_err", ctypes.c_void_p)]
+                ("d_plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t), ("d_err", ctypes.c_void_p)]
 
 
 class AdamWItem(ctypes.Structure):
@@ -753,9 +753,10 @@ assert _LORA_ITEM.size == ctypes.sizeof(LoraItem) == 160
 class LoraPlan:
     """The routing of a batch of ``tokens`` tokens to ``n_adapters`` adapters (bs_lora_plan), in
     device memory. update(idx) sets it from an int32 CUDA tensor, an adapter per token (negative:
-    none); one plan serves every projection of the batch, and may be updated for the next batch.
+    none; a new plan gives no token an adapter); one plan serves every projection of the batch, and may be updated for the next batch.
     ``err``, an int32 device word, gathers what the calls that use the plan report: bit 2 an index past
-    the adapters, bit 1 a wait inside a kernel that ran out (0 in a working program)."""
+    the adapters, bit 1 a wait inside a kernel that ran out, bit 3 a plan of another batch (the last two
+    never in a working program)."""
 
     def __init__(self, tokens: int, n_adapters: int, device="cuda"):
         if not torch.cuda.is_available():
@@ -769,6 +770,7 @@ class LoraPlan:
         self.device = self.data.device
         self._index = self.data.get_device()
         self._args = (tokens, n_adapters, self.data.data_ptr(), nb, self.err.data_ptr())
+        self.update(torch.full((tokens,), -1, dtype=torch.int32, device=self.device))
 
     def update(self, idx: torch.Tensor, stream=None) -> "LoraPlan":
         """Enqueued on the stream. An index past the adapters counts as none and sets bit 2 of ``err``."""
@@ -863,7 +865,7 @@ class LoraAdapters:
         for t in states:
             if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != index:
                 raise BsError(E_SIZE, "lora", "a state is of another batch")
-        return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, plan._args[2], plan._args[4])
+        return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, *plan._args[2:])
 
     def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
         n, T = self._n, plan.tokens

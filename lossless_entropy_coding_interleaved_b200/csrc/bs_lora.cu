@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
     after_kernel_before(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    const uint32_t tiles = p.b.plan[0];
+    const uint32_t tiles = plan_head(p.b).x;
     const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[tile];
     const ShrinkJob& job = p.job[blockIdx.y];
     const uint32_t a = tl.x, first = tl.y, count = tl.z, K = job.width;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
     after_kernel_before<false>(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    const uint32_t tiles = p.b.plan[1];
+    const uint32_t tiles = plan_head(p.b).y;
     const uint4* tile_of = reinterpret_cast<const uint4*>(p.b.plan + o.tiles);
     auto blocks_of = [&](uint32_t job) { return (p.job[job].width + kCols - 1) / kCols; };
     uint64_t total = 0;
@@ -773,7 +773,9 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
     if (!p.beside_expand) after_kernel_before(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
-    const uint4 entry = reinterpret_cast<const uint4*>(p.b.plan + o.order)[blockIdx.y];
+    bool planned;
+    plan_head(p.b, &planned);
+    const uint4 entry = planned ? reinterpret_cast<const uint4*>(p.b.plan + o.order)[blockIdx.y] : make_uint4(0, 0, 0, 0);
     // all jobs' blocks of columns for the adapter with the most tokens first, then the next: the last
     // CTAs to start are the shortest
     const uint32_t part = blockIdx.x % p.split, a = entry.x;
@@ -792,6 +794,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     const uint32_t tmem = s_tmem;
     if (t_begin == t_end) { // no tokens: zero, or as it is
         if (warp == kIssueWarp) tmem_free(tmem, kTmem);
+        if (!planned) return;
         if (p.accumulate) {
             if (p.beside_expand) kernels_before_done();
             return;
@@ -954,7 +957,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bs_status check_batch(const bs_lora_batch* b) {
     if (!b || b->tokens > kMaxTokens || b->n_adapters < 1 || b->n_adapters > kMaxAdapters || b->reserved) return BS_E_ARG;
     if (b->rank_max < 8 || b->rank_max > kMaxRank || b->rank_max % 8) return BS_E_ARG;
-    if (!b->d_plan || !aligned(b->d_plan, 16) || !aligned(b->d_ranks, 4) || !aligned(b->d_scales, 4) || !aligned(b->d_err, 4)) return BS_E_ARG;
+    if (!b->d_plan || !aligned(b->d_plan, 16) || b->plan_bytes < bs_lora_plan_bytes(b->tokens, b->n_adapters) || !aligned(b->d_ranks, 4) || !aligned(b->d_scales, 4) || !aligned(b->d_err, 4)) return BS_E_ARG;
     return BS_OK;
 }
 bs_status check_item(const bs_lora_item& t) {
@@ -1008,8 +1011,13 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? BS_OK : cuda_status(e);
 }
-// Whether a batch goes through the decoding kernel.
-bool few_tokens(uint32_t tokens, uint32_t n) { return tokens <= 128 || (tokens <= kFewTokens && tokens <= 4 * n); }
+// Whether a batch goes through the decoding kernel. It reads an adapter's weights for every 8 of its
+// tokens (0.4 to 0.8 us a tile of 8 at 3584 x 14336, ranks 16 and 64), the tiled kernels for every
+// 128, but they pass through tiles that are mostly empty (2 to 2.4 us an adapter). 64 tokens of one
+// adapter: 27 and 33 us here, 22 and 25 us tiled (18 and 22 us at 3584 x 4096, rank 64); 256 tokens of 8:
+// 31 and 39 us, tiled 35 and 41; 512 of 32: 55 and 82, tiled 78 and 92; 1024 of 256: 121 and 223,
+// tiled 514 and 618.
+bool few_tokens(uint32_t tokens, uint32_t n) { return tokens <= kFewTokens && tokens <= 16 * n + 48; }
 
 // CTAs of a cluster that share a sum: the most of 1, 2, 4, 8 that leave each CTA 4 steps and fit into
 // `slots` CTAs at a time.

@@ -58,8 +58,18 @@ struct Batch {
     const uint32_t* plan;
     const int32_t* ranks;  // nullptr: every adapter has rank_max
     const float* scales;   // nullptr: 1
-    uint32_t* err;         // nullptr, or a word whose bit 1 says that a wait inside a kernel ran out
+    uint32_t* err;         // nullptr, or a word for what kernels report (bits 1 and 3)
 };
+// The plan's first four words: tiles with an adapter, all tiles, the same of kFew. All 0, and bit 3 of
+// the error word, where the plan is of another batch (its buffer is as large as this batch's at least,
+// so whatever is read of it besides is in its bounds).
+__device__ __forceinline__ uint4 plan_head(const Batch& b, bool* good = nullptr) {
+    const uint4 head = *reinterpret_cast<const uint4*>(b.plan), of = *reinterpret_cast<const uint4*>(b.plan + 4);
+    const bool ok = of.x == b.tokens && of.y == b.n;
+    if (!ok && b.err && threadIdx.x == 0) atomicOr(b.err, 8u);
+    if (good) *good = ok;
+    return ok ? head : make_uint4(0, 0, 0, 0);
+}
 __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
     if (!b.ranks) return b.rank_max;
     const int32_t r = __ldg(b.ranks + a);

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const FewTile* entry = reinterpret_cast<const FewTile*>(p.b.plan + o.few) + tile;
     const uint32_t a = entry->bucket, first = entry->first, count = entry->count, tok_g = entry->token[g];
-    if (tile >= p.b.plan[3]) return; // the whole cluster
+    if (tile >= plan_head(p.b).w) return; // the whole cluster
     if (a >= p.b.n) { // tokens without an adapter: base as it is
         if (!job.out || (job.base == job.out && job.base_stride == job.out_stride)) return;
         const uint32_t es = job.bf16 ? 2 : 4, pieces = N * es / 16;

@@ -267,6 +267,41 @@ def test_an_index_past_the_adapters_counts_as_none_and_is_reported():
     assert int(c.plan.err) == 4
 
 
+@pytest.mark.parametrize("tokens", [60, 200])
+def test_a_plan_of_another_batch_is_refused_on_the_device(tokens):
+    c = Case(14, tokens, 3, 16, [(64, 128)])
+    other = bs.LoraPlan(tokens + 1, 3)
+    state, y, das, dbs = c.set.state(tokens), torch.full((tokens, 64), 3.0, device="cuda"), torch.full((3, 16, 128), 3.0, device="cuda"), \
+        torch.full((3, 64, 16), 3.0, device="cuda")
+    items, _ = c.set._begin(c.plan, (), state)
+    dx, dy = torch.full((tokens, 128), 3.0, device="cuda"), torch.zeros(tokens, 64, dtype=BF, device="cuda")
+    it = items[0]
+    it.d_a, it.d_b, it.rows, it.cols = c.set._fixed[0]
+    it.d_x, it.x_stride, it.d_h, it.d_y, it.y_stride = c.xd[0].data_ptr(), 128, state[0].data_ptr(), y.data_ptr(), 64
+    it.d_dy, it.dy_stride, it.d_g, it.d_dx, it.dx_stride = dy.data_ptr(), 64, c.set.state(tokens)[0].data_ptr(), dx.data_ptr(), 128
+    it.d_da, it.d_db = das.data_ptr(), dbs.data_ptr()
+    import ctypes
+    batch = bs.LoraBatch(tokens, 3, 16, 0, None, c.set._scales_at, other.data.data_ptr(), other.data.numel(), other.err.data_ptr())
+    st = torch.cuda.current_stream().cuda_stream
+    assert bs.lib.bs_lora_forward(1, items, ctypes.byref(batch), st) == bs.OK
+    assert int(other.err) == 8
+    other.err.zero_()
+    assert bs.lib.bs_lora_backward(1, items, ctypes.byref(batch), 0, st) == bs.OK
+    assert int(other.err) == 8
+    for t in (y, dx, das, dbs):
+        assert torch.all(t == 3)
+
+
+def test_a_new_plan_gives_no_token_an_adapter():
+    c = Case(15, 150, 3, 16, [(64, 128)])
+    plan = bs.LoraPlan(150, 3)
+    y = torch.full((150, 64), 3.0, device="cuda")
+    c.set.forward(plan, c.xd, [y])
+    das, dbs = [torch.full((3, 16, 128), 3.0, device="cuda")], [torch.full((3, 64, 16), 3.0, device="cuda")]
+    c.set.backward(plan, c.xd, [torch.ones(150, 64, dtype=BF, device="cuda")], c.set.state(150), das, dbs)
+    assert torch.all(y == 3) and not das[0].any() and not dbs[0].any() and int(plan.err) == 0
+
+
 def test_tokens_without_an_adapter_are_left_as_they_are():
     # NaN payloads in base survive, and NaN and infinities in x of such tokens reach nothing
     c = Case(6, 40, 3, 16, [(64, 128)])

@@ -16,7 +16,7 @@ def _item(**kw):
 
 
 def _batch(**kw):
-    b = bs.LoraBatch(10, 4, 16, 0, None, None, 256, None)
+    b = bs.LoraBatch(10, 4, 16, 0, None, None, 256, 1 << 20, None)
     for k, v in kw.items():
         setattr(b, k, v)
     return b
@@ -51,7 +51,8 @@ def test_plan_refusals_before_any_launch():
 
 def test_batch_refusals_before_any_launch():
     for b in (_batch(tokens=(1 << 20) + 1), _batch(n_adapters=0), _batch(n_adapters=8193), _batch(rank_max=0), _batch(rank_max=12),
-              _batch(rank_max=136), _batch(reserved=1), _batch(d_plan=None), _batch(d_plan=8), _batch(d_ranks=2), _batch(d_scales=1), _batch(d_err=2)):
+              _batch(rank_max=136), _batch(reserved=1), _batch(d_plan=None), _batch(d_plan=8), _batch(d_ranks=2), _batch(d_scales=1), _batch(d_err=2),
+              _batch(plan_bytes=L.bs_lora_plan_bytes(10, 4) - 1)):
         assert _forward([_item()], b) == bs.E_ARG and _backward([_item()], b) == bs.E_ARG
     assert L.bs_lora_forward(1, None, ctypes.byref(_batch()), None) == bs.E_ARG
     assert L.bs_lora_forward(-1, ctypes.byref(_item()), ctypes.byref(_batch()), None) == bs.E_ARG
