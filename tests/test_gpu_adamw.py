@@ -139,6 +139,31 @@ def test_8_bit_blocks_of_zeros_of_tiny_values_and_with_a_nan():
     assert torch.all(~torch.isfinite(m[1024:]))
 
 
+@pytest.mark.parametrize("pt,gt,master", [(F32, F32, False), (BF, BF, False), (BF, F32, True), (F32, BF, False)])
+def test_8_bit_codes_of_blocks_of_every_magnitude(pt, gt, master):
+    # blocks from 1e-14 to 1e14 (m above 28672 and v above 1e9 among them), a third of each zero and a
+    # few elements far below their block's largest
+    n, betas, seed = 256 * 70 + 100, (0.9, 0.999), 7
+    rng = np.random.default_rng(17)
+    p, g = _tensor(n, pt, rng, 1.0), _tensor(n, gt, rng, 1.0)
+    mc, vc, ms, vs = np.zeros(n, np.uint8), np.zeros(n, np.uint8), np.zeros(-(-n // 256), np.float32), np.zeros(-(-n // 256), np.float32)
+    opt = bs.AdamW([p], [g], lr=1e-3, betas=betas, bits=8, seed=seed, masters=[p.float()] if master else None)
+    for t in range(1, 4):
+        x = rng.standard_normal(n) * np.repeat(10.0 ** rng.uniform(-14, 14, ms.size), 256)[:n]
+        x = np.where(rng.random(n) < 0.01, x * 1e-5, x) * (rng.random(n) > 1 / 3)
+        g.copy_(torch.from_numpy(x.astype(np.float32)))
+        opt.step()
+        torch.cuda.synchronize()
+        m0, v0 = A.decode(mc, ms, "m"), A.decode(vc, vs, "v")
+        _, m, v = A.step(np.zeros(n, np.float32), _np(g), m0, v0, t, 0.0, betas, 1e-8, 0.0, 1.0, np.float32)
+        um, uv = A.random_bits(seed, t, 0, n)
+        mc, ms = A.encode(m, um, "m")
+        vc, vs = A.encode(v, uv, "v")
+        for name, got, want in (("mc", opt.exp_avg, mc), ("vc", opt.exp_avg_sq, vc), ("ms", opt.exp_avg_scale, ms), ("vs", opt.exp_avg_sq_scale, vs)):
+            got = got[0].cpu().numpy()
+            assert np.array_equal(got, want), (t, name, np.flatnonzero(got != want)[:5])
+
+
 def test_v_in_8_bits_follows_its_mean():
     # with rounding to nearest, v would stop far below the mean square of the gradients
     n, steps = 1 << 14, 3000
