@@ -83,3 +83,17 @@ def test_two_items_of_one_call_may_not_write_the_same_memory():
     dx = dict(d_dx=1 << 25, dx_stride=128)
     for kw in (dict(dx_stride=136), dict(type=1), dict(d_dx_base=1 << 26, dx_base_stride=128)):
         assert _backward([_item(**dx), _item(**{**other, **dx, **kw})]) == bs.E_ARG, kw
+
+
+def test_what_a_call_writes_may_not_be_what_it_reads():
+    square = dict(rows=128, y_stride=128, dy_stride=128, type=1)
+    for kw in (dict(d_y=1024), dict(d_base=4096, base_stride=136)):
+        assert _forward([_item(**{**square, **kw})]) == bs.E_ARG, kw
+    other = dict(d_h=1 << 20, d_y=1 << 21, d_g=1 << 22, d_da=1 << 23, d_db=1 << 24, d_x=1 << 27, d_dy=1 << 28)
+    for kw in (dict(d_x=4096), dict(d_base=4096, base_stride=64)):
+        assert _forward([_item(), _item(**{**other, **kw})]) == bs.E_ARG, kw
+    dx = dict(dx_stride=128, type=1)
+    for kw in (dict(d_dx=1024), dict(d_dx=8192), dict(d_dx=1 << 25, d_dx_base=1 << 25, dx_base_stride=136), dict(d_g=2048)):
+        assert _backward([_item(**{**square, **dx, **kw})]) == bs.E_ARG, kw
+    for kw in (dict(d_x=1 << 25), dict(d_dy=1 << 25), dict(d_h=16384)):
+        assert _backward([_item(**dx, d_dx=1 << 25), _item(**{**other, **kw})]) == bs.E_ARG, kw
