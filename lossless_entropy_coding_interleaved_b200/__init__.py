@@ -830,11 +830,11 @@ class LoraAdapters:
     def _rows(self, t, width, dtype, what, tokens):
         """(address, stride) of a [tokens, width] tensor of contiguous rows."""
         if t.dtype is dtype and t.shape == (tokens, width) and t.get_device() == self._index:
-            if t.is_contiguous() or tokens <= 1:
+            if t.is_contiguous():
                 return t.data_ptr(), width
             s0, s1 = t.stride()
             if s1 == 1:
-                return t.data_ptr(), s0
+                return t.data_ptr(), s0 if tokens > 1 else width
         raise BsError(E_ARG, "lora", f"{what}: [{tokens}, {width}] of {dtype}, rows contiguous, on the adapters' device")
 
     def _out(self, t, base, width, what, tokens):

@@ -413,6 +413,20 @@ def test_empty_batch():
     assert torch.all(das[0] == 3) and torch.all(dbs[0] == 3)
 
 
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_rows_that_are_not_contiguous_are_refused(tokens):
+    c = Case(5, tokens, 2, 8, [(64, 64)])
+    wide = lambda dt: torch.zeros(64, 2 * tokens, dtype=dt, device="cuda")[:, :tokens].t()  # noqa: E731
+    x, y = c.xd, [torch.zeros(tokens, 64, device="cuda")]
+    das, dbs = [torch.zeros(2, 8, 64, device="cuda")], [torch.zeros(2, 64, 8, device="cuda")]
+    state = c.set.state(tokens)
+    for call in (lambda: c.set.forward(c.plan, [wide(BF)], y), lambda: c.set.forward(c.plan, x, [wide(F32)]),
+                 lambda: c.set.forward(c.plan, x, y, [wide(F32)]), lambda: c.set.backward(c.plan, x, [wide(BF)], state, das, dbs)):
+        with pytest.raises(bs.BsError) as e:
+            call()
+        assert e.value.code == bs.E_ARG
+
+
 def test_binding_refusals():
     c = Case(12, 10, 2, 8, [(16, 64)])
     y = torch.zeros(10, 16, device="cuda")
