@@ -263,6 +263,15 @@ def _on(index: int, what: str, fn, *args, stream=None):
         _check(r, what)
 
 
+def _made_on(stream, index: int, make):
+    """make()'s new tensors, belonging to the stream that a call is enqueued on: their memory goes back to
+    that stream's later work when they are freed, not to another's that may run before the call."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=index)):
+        return make()
+
+
 def _host_bytes(container) -> np.ndarray:
     if isinstance(container, np.ndarray):
         a = np.ascontiguousarray(container.reshape(-1).view(np.uint8))
@@ -869,7 +878,7 @@ class LoraAdapters:
 
     def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
         n, T = self._n, plan.tokens
-        state = self.state(T) if state is None else state
+        state = _made_on(stream, self._index, lambda: self.state(T)) if state is None else state
         ys = [None] * n if ys is None else ys
         bases = ys if bases is None else bases
         items, batch = self._begin(plan, (xs, ys, bases, state), state)
@@ -887,7 +896,7 @@ class LoraAdapters:
 
     def backward(self, plan: LoraPlan, xs, dys, state, das, dbs, dxs=None, dx_bases=None, work=None, accumulate: bool = False,
                  stream=None):
-        work = self.state(plan.tokens) if work is None else work
+        work = _made_on(stream, self._index, lambda: self.state(plan.tokens)) if work is None else work
         dxs = [None] * self._n if dxs is None else dxs
         dx_bases = [None] * self._n if dx_bases is None else dx_bases
         items, batch = self._begin(plan, (xs, dys, das, dbs, dxs, dx_bases, state, work), (*state, *work))
@@ -1050,10 +1059,11 @@ class AdamW:
 
     def read_states(self, ms=None, vs=None, stream=None):
         """The moments as float32 lists, (exp_avgs, exp_avg_sqs). 32-bit moments are returned as they
-        stand; 8-bit ones are decoded (bs_adamw_read_states) into ms and vs, or into new tensors."""
+        stand; 8-bit ones are decoded (bs_adamw_read_states) into ms and vs, or into new tensors of the stream."""
         if self.bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        ms, vs = ([torch.empty(k, dtype=torch.float32, device=self.device) for k in self._sizes] if t is None else list(t) for t in (ms, vs))
+        new = lambda: [torch.empty(k, dtype=torch.float32, device=self.device) for k in self._sizes]  # noqa: E731
+        ms, vs = (_made_on(stream, self._index, new) if t is None else list(t) for t in (ms, vs))
         index, f32, at = self._index, torch.float32, []
         for ts in (ms, vs):
             if len(ts) != self._n:

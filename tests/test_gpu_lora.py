@@ -398,6 +398,30 @@ def test_on_another_stream():
     _equal(y, L.forward(x, c.idx, a, b, c.scales, c.ranks, np.zeros((100, 264)))[0], F32, 0)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_state_of_a_call_on_another_stream_is_not_given_away_before_it_has_run(raw):
+    c = Case(31, 300, 2, 16, [(264, 520)])  # the tiled kernels: h goes through the state
+    s, x = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    y, y2 = (torch.zeros(300, 264, device="cuda") for _ in range(2))
+    size = c.set.state(300)[0].numel()
+    s.wait_stream(torch.cuda.current_stream())
+    taken = []
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            x = x @ x * 1e-3
+    for out in (y, y2):
+        c.set.forward(c.plan, c.xd, [out], stream=s.cuda_stream if raw else s)
+        taken += [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        with torch.cuda.stream(s):
+            x = x @ x * 1e-3
+    torch.cuda.synchronize()
+    xs, a, b = c.f64(0)
+    want = L.forward(xs, c.idx, a, b, c.scales, c.ranks, np.zeros((300, 264)))[0]
+    _equal(y, want, F32, 0)
+    _equal(y2, want, F32, 0)
+    assert all(bool((t == 255).all()) for t in taken)  # nor is memory written that others have
+
+
 def test_more_projections_than_one_launch_holds():
     c = Case(10, 9, 2, 8, [(16, 64)] * 21)
     check_forward(c, F32)
