@@ -801,8 +801,7 @@ __global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_
     const uint32_t tmem = s_tmem;
     if (t_begin == t_end) { // no tokens: zero, or as it is
         if (warp == kIssueWarp) tmem_free(tmem, kTmem);
-        if (!planned) return;
-        if (p.accumulate) {
+        if (!planned || p.accumulate) {
             if (p.beside_expand) kernels_before_done();
             return;
         }
