@@ -15,6 +15,7 @@ The byte layout is the BF16RANS container, version 2.
 """
 from __future__ import annotations
 
+import array
 import bisect
 import ctypes
 import os
@@ -1000,7 +1001,7 @@ class AdamW:
             it.d_m_scale, it.d_v_scale = ptr(self.exp_avg_scale, k), ptr(self.exp_avg_sq_scale, k)
             it.n, it.param_type, it.grad_type = sizes[k], _TYPES[self.params[k].dtype], _TYPES[self.grads[k].dtype]
             it.weight_decay = decay[k]
-        self._n, self._sizes, self._index, self._pointers = n, sizes, self.params[0].get_device(), ctypes.c_void_p * n
+        self._n, self._sizes, self._index = n, sizes, self.params[0].get_device()
         self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
         self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
@@ -1064,14 +1065,14 @@ class AdamW:
             return self.exp_avg, self.exp_avg_sq
         new = lambda: [torch.empty(k, dtype=torch.float32, device=self.device) for k in self._sizes]  # noqa: E731
         ms, vs = (_made_on(stream, self._index, new) if t is None else list(t) for t in (ms, vs))
-        index, f32, at = self._index, torch.float32, []
-        for ts in (ms, vs):
-            if len(ts) != self._n:
-                raise BsError(E_ARG, "adamw", "read_states: one tensor for each parameter")
-            for t, k in zip(ts, self._sizes):
-                if t.numel() != k or t.dtype is not f32 or t.get_device() != index or not t.is_contiguous():
-                    raise BsError(E_ARG, "adamw", "read_states: a contiguous float32 tensor of each parameter's size")
-                at.append(t.data_ptr())
-        pm, pv = self._pointers(*at[:self._n]), self._pointers(*at[self._n:])
+        T, n, every = torch.Tensor, self._n, [*ms, *vs]  # one look at a time at all tensors: several hundred are usual
+        if len(ms) != n or len(vs) != n:
+            raise BsError(E_ARG, "adamw", "read_states: one tensor for each parameter")
+        if not (list(map(T.numel, every)) == self._sizes * 2 and set(map(T.dtype.__get__, every)) == {torch.float32} and
+                set(map(T.get_device, every)) == {self._index} and all(map(T.is_contiguous, every))):
+            raise BsError(E_ARG, "adamw", "read_states: a contiguous float32 tensor of each parameter's size")
+        at = array.array("Q", map(T.data_ptr, every))
+        pm = at.buffer_info()[0]
+        pv = pm + 8 * n
         _on(self._index, "adamw_read_states", lib.bs_adamw_read_states, self._n, self._items, pm, pv, stream=stream)
         return ms, vs

@@ -727,35 +727,41 @@ struct OuterParams {
 };
 // Threads that add up, that load; a warp more issues. A stage holds 64 tokens: their columns (MN-major)
 // and the three parts of their ranks side by side (MN-major). Up to rank 32: 128 columns a CTA, a
-// thread each, and 2 or 3 CTAs an SM, since batches of few tokens per adapter are all latency; rank
-// 64: 256 columns; rank 128: 128 columns, two threads each, 64 ranks a thread.
+// thread each; rank 64: 256 columns; rank 128: 128 columns, two threads each, 64 ranks a thread.
 template <int R>
 constexpr uint32_t outer_out = R > 32 ? 256 : 128;
 template <int R>
 constexpr uint32_t outer_cols = R == 64 ? 256 : 128;
 template <int R>
 constexpr uint32_t outer_load = R > 32 ? 256 : 128;
-constexpr uint32_t kOuterTok = 64, kOuterStages = 3;
+constexpr uint32_t kOuterTok = 64;
+// Up to rank 32 a CTA is small and an adapter's tokens are often few, so that its start and end are what
+// it costs: 4 CTAs of 2 stages an SM (3 at rank 32, with one sum in tensor memory). 1003 tokens of 36
+// adapters, gate and up projections: 113 us at rank 16, 220 at rank 32; with 2 CTAs of 3 stages 182
+// and 283. 8192 tokens of 2 adapters, gate: 53 and 68 us, against 59 and 78.
+template <int R>
+constexpr uint32_t outer_stages = R <= 32 ? 2 : 3;
+constexpr uint32_t outer_ctas(uint32_t R) { return R <= 16 ? 4 : R <= 32 ? 3 : 1; }
 template <int R>
 constexpr uint32_t outer_threads = outer_out<R> + outer_load<R> + 32;
 template <int R>
 __host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 8192 * ((3 * R + 63) / 64); }
 template <int R>
-constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(kOuterStages * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
+constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(outer_stages<R> * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
 constexpr uint32_t kOuterFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
 // Sums in tensor memory: 128 columns x the 3 parts' ranks, beside each other (one matrix instruction
 // reads the columns once for all parts; one for each part read them three times, and 8192 tokens at
-// rank 64 took 135 us, bound by shared memory, against 86 to 93). Up to rank 32 two of them take turns;
+// rank 64 took 135 us, bound by shared memory, against 86 to 93). At rank 16 two of them take turns;
 // rank 64 has one for each 128 of its 256 columns, which are added up two stages apart, so that one
-// half's matrix instructions go on meanwhile; rank 128 has one.
+// half's matrix instructions go on meanwhile; ranks 32 and 128 have one.
 template <int R>
-constexpr uint32_t outer_accs = R > 64 ? 1 : 2;
+constexpr uint32_t outer_accs = R == 16 || R == 64 ? 2 : 1;
 
 template <int R>
-__global__ void __launch_bounds__(outer_threads<R>, R <= 32 ? 2 : 1) lora_outer_kernel(const __grid_constant__ OuterParams p) {
+__global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_kernel(const __grid_constant__ OuterParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr uint32_t S = kOuterStages, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kAccs = outer_accs<R>, kWide = 3 * R;
-    constexpr uint32_t kTmem = R == 16 ? 128 : R == 32 ? 256 : 512; // at least kAccs * kWide, a power of two
+    constexpr uint32_t S = outer_stages<R>, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kAccs = outer_accs<R>, kWide = 3 * R;
+    constexpr uint32_t kTmem = R <= 32 ? 128 : 512; // at least kAccs * kWide, a power of two
     constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
     constexpr uint32_t kOuterLoad = outer_load<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
@@ -1079,7 +1085,7 @@ bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu
     const uint32_t cols = R == 64 ? outer_cols<64> : outer_cols<128>;
     uint32_t ctas = 0;
     for (uint32_t k = 0; k < jobs; ++k) ctas += (p.job[k].width + cols - 1) / cols;
-    p.split = split_for(uint64_t(ctas) * p.b.n, p.b.tokens / p.b.n / kOuterTok, 2ull * gpu.sms);
+    p.split = split_for(uint64_t(ctas) * p.b.n, p.b.tokens / p.b.n / kOuterTok, uint64_t(std::max(2u, outer_ctas(R))) * gpu.sms);
     const dim3 grid(ctas * p.split, p.b.n);
     switch (R) {
     case 16: return launch<lora_outer_kernel<16>, outer_threads<16>>(grid, outer_smem<16>(), p.split, gpu, p);
