@@ -424,7 +424,10 @@ struct ExpandParams {
 };
 // threads that write and that load; a warp more issues
 constexpr uint32_t kExpandOut = 256, kExpandLoad = 128, kExpandThreads = kExpandOut + kExpandLoad + 32;
-constexpr uint32_t kRowBytes = 256, kRowPitch = kRowBytes + 16; // of a block's rows of base, which become those of out
+// A block's rows of base, which become those of out. The 16-byte piece c of row r stands at piece
+// (c & 8) | ((c ^ r) & 7): 8 lanes that take one piece of 8 rows, or 8 pieces of one, meet no bank twice.
+constexpr uint32_t kRowBytes = 256;
+__device__ __forceinline__ uint32_t row_piece(uint32_t r, uint32_t c) { return ((c & 8u) | ((c ^ r) & 7u)) << 4; }
 template <bool BF16>
 constexpr uint32_t expand_cols = kRowBytes / (BF16 ? 2 : 4); // columns of a block
 // Buffers of base and of sums: as many as fit beside the operands, of which rank 128 has twice the bytes.
@@ -438,7 +441,7 @@ template <int R, bool BF16>
 __host__ __device__ constexpr uint32_t expand_w() { return expand_cols<BF16> * 128 * atoms_of<R>; }
 template <int R, bool BF16>
 constexpr uint32_t expand_smem() {
-    return 1024 + (BF16 ? 2 : 3) * 16384 * atoms_of<R> + 2 * expand_w<R, BF16>() + expand_bufs<R> * kTile * kRowPitch;
+    return 1024 + 3 * 16384 * atoms_of<R> + 2 * expand_w<R, BF16>() + expand_bufs<R> * kTile * kRowBytes;
 }
 
 // A place in the sequence of (job, tile, block) that the CTAs share out.
@@ -455,15 +458,16 @@ struct ExpandAt {
 // instructions for each 32 of them), 143 us with a bulk copy for each row's 256 or 128 bytes, which
 // the copy engine takes 14 cycles each for.
 // WT: the weights' column index is the contiguous one (A), else the rank index is (B).
-// BF16: base and out are BF16; h then enters as its two upper parts (16 bits), whose loss is 2^-17
-// where the output's own rounding is 2^-9. FP32 outputs take all three (24 bits).
+// BF16: base and out are BF16. h enters as all of its three parts (24 bits) here too: with the upper two
+// an output could be off by 2^-17 of the products' magnitudes, which is more than its own rounding
+// where the products cancel.
 template <int R, bool WT, bool BF16>
 __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_bar[4 + 3 * expand_bufs<R>];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    constexpr uint32_t kParts = BF16 ? 2 : 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
+    constexpr uint32_t kParts = 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
     constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -551,10 +555,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 const uint32_t buf = turn % kBufs, n = n0 + piece * (16 / es);
                 if (turn >= kBufs && !bar_wait(bar_free + 8 * buf, (turn / kBufs - 1) & 1u, abort_flag)) break;
                 if (job.base && n < N) {
-                    const uint32_t dst = sRow + (buf * kTile + (t0 >> 4)) * kRowPitch + 16 * piece;
+                    const uint32_t dst = sRow + (buf * kTile + (t0 >> 4)) * kRowBytes + row_piece(t0 >> 4, piece);
 #pragma unroll
                     for (uint32_t i = 0; i < 16; ++i)
-                        cp_async16_if(row[i] != ~0ull, dst + 8 * i * kRowPitch, job.base + (row[i] + n) * es, 16u);
+                        cp_async16_if(row[i] != ~0ull, dst + 8 * i * kRowBytes, job.base + (row[i] + n) * es, 16u);
                 }
                 bar_arrive_copies(bar_base + 8 * buf);
                 ++turn;
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             }
             if (!left_out(job, rank)) {
                 const uint32_t buf = turn % kBufs, n = at.block * kCols + half * kHalf + (lane & 7u) * (16 / es);
-                uint8_t* mine = rows + (buf * kTile + r0) * kRowPitch + half * (kRowBytes / 2);
+                uint8_t* mine = rows + (buf * kTile + r0) * kRowBytes; // the warp's rows
                 if (!bar_wait(bar_base + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
                 if (!bar_wait(bar_d + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
                 fence_after();
@@ -668,10 +672,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                     for (uint32_t c = 0; c < kHalf; c += 16) {
                         uint32_t d[16] = {};
                         if (rank) tmem_ld16(d, tmem + (r0 << 16) + buf * kCols + half * kHalf + c);
-                        uint4* at16 = reinterpret_cast<uint4*>(mine + lane * kRowPitch + c * es);
 #pragma unroll
                         for (uint32_t q = 0; q < es; ++q) { // 16 bytes: 8 BF16 or 4 FP32
-                            uint4 v = job.base ? at16[q] : make_uint4(0, 0, 0, 0);
+                            uint4* at16 = reinterpret_cast<uint4*>(mine + lane * kRowBytes + row_piece(lane, 8 * half + c * es / 16 + q));
+                            uint4 v = job.base ? *at16 : make_uint4(0, 0, 0, 0);
                             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (uint32_t i = 0; i < 4; ++i) {
@@ -681,17 +685,18 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                                 else
                                     w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(d[4 * q + i]));
                             }
-                            at16[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                            *at16 = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                 fence_before();
                 __syncwarp();
                 if (n < job.width) {
-                    const uint8_t* from = mine + (lane >> 3) * kRowPitch + (lane & 7u) * 16;
                     uint8_t* to = job.out + uint64_t(n) * es;
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i)
-                        if (row[i] != ~0ull) *reinterpret_cast<uint4*>(to + row[i] * es) = *reinterpret_cast<const uint4*>(from + 4 * i * kRowPitch);
+                    for (uint32_t i = 0; i < 8; ++i) {
+                        const uint32_t r = (lane >> 3) + 4 * i;
+                        if (row[i] != ~0ull) *reinterpret_cast<uint4*>(to + row[i] * es) = *reinterpret_cast<const uint4*>(mine + r * kRowBytes + row_piece(r, 8 * half + (lane & 7u)));
+                    }
                 }
                 __syncwarp();
                 bar_arrive(bar_free + 8 * buf);
