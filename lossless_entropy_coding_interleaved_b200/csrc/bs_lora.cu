@@ -43,7 +43,7 @@ namespace cg = cooperative_groups;
 // the same bucket are ranked by their lane. No order depends on timing.
 // 7 us for up to 333 tokens, 12 us for 8192, alone on the GPU: latency, and the steps of one CTA. The
 // next kernel's start is beside its end.
-__global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restrict__ idx, uint32_t tokens, uint32_t n,
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* idx, uint32_t tokens, uint32_t n,
                                                          uint32_t* plan, uint32_t warps, uint32_t* err) {
     extern __shared__ uint32_t sm[];
     __shared__ uint32_t s_scan[3][32], s_carry[3];
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     const uint32_t b0 = min(warp * per, tokens), b1 = min(b0 + per, tokens);
     bool bad = false;
     auto bucket = [&](uint32_t t) {
-        const int32_t a = __ldg(idx + t);
+        const int32_t a = idx[t];
         bad |= a >= static_cast<int32_t>(n);
         return a < 0 || a >= static_cast<int32_t>(n) ? n : static_cast<uint32_t>(a);
     };
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     fence_before();
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
+    const float scale = p.b.scales ? p.b.scales[a] : 1.f;
     const uint32_t rows = kTile / p.split; // rows that this CTA adds up and writes
     for (uint32_t i = tid; i < rows * (R / 8); i += shrink_threads<R>) {
         const uint32_t r = part * rows + i / (R / 8), c = 8 * (i % (R / 8));

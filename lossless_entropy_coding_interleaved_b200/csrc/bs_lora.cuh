@@ -72,13 +72,15 @@ __device__ __forceinline__ uint4 plan_head(const Batch& b, bool* good = nullptr)
 }
 __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
     if (!b.ranks) return b.rank_max;
-    const int32_t r = __ldg(b.ranks + a);
+    const int32_t r = b.ranks[a];
     return r < 0 ? 0u : min(static_cast<uint32_t>(r), b.rank_max);
 }
 
 // Programmatic dependent launch: the next kernel of the stream may be scheduled once every CTA of this
 // one has started, and takes over the SMs that it leaves; this one goes on when the kernels before it
-// have completed and what they wrote is visible. Nothing global is read or written before.
+// have completed and what they wrote is visible. Nothing global is read or written before, and nothing by
+// ld.global.nc (or __ldg), which is for data that stays as it is from the kernel's start to its end: the kernel
+// before, which may still run then, can be the one that writes it (x may be the y of the call before).
 // EARLY false: the next kernel is let go only after that wait, so that it knows the kernels before this
 // one complete without a wait of its own.
 __device__ __forceinline__ void kernels_before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

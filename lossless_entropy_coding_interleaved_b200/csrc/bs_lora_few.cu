@@ -33,16 +33,16 @@ namespace cg = cooperative_groups;
 
 constexpr uint32_t kWarps = kFewThreads / 32, kSlices = kFewCluster * kWarps;
 
-__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // WORDS words from p, where `on`; what stands in d is undefined where not.
 template <int WORDS>
 __device__ __forceinline__ void load_if(uint32_t* d, const uint16_t* p, uint32_t on) {
     if constexpr (WORDS == 2)
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n @p ld.global.nc.v2.u32 {%0, %1}, [%2];\n}"
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n @p ld.global.v2.u32 {%0, %1}, [%2];\n}"
                      : "=r"(d[0]), "=r"(d[1]) : "l"(p), "r"(on));
     else
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
                      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "l"(p), "r"(on));
 }
 
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
         return;
     }
     const uint32_t rank = rank_of(p.b, a);
-    const float scale = p.b.scales ? __ldg(p.b.scales + a) : 1.f;
+    const float scale = p.b.scales ? p.b.scales[a] : 1.f;
     const uint16_t* A = job.a + uint64_t(a) * rm * K;
     const uint16_t* B = job.b + uint64_t(a) * rm * N;
     // ---- A x: the warp's columns, 64 at a time; lane (g, q) has row g (and g + 8) of each 16 ranks,

@@ -1,5 +1,7 @@
 """CPU checks of the adapters' entry points: sizes, and refusals before any launch."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -97,3 +99,15 @@ def test_what_a_call_writes_may_not_be_what_it_reads():
         assert _backward([_item(**{**square, **dx, **kw})]) == bs.E_ARG, kw
     for kw in (dict(d_x=1 << 25), dict(d_dy=1 << 25), dict(d_h=16384)):
         assert _backward([_item(**dx, d_dx=1 << 25), _item(**{**other, **kw})]) == bs.E_ARG, kw
+
+
+def _source(name):
+    src = open(os.path.join(os.path.dirname(bs.__file__), "csrc", name)).read()
+    return re.sub(r"//[^\n]*", "", src)
+
+
+@pytest.mark.parametrize("name", ["bs_lora.cuh", "bs_lora_tc.cuh", "bs_lora.cu", "bs_lora_few.cu", "bs_fw_gemv.cu"])
+def test_kernels_that_start_beside_the_one_before_read_nothing_as_constant(name):
+    # ld.global.nc is undefined for data that is written while the kernel runs, and a programmatic dependent
+    # launch runs from before the end of the kernel that may write its x, its index or its weights
+    assert not re.search(r"__ldg|ld\.global(\.\w+)*\.nc|__ldlu|__ldcs\b", _source(name))
