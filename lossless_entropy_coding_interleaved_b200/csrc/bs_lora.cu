@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* idx, uin
     extern __shared__ uint32_t sm[];
     __shared__ uint32_t s_scan[3][32], s_carry[3];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, nb = n + 1; // buckets
-    after_kernel_before();
+    next_kernel_may_start();
+    kernels_before_done();
     uint32_t* hist = sm;                    // [warps][nb]
     uint32_t* first = hist + warps * nb;    // [nb + 1] first place of each bucket
     uint32_t* t128 = first + nb + 1;        // [nb + 1] first tile of each bucket
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     }
     constexpr uint32_t kIssueWarp = (kShrinkOut + kShrinkLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
-    after_kernel_before(); // the above goes on beside the end of the kernel before
+    kernels_before_done(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t tiles = plan_head(p.b).x;
     const uint4 tl = reinterpret_cast<const uint4*>(p.b.plan + o.tiles)[tile];
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
+    next_kernel_may_start();
     if (tile >= tiles) { // the whole cluster
         if (warp == kIssueWarp) tmem_free(tmem, kTmem);
         return;
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     }
     constexpr uint32_t kIssueWarp = (kExpandOut + kExpandLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
-    after_kernel_before<false>(); // the above goes on beside the end of the kernel before
+    kernels_before_done(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const uint32_t tiles = plan_head(p.b).y;
     const uint4* tile_of = reinterpret_cast<const uint4*>(p.b.plan + o.tiles);
@@ -523,6 +525,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
+    next_kernel_may_start(); // outer, of the same call, relies on every CTA of this one having waited above
     volatile int* abort_flag = &s_abort;
     // What a role needs of a tile: its adapter's rank (0: base as it is), and whether nothing at all is
     // to be done for it. Units left out take no turn of the buffers: every role counts the same ones.
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
     }
     constexpr uint32_t kIssueWarp = (kOuterOut + kOuterLoad) / 32;
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&s_tmem), kTmem);
-    if (!p.beside_expand) after_kernel_before(); // the above goes on beside the end of the kernel before
+    if (!p.beside_expand) kernels_before_done(); // the above goes on beside the end of the kernel before
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     bool planned;
     plan_head(p.b, &planned);
@@ -812,6 +815,7 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
+    if (!p.beside_expand) next_kernel_may_start();
     if (t_begin == t_end) { // no tokens: zero, or as it is
         if (warp == kIssueWarp) tmem_free(tmem, kTmem);
         if (!planned || p.accumulate) {
@@ -1021,7 +1025,7 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see after_kernel_before
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see kernels_before_done
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -1142,7 +1146,7 @@ extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see after_kernel_before
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization; // see kernels_before_done
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

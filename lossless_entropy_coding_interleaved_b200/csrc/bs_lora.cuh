@@ -81,15 +81,13 @@ __device__ __forceinline__ uint32_t rank_of(const Batch& b, uint32_t a) {
 // have completed and what they wrote is visible. Nothing global is read or written before, and nothing by
 // ld.global.nc (or __ldg), which is for data that stays as it is from the kernel's start to its end: the kernel
 // before, which may still run then, can be the one that writes it (x may be the y of the call before).
-// EARLY false: the next kernel is let go only after that wait, so that it knows the kernels before this
-// one complete without a wait of its own.
+// A kernel that takes tensor memory lets the next one go only once all of its CTA has seen tcgen05.alloc
+// return (next_kernel_may_start behind that barrier). The next kernel's CTAs take tensor memory too, and hold it
+// while they wait for this kernel to complete: if a CTA of this one still had to wait for its own share then, both
+// could wait for good. So whenever a kernel's CTA is resident, those of the kernels before it have
+// what they need.
 __device__ __forceinline__ void kernels_before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <bool EARLY = true>
-__device__ __forceinline__ void after_kernel_before() {
-    if (EARLY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    kernels_before_done();
-    if (!EARLY) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // The decoding kernel (bs_lora_few.cu): a cluster takes up to kFew tokens of one adapter through
 // both products.

@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
     const uint32_t cta = blockIdx.x % kFewCluster, part = blockIdx.x / kFewCluster % p.split, tile = blockIdx.x / kFewCluster / p.split;
     const FewJob& job = p.job[blockIdx.y];
     const uint32_t N = job.rows, K = job.cols, rm = p.b.rank_max;
-    after_kernel_before();
+    next_kernel_may_start();
+    kernels_before_done();
     const PlanAt o = plan_at(p.b.tokens, p.b.n);
     const FewTile* entry = reinterpret_cast<const FewTile*>(p.b.plan + o.few) + tile;
     const uint32_t a = entry->bucket, first = entry->first, count = entry->count, tok_g = entry->token[g];

@@ -111,3 +111,19 @@ def test_kernels_that_start_beside_the_one_before_read_nothing_as_constant(name)
     # ld.global.nc is undefined for data that is written while the kernel runs, and a programmatic dependent
     # launch runs from before the end of the kernel that may write its x, its index or its weights
     assert not re.search(r"__ldg|ld\.global(\.\w+)*\.nc|__ldlu|__ldcs\b", _source(name))
+
+
+def test_kernels_let_the_next_one_go_only_once_they_hold_their_tensor_memory():
+    # else a CTA of the next kernel could take the tensor memory that one of this kernel still waits for, and
+    # wait for this kernel itself: in every kernel the release stands behind the barrier that follows the
+    # allocation, for all threads, and nowhere else
+    kernels = [k for k in re.split(r"(?=__global__)", _source("bs_lora.cu") + _source("bs_lora_few.cu")) if k.startswith("__global__")]
+    assert len(kernels) == 5
+    taking = [k for k in kernels if "tmem_alloc(" in k]
+    assert len(taking) == 3
+    for k in taking:
+        assert k.count("next_kernel_may_start();") == 1 and "launch_dependents" not in k
+        before = k[:k.index("next_kernel_may_start();")]
+        assert before.index("tmem_alloc(") < before.index("kernels_before_done();") < before.rindex("__syncthreads();")
+        assert re.search(r"__syncthreads\(\);\s*fence_after\(\);\s*const uint32_t tmem = s_tmem;\s*(if \(!p\.beside_expand\) )?$", before)
+    assert all("launch_dependents" not in _source(f) for f in ("bs_lora.cu", "bs_lora_few.cu", "bs_lora_tc.cuh"))
