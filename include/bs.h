@@ -590,7 +590,8 @@ typedef struct {
     float lr;
     float clip;        /* factor on every gradient; bs_grad_norm writes it */
     int32_t step;      /* completed steps: bs_adamw leaves its step's number */
-    uint32_t skip;     /* nonzero: bs_adamw changes nothing, the step count included */
+    uint32_t skip;     /* nonzero: bs_adamw changes nothing, the step count included; into other buffers it copies
+                        * what the items hold, bit for bit */
     float norm;        /* of the last bs_grad_norm */
     uint32_t arrived;  /* internal, 0 between calls */
     uint32_t reserved[2];
@@ -614,7 +615,8 @@ bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs
                        size_t scratch_bytes, void* stream);
 /* One step over every item. to: NULL, and the items are updated in place; or n items whose d_param,
  * d_master, d_m, d_v and scales receive what the step makes of those of items, which stay as they are
- * (with the same n, param_type and kinds of buffers). So the weights of a step can be coded for a
+ * (with the same n, param_type and kinds of buffers); a step that is left out (d_ctl->skip) copies them
+ * there, so that the next step may start from `to` either way. So the weights of a step can be coded for a
  * checkpoint (bs_encoder_run needs them unchanged until bs_encoder_emit) while the next steps run. Pointers need their type's alignment (16 bytes, 8 for codes, are faster).
  * Written buffers must not overlap each other nor anything that is read, but for an item's own in a
  * step in place. Two calls that share d_ctl must be ordered (one stream, or events). Enqueued on

@@ -1037,7 +1037,8 @@ class AdamW:
     def twin(self, params=None, masters=None, states=None) -> "AdamW":
         """A second set of parameters, masters and moments (new tensors where none are given) for the
         same gradients and the same ctl: step(into=twin) leaves this handle's as they are, to be
-        coded or compared, and the twin's next step, into this one, goes on from there."""
+        coded or compared, and the twin's next step, into this one, goes on from there. A step that is
+        left out (its norm was not finite) leaves the twin with this handle's values."""
         new = lambda ts, given: (None if ts is None else list(given) if given is not None else [torch.empty_like(t) for t in ts])  # noqa: E731
         if states is None:
             m, v, ms, vs = (new(ts, None) for ts in (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))

@@ -91,6 +91,7 @@ struct OptParams {
     uint32_t n_items, groups, per_cta; // groups of the launch, groups a CTA takes
     uint32_t last;                     // the call's last launch
     uint32_t step;                     // the step's number, 0: one more than ctl->step
+    uint32_t into;                     // results go into other buffers than those that are read
     float b1, b2, c1, c2, eps;         // c = 1 - b, rounded from 64 bits
     double log_b1, log_b2;
     uint64_t seed;
@@ -431,6 +432,44 @@ __device__ __forceinline__ void whole_groups(const OptItem& it, const StepConst&
     }
 }
 
+// 8 elements of a lane, of es bytes each, as they are.
+__device__ __forceinline__ void copy8(uint8_t* to, const uint8_t* from, uint64_t at, uint32_t es, bool full, uint32_t cnt) {
+    to += at * es;
+    from += at * es;
+    if (full) {
+        if (es == 1) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+        else
+            for (uint32_t i = 0; i < es / 2; ++i) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
+    } else {
+        for (uint32_t i = 0; i < cnt; ++i)
+            if (es == 1) to[i] = from[i];
+            else if (es == 2) reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(from)[i];
+            else reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(from)[i];
+    }
+}
+// A step that is left out but has buffers of its own for its results: they receive everything as it was,
+// so that the caller may go on from them. Not inlined: the step's registers are not these.
+template <int CAP, int BITS>
+__device__ __noinline__ void copy_all(const OptParams<CAP>& p) {
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    for (uint32_t g0 = blockIdx.x * p.per_cta; g0 < p.groups; g0 += gridDim.x * p.per_cta) {
+        const uint32_t g1 = min(g0 + p.per_cta, p.groups);
+        int k = item_of(p, g0, 0);
+        for (uint32_t g = g0 + warp; g < g1; g += kWarps) {
+            if (k + 1 < static_cast<int>(p.n_items) && p.item[k + 1].group_begin <= g) k = item_of(p, g, k);
+            const OptItem& it = p.item[k];
+            const uint64_t block = g - it.group_begin, at = block * kBlock + 8u * lane;
+            const uint32_t cnt = at < it.n ? static_cast<uint32_t>(it.n - at < 8 ? it.n - at : 8) : 0u;
+            const bool full = cnt == 8 && (it.flags & kVec);
+            copy8(it.to.p, it.p, at, it.flags & kP16 ? 2 : 4, full, cnt);
+            if (it.master) copy8(reinterpret_cast<uint8_t*>(it.to.master), reinterpret_cast<const uint8_t*>(it.master), at, 4, full, cnt);
+            copy8(it.to.m, it.m, at, BITS / 8, full, cnt);
+            copy8(it.to.v, it.v, at, BITS / 8, full, cnt);
+            if (BITS == 8 && lane < 2) (lane ? it.to.vs : it.to.ms)[block] = (lane ? it.vs : it.ms)[block];
+        }
+    }
+}
+
 // CTAs of a pass that an SM holds: with 32-bit moments 2 of up to 128 registers, which hold the next
 // group, with 8-bit ones 4 of up to 64 (208M BF16 weights: 520 us, with 3 of up to 80 535 us). The
 // moments' read-out takes the same time with 2, 4 and 6.
@@ -491,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) adamw_kernel(cons
             }
         }
         }
+    } else if (p.into) {
+        copy_all<CAP, BITS>(p);
     }
     if (!p.last) return;
     __syncthreads();
@@ -848,6 +889,7 @@ extern "C" bs_status bs_adamw(int32_t n, const bs_adamw_item* items, const bs_ad
         p.log_b2 = prm->beta2 > 0 ? std::log(prm->beta2) : -1e9;
         p.seed = prm->seed;
         p.step = prm->step;
+        p.into = to != items;
         p.ctl = d_ctl;
     });
 }
