@@ -588,13 +588,18 @@ typedef struct {
  * new values. The caller sets lr, and clip = 1 and the rest 0 before the first use. */
 typedef struct {
     float lr;
-    float clip;        /* factor on every gradient; bs_grad_norm writes it */
+    float clip;        /* factor on every gradient; bs_grad_norm writes it. See once */
     int32_t step;      /* completed steps: bs_adamw leaves its step's number */
     uint32_t skip;     /* nonzero: bs_adamw changes nothing, the step count included; into other buffers it copies
                         * what the items hold, bit for bit */
     float norm;        /* of the last bs_grad_norm */
     uint32_t arrived;  /* internal, 0 between calls */
-    uint32_t reserved[2];
+    float own_clip;    /* used where once is set */
+    uint32_t once;     /* 0: clip and skip stay as bs_grad_norm left them until someone writes them again, so that
+                        * several calls may share one norm. 1: they are for the next bs_adamw alone. A step with no
+                        * norm since the last one takes own_clip as its factor (and leaves it in clip), and
+                        * a skip that a norm has set is cleared by the step that it left out. (Bit 1 is
+                        * internal: a norm is pending.) */
 } bs_adamw_ctl;
 
 typedef struct {
@@ -610,7 +615,7 @@ size_t bs_grad_norm_scratch_bytes(int32_t n, const bs_adamw_item* items);
  * order: d_ctl->norm = norm, d_ctl->clip = min(1, max_norm / (norm + 1e-6)) (max_norm above 0, may be
  * infinite), d_ctl->skip = 0. A norm that is not finite (a NaN or infinity in a gradient, or
  * gradients whose squares leave the FP32 range) sets clip = 0 and skip = 1 instead, so that the step
- * that follows is left out. d_scratch: 8-byte aligned. Enqueued on stream. */
+ * that follows is left out (and those after it, until the next norm: see once). d_scratch: 8-byte aligned. Enqueued on stream. */
 bs_status bs_grad_norm(int32_t n, const bs_adamw_item* items, float max_norm, bs_adamw_ctl* d_ctl, void* d_scratch,
                        size_t scratch_bytes, void* stream);
 /* One step over every item. to: NULL, and the items are updated in place; or n items whose d_param,

@@ -942,11 +942,14 @@ class AdamW:
     is rounded to nearest each step). weight_decay: a number, or one for each tensor.
     states: existing moments to go on with, (exp_avgs, exp_avg_sqs) in 32 bits, or
     ((codes, scales), (codes, scales)) in 8 bits, each a list; they are updated in place. step: the
-    steps already done. clip: the factor on gradients where step() computes no norm.
+    steps already done. clip: the factor on gradients where step() computes no norm (nor grad_norm() has
+    since the last step).
 
     The learning rate, the factor, the step count and the norm live on the device (``ctl``): set
     ``lr`` and ``clip`` by attribute, read ``norm`` and ``steps`` as device tensors; a captured step
-    sees new values.
+    sees new values. ``clip`` reads as the factor that was set, or that the last norm or step had; setting it
+    replaces a norm's that no step has used yet. A norm, and the skip of a step whose norm is not finite,
+    are for that one step.
     """
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
@@ -1006,7 +1009,9 @@ class AdamW:
         self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
         self._lr, self._clip, self.norm, self.steps = f[0], f[1], f[4], self.ctl[2]
+        self._clips = f[1:7:5]  # clip and own_clip
         if _ctl is None:
+            self.ctl[7:].fill_(1)  # once
             self.lr, self.clip = lr, clip
             self.steps.fill_(step)
         self._scratch = torch.empty(max(8, lib.bs_grad_norm_scratch_bytes(n, self._items)), dtype=torch.uint8, device=dev)
@@ -1026,7 +1031,7 @@ class AdamW:
 
     @clip.setter
     def clip(self, v):
-        self._clip.fill_(v)
+        self._clips.fill_(v)
 
     def grad_norm(self, max_norm: float = float("inf"), stream=None) -> torch.Tensor:
         """bs_grad_norm: the norm of all gradients as a device scalar; sets the factor of the next

@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 #include <memory>
@@ -484,14 +485,16 @@ constexpr uint32_t kRun = 32;
 template <int CAP, int BITS>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) adamw_kernel(const __grid_constant__ OptParams<CAP> p) {
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    // Read before this CTA arrives below: the step count moves only after every CTA has arrived.
+    // Read before this CTA arrives below: ctl changes only after every CTA has arrived.
     const volatile bs_adamw_ctl* ctl = p.ctl;
     const bool skip = ctl->skip != 0;
     if (!skip) {
         const uint32_t t = p.step ? p.step : static_cast<uint32_t>(ctl->step) + 1u;
+        // once: 0: clip is for every step; 1: no norm since the last step; 3: this is a norm's step
+        const float shared_clip = ctl->clip, own_clip = ctl->own_clip, clip = ctl->once == 1 ? own_clip : shared_clip;
         // 1 - b^t = -expm1(t log b): relative error of a few 2^-24 for every t
         const float bc1 = -expm1f(static_cast<float>(t * p.log_b1)), bc2 = -expm1f(static_cast<float>(t * p.log_b2));
-        StepConst c{p.b1, p.b2, p.c1, p.c2, p.eps, ctl->clip, ctl->lr, 0.f, rsqrtf(bc2)};
+        StepConst c{p.b1, p.b2, p.c1, p.c2, p.eps, clip, ctl->lr, 0.f, rsqrtf(bc2)};
         c.step = c.lr / bc1;
         const uint64_t key0 = mix64(p.seed + t * 2654435769ull);
         // A CTA's runs of per_cta groups; a run may cross tensors, and warp w takes the groups at w,
@@ -535,8 +538,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) adamw_kernel(cons
     }
     if (!p.last) return;
     __syncthreads();
-    if (threadIdx.x == 0 && atomicInc(&p.ctl->arrived, gridDim.x - 1) == gridDim.x - 1 && !skip)
-        p.ctl->step = p.step ? static_cast<int32_t>(p.step) : p.ctl->step + 1;
+    if (threadIdx.x != 0) return;
+    const uint32_t once = __ldcg(&p.ctl->once); // again: it would take a register all the way
+    if (atomicInc(&p.ctl->arrived, gridDim.x - 1) != gridDim.x - 1) return;
+    if (!skip) p.ctl->step = p.step ? static_cast<int32_t>(p.step) : p.ctl->step + 1;
+    if (once == 1) p.ctl->clip = p.ctl->own_clip;
+    if (once == 3) { // this was the norm's step
+        p.ctl->skip = 0;
+        p.ctl->once = 1;
+    }
 }
 
 // The squares of 4 groups of a warp, kWarps groups apart, all loads before the sums.
@@ -638,6 +648,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         const float norm = static_cast<float>(sqrt(x));
         const bool finite = norm < __uint_as_float(0x7F800000u);
         p.ctl->norm = norm;
+        if (p.ctl->once) p.ctl->once = 3;
         p.ctl->skip = finite ? 0u : 1u;
         p.ctl->clip = finite ? static_cast<float>(fmin(1.0, static_cast<double>(p.max_norm) / (sqrt(x) + 1e-6))) : 0.f;
     }
