@@ -869,9 +869,10 @@ class LoraAdapters:
         for v in lists:
             if len(v) != n:
                 raise BsError(E_ARG, "lora", "one entry for each projection")
-        if plan.tokens != self._need[0]:
-            self._need = (plan.tokens, lib.bs_lora_state_bytes(plan.tokens, self.rank_max))
-        need, index = self._need[1], self._index
+        known, index = self._need, self._index  # read once: another thread may serve another batch meanwhile
+        if plan.tokens != known[0]:
+            self._need = known = (plan.tokens, lib.bs_lora_state_bytes(plan.tokens, self.rank_max))
+        need = known[1]
         for t in states:
             if t.numel() < need or t.dtype is not torch.uint8 or t.get_device() != index:
                 raise BsError(E_SIZE, "lora", "a state is of another batch")

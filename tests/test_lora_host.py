@@ -127,3 +127,44 @@ def test_kernels_let_the_next_one_go_only_once_they_hold_their_tensor_memory():
         assert before.index("tmem_alloc(") < before.index("kernels_before_done();") < before.rindex("__syncthreads();")
         assert re.search(r"__syncthreads\(\);\s*fence_after\(\);\s*const uint32_t tmem = s_tmem;\s*(if \(!p\.beside_expand\) )?$", before)
     assert all("launch_dependents" not in _source(f) for f in ("bs_lora.cu", "bs_lora_few.cu", "bs_lora_tc.cuh"))
+
+
+class _Shared(bs.LoraAdapters):
+    """Adapters without tensors whose last batch's size another thread replaces after every look at it."""
+    others = ()
+
+    def __init__(self, rank_max, last):
+        self.n, self.rank_max, self._n, self._index, self._array = 4, rank_max, 1, -1, bs.LoraItem * 1
+        self._ranks_at = self._scales_at = None
+        self.last = last
+
+    @property
+    def _need(self):
+        now, self.last = self.last, self.other
+        return now
+
+    @_need.setter
+    def _need(self, v):
+        self.last = self.other
+
+
+class _Plan:
+    n_adapters, _index, _args = 4, -1, (0, 4, 256, 1 << 20, 0)
+
+    def __init__(self, tokens):
+        self.tokens = tokens
+
+
+@pytest.mark.parametrize("last", [5, 9, 300])
+@pytest.mark.parametrize("other", [1, 1000])
+def test_a_state_is_held_against_its_own_batch_whatever_other_threads_serve(last, other):
+    import torch
+    size = lambda t: (t, L.bs_lora_state_bytes(t, 16))  # noqa: E731
+    who = _Shared(16, size(last))
+    who.other = size(other)
+    state = lambda t: [torch.zeros(size(t)[1], dtype=torch.uint8)]  # noqa: E731
+    who._begin(_Plan(9), (), state(9))
+    who.last = size(last)
+    with pytest.raises(bs.BsError) as e:
+        who._begin(_Plan(9), (), [state(9)[0][:-1]])
+    assert e.value.code == bs.E_SIZE
