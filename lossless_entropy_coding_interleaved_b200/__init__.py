@@ -20,6 +20,7 @@ import bisect
 import ctypes
 import os
 import struct
+import weakref
 
 import numpy as np
 import torch
@@ -954,7 +955,7 @@ class AdamW:
     """
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
-                 bits: int = 32, masters=None, seed: int = 0, step: int = 0, clip: float = 1.0, states=None, _ctl=None):
+                 bits: int = 32, masters=None, seed: int = 0, step: int = 0, clip: float = 1.0, states=None, _ctl=None, _family=None):
         params = list(params)
         if not torch.cuda.is_available():
             raise BsError(E_UNSUPPORTED, "adamw", "no CUDA device")
@@ -986,14 +987,22 @@ class AdamW:
             (m, ms), (v, vs) = states
             self.exp_avg, self.exp_avg_sq = (_flat_list(c, "states", n, sizes, (torch.uint8,), dev) for c in (m, v))
             self.exp_avg_scale, self.exp_avg_sq_scale = (_flat_list(c, "states", n, blocks, (torch.float32,), dev) for c in (ms, vs))
-        written = [t for ts in (self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
-                   if ts is not None for t in ts]
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written if t.numel())
+        # what a step writes: (first byte, behind the last, (which buffer, of which parameter))
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), (i, k)) for i, ts in enumerate(
+            (self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale))
+            if ts is not None for k, t in enumerate(ts) if t.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise BsError(E_ARG, "adamw", "parameters, masters and moments must not overlap")
+        # a step into a twin reads one's and writes the other's: they may share a whole buffer, which is then
+        # updated in place, but not overlap otherwise
+        self._spans, self._family = spans, _family if _family is not None else weakref.WeakSet()
+        for other in self._family:
+            both = sorted({*spans, *other._spans})
+            if any(a[1] > b[0] for a, b in zip(both, both[1:])):
+                raise BsError(E_ARG, "adamw", "a twin's parameters, masters and moments must not overlap its handle's")
         for g in self.grads:  # a gradient may be read by several items, but not written by any
             lo, hi = g.data_ptr(), g.data_ptr() + g.numel() * g.element_size()
-            at = bisect.bisect_left(spans, (hi,))
+            at = bisect.bisect_left(spans, (hi,))  # the first that begins at or behind the gradient's end
             if g.numel() and at and spans[at - 1][1] > lo:
                 raise BsError(E_ARG, "adamw", "gradients must not overlap what the step writes")
         self._items = (AdamWItem * n)()
@@ -1017,6 +1026,7 @@ class AdamW:
             self.steps.fill_(step)
         self._scratch = torch.empty(max(8, lib.bs_grad_norm_scratch_bytes(n, self._items)), dtype=torch.uint8, device=dev)
         self._at = (self.ctl.data_ptr(), self._scratch.data_ptr(), self._scratch.numel())
+        self._family.add(self)
 
     @property
     def lr(self):
@@ -1042,7 +1052,8 @@ class AdamW:
 
     def twin(self, params=None, masters=None, states=None) -> "AdamW":
         """A second set of parameters, masters and moments (new tensors where none are given) for the
-        same gradients and the same ctl: step(into=twin) leaves this handle's as they are, to be
+        same gradients and the same ctl, which must not overlap this handle's in part (one that is the same
+        tensor is updated in place): step(into=twin) leaves this handle's as they are, to be
         coded or compared, and the twin's next step, into this one, goes on from there. A step that is
         left out (its norm was not finite) leaves the twin with this handle's values."""
         new = lambda ts, given: (None if ts is None else list(given) if given is not None else [torch.empty_like(t) for t in ts])  # noqa: E731
@@ -1051,7 +1062,7 @@ class AdamW:
             states = (m, v) if self.bits == 32 else ((m, ms), (v, vs))
         return AdamW(new(self.params, params), self.grads, betas=(self._prm.beta1, self._prm.beta2), eps=self._prm.eps,
                   weight_decay=[it.weight_decay for it in self._items], bits=self.bits, masters=new(self.masters, masters),
-                  seed=self._prm.seed, states=states, _ctl=self.ctl)
+                  seed=self._prm.seed, states=states, _ctl=self.ctl, _family=self._family)
 
     def step(self, max_norm: float | None = None, into: "AdamW | None" = None, number: int = 0, stream=None):
         """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first. into: a twin
