@@ -1232,7 +1232,9 @@ extern "C" bs_status bs_lora_backward(int32_t n, const bs_lora_item* items, cons
             if (items[q].d_g == t.d_g || items[q].d_da == t.d_da || items[q].d_db == t.d_db) return BS_E_ARG;
         if (t.d_dx_base && t.d_dx_base == t.d_dx && t.dx_base_stride != t.dx_stride && batch->tokens > 1) return BS_E_ARG;
         for (int32_t q = 0; q < n; ++q) // what is written is not also read
-            if (items[q].d_h == t.d_g || (t.d_dx && (items[q].d_x == t.d_dx || items[q].d_dy == t.d_dx))) return BS_E_ARG;
+            if (items[q].d_h == t.d_g || (t.d_dx && (items[q].d_x == t.d_dx || items[q].d_dy == t.d_dx ||
+                                                     (items[q].d_dx_base == t.d_dx && items[q].d_dx != t.d_dx))))
+                return BS_E_ARG;
         // items that share dx share its base, strides and type too
         for (int32_t q = 0; q < k; ++q)
             if (t.d_dx && items[q].d_dx == t.d_dx &&

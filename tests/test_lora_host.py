@@ -168,3 +168,11 @@ def test_a_state_is_held_against_its_own_batch_whatever_other_threads_serve(last
     with pytest.raises(bs.BsError) as e:
         who._begin(_Plan(9), (), [state(9)[0][:-1]])
     assert e.value.code == bs.E_SIZE
+
+
+def test_a_dx_may_not_be_the_base_of_another():
+    dx = dict(dx_stride=128, type=1)
+    other = dict(d_h=1 << 20, d_y=1 << 21, d_g=1 << 22, d_da=1 << 23, d_db=1 << 24, d_x=1 << 27, d_dy=1 << 28, dx_base_stride=128, **dx)
+    for d_dx in (1 << 26, None):
+        items = [_item(**dx, d_dx=1 << 25), _item(**other, d_dx=d_dx, d_dx_base=1 << 25)]
+        assert _backward(items) == bs.E_ARG and _backward(items[::-1]) == bs.E_ARG
