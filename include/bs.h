@@ -537,6 +537,9 @@ typedef struct {
 /* Every item's h and y. Outputs and states of one call must not overlap, nor an output its inputs
  * (but for d_base == d_y with equal strides). */
 bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, void* stream);
+/* What bs_lora_forward answers to these arguments before it enqueues anything (BS_OK or a refusal), for a
+ * caller that is about to enqueue the product whose output is the base. */
+bs_status bs_lora_forward_check(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch);
 /* Every item's dx, dA and dB. Items that read the same x (q, k and v) may name the same d_dx, with
  * the same base, strides, cols and type, within one run of 16 items: dx then receives base plus all
  * their parts, rounded once.

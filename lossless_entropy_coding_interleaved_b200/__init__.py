@@ -178,8 +178,9 @@ def _load():
     L.bs_lora_state_bytes.restype = sz
     L.bs_lora_plan.argtypes = [P, u32, u32, P, sz, P, P]
     L.bs_lora_forward.argtypes = [i32, LI, LB, P]
+    L.bs_lora_forward_check.argtypes = [i32, LI, LB]
     L.bs_lora_backward.argtypes = [i32, LI, LB, u32, P]
-    for fn in ("bs_lora_plan", "bs_lora_forward", "bs_lora_backward"):
+    for fn in ("bs_lora_plan", "bs_lora_forward", "bs_lora_forward_check", "bs_lora_backward"):
         getattr(L, fn).restype = ctypes.c_int
     IT = ctypes.POINTER(AdamWItem)
     L.bs_grad_norm_scratch_bytes.argtypes = [i32, IT]
@@ -215,7 +216,7 @@ EXPORTS = ("bs_plan_workspace_bytes", "bs_plan_workspace_bytes_device", "bs_plan
            "bs_streamer_acquire",
            "bs_streamer_release", "bs_streamer_get_stats", "bs_streamer_check", "bs_streamer_destroy",
            "bs_fw_scratch_bytes", "bs_fw_measure", "bs_fw_write", "bs_fw_parse", "bs_fw_decode", "bs_fw_gemv",
-           "bs_fw_gemm", "bs_lora_plan_bytes", "bs_lora_state_bytes", "bs_lora_plan", "bs_lora_forward", "bs_lora_backward",
+           "bs_fw_gemm", "bs_lora_plan_bytes", "bs_lora_state_bytes", "bs_lora_plan", "bs_lora_forward", "bs_lora_forward_check", "bs_lora_backward",
            "bs_grad_norm_scratch_bytes", "bs_grad_norm", "bs_adamw", "bs_adamw_read_states")
 
 
@@ -700,12 +701,17 @@ def _fw_products(products, max_batch):
 
 
 def _with_adapters(products, adapters, stream):
-    """Adds each token's adapter to the products' outputs: adapters is (LoraAdapters, LoraPlan) or
-    (LoraAdapters, LoraPlan, state), the adapters' projections being the products in order."""
+    """What adds each token's adapter to the products' outputs, to be called once they are enqueued: adapters is
+    (LoraAdapters, LoraPlan) or (LoraAdapters, LoraPlan, state), the adapters' projections being the products
+    in order. Whatever is to be refused of them is refused here, before anything is enqueued."""
+    if adapters is None:
+        return lambda: None
     who, plan = adapters[:2]
     two = lambda t: t.view(1, -1) if t.dim() == 1 else t  # noqa: E731
-    who.forward(plan, [two(p[4].view(torch.bfloat16)) for p in products], [two(p[5]) for p in products],
-                state=adapters[2] if len(adapters) > 2 else None, stream=stream)
+    args = who._forward_args(plan, [two(p[4].view(torch.bfloat16)) for p in products], [two(p[5]) for p in products], None,
+                             adapters[2] if len(adapters) > 2 else None, stream)
+    _check(lib.bs_lora_forward_check(*args[:3]), "lora_forward")
+    return lambda: _on(who._index, "lora_forward", lib.bs_lora_forward, *args[:3], stream=stream)
 
 
 def fw_gemm(products, err: torch.Tensor, stream=None, adapters=None):
@@ -714,10 +720,10 @@ def fw_gemm(products, err: torch.Tensor, stream=None, adapters=None):
     err: a zeroed int32 CUDA tensor of one element. adapters: as fw_gemv's. Enqueued on the stream."""
     n, arr, batch = _fw_products(products, None)
     assert err.is_cuda and err.dtype == torch.int32 and err.numel() >= 1
+    add = _with_adapters(products, adapters, stream)
     with torch.cuda.device(err.device):
         _check(lib.bs_fw_gemm(n, arr, batch, err.data_ptr(), _stream(stream)), "fw_gemm")
-    if adapters is not None:
-        _with_adapters(products, adapters, stream)
+    add()
     return [p[5] for p in products]
 
 
@@ -746,11 +752,11 @@ def fw_gemv(products, err: torch.Tensor, stream=None, layouts_resident: bool = F
         arr[k].d_x = x.data_ptr()
         arr[k].d_y = y.data_ptr()
     assert err.is_cuda and err.dtype == torch.int32 and err.numel() >= 1
+    add = _with_adapters(products, adapters, stream)
     with torch.cuda.device(err.device):
         _check(lib.bs_fw_gemv(n, arr, batch or 1, FW_LAYOUTS_RESIDENT if layouts_resident else 0, err.data_ptr(),
                               _stream(stream)), "fw_gemv")
-    if adapters is not None:
-        _with_adapters(products, adapters, stream)
+    add()
     return [p[5] for p in products]
 
 
@@ -879,7 +885,8 @@ class LoraAdapters:
                 raise BsError(E_SIZE, "lora", "a state is of another batch")
         return self._array(), LoraBatch(plan.tokens, self.n, self.rank_max, 0, self._ranks_at, self._scales_at, *plan._args[2:])
 
-    def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
+    def _forward_args(self, plan, xs, ys, bases, state, stream):
+        """bs_lora_forward's arguments, and what has to outlive its call."""
         n, T = self._n, plan.tokens
         state = _made_on(stream, self._index, lambda: self.state(T)) if state is None else state
         ys = [None] * n if ys is None else ys
@@ -894,7 +901,11 @@ class LoraAdapters:
             ty, bp, b_stride, y, y_stride = self._out(ys[k], bases[k], rows, "y", T)
             pack(items, 160 * k, a, b, rows, cols, ty, 0, xp, x_stride, state[k].data_ptr(), bp, b_stride, y, y_stride,
                  0, 0, 0, 0, 0, 0, 0, 0, 0)
-        _on(self._index, "lora_forward", lib.bs_lora_forward, n, items, ctypes.byref(batch), stream=stream)
+        return n, items, ctypes.byref(batch), state, ys
+
+    def forward(self, plan: LoraPlan, xs, ys=None, bases=None, state=None, stream=None):
+        *args, _, ys = self._forward_args(plan, xs, ys, bases, state, stream)
+        _on(self._index, "lora_forward", lib.bs_lora_forward, *args, stream=stream)
         return ys
 
     def backward(self, plan: LoraPlan, xs, dys, state, das, dbs, dxs=None, dx_bases=None, work=None, accumulate: bool = False,

@@ -1156,7 +1156,7 @@ extern "C" bs_status bs_lora_plan(const int32_t* d_idx, uint32_t tokens, uint32_
     return e == cudaSuccess ? BS_OK : cuda_status(e);
 }
 
-extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, void* stream) {
+extern "C" bs_status bs_lora_forward_check(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch) {
     bs_status st = check_batch(batch);
     if (st != BS_OK) return st;
     if (n < 0 || (n > 0 && !items)) return BS_E_ARG;
@@ -1173,6 +1173,12 @@ extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const
         for (int32_t q = 0; t.d_y && q < n; ++q) // a y is not also read
             if (items[q].d_x == t.d_y || (q != k && items[q].d_base == t.d_y)) return BS_E_ARG;
     }
+    return BS_OK;
+}
+
+extern "C" bs_status bs_lora_forward(int32_t n, const bs_lora_item* items, const bs_lora_batch* batch, void* stream) {
+    bs_status st = bs_lora_forward_check(n, items, batch);
+    if (st != BS_OK) return st;
     Gpu gpu;
     gpu.s = static_cast<cudaStream_t>(stream);
     if ((st = current_device(&gpu.dev, &gpu.sms)) != BS_OK) return st;

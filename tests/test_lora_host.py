@@ -176,3 +176,12 @@ def test_a_dx_may_not_be_the_base_of_another():
     for d_dx in (1 << 26, None):
         items = [_item(**dx, d_dx=1 << 25), _item(**other, d_dx=d_dx, d_dx_base=1 << 25)]
         assert _backward(items) == bs.E_ARG and _backward(items[::-1]) == bs.E_ARG
+
+
+def test_the_check_answers_what_the_call_would():
+    check = lambda items, batch=None: L.bs_lora_forward_check(len(items), (bs.LoraItem * max(1, len(items)))(*items), ctypes.byref(batch or _batch()))  # noqa: E731
+    assert check([_item()]) == check([]) == check([_item(d_base=4096, base_stride=64)]) == bs.OK
+    for kw in (dict(d_y=4100), dict(rows=60), dict(x_stride=120), dict(d_x=4096), dict(d_h=2056)):
+        assert check([_item(**kw)]) == _forward([_item(**kw)]) == bs.E_ARG, kw
+    assert check([_item()], _batch(rank_max=12)) == bs.E_ARG and check([_item(), _item()]) == bs.E_ARG
+    assert L.bs_lora_forward_check(-1, None, ctypes.byref(_batch())) == bs.E_ARG and L.bs_lora_forward_check(1, None, None) == bs.E_ARG
