@@ -477,7 +477,8 @@ bs_status bs_fw_gemm(int32_t n, const bs_fw_gemv_item* items, uint32_t batch, ui
  * A token without an adapter keeps base (dx_base). An adapter uses the first ranks[a] of its
  * rank_max rank rows: the rest of A and B is never read, and their gradients are 0.
  * x, dy, A and B are BF16; y, dx and their bases FP32 or BF16; sums, h, g, dA and dB FP32 (h and g
- * are kept in 24 bits). Sums are in a fixed order: the same call gives the same bits.
+ * are kept in 24 bits). Sums are in a fixed order: the same call gives the same bits. Infinities and NaN in x
+ * and dy are where the formulas have them; weights are finite (an infinite one gives infinities or NaN).
  * All device memory belongs to the caller. Calls are enqueued on stream, launch nothing that
  * depends on host-side values of the routing, and can be captured.
  * ------------------------------------------------------------------------------------ */

@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
     constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
     constexpr uint32_t kOuterLoad = outer_load<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_rank;
     __shared__ int s_abort;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -914,22 +914,50 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
         }
     } else if (warp < kOuterOut / 32) {
         // column 32 (warp % 4) + lane of a half; warps 4 to 7: the other half, or the other ranks
+        if (tid == 0) s_rank = rank_of(p.b, a); // for the end, while nothing is there to be added up
         const uint32_t up = warp >> 2, h = kHalves == 2 ? up : 0, j0 = R > 64 ? up * kRanks : 0; // up: 0 with 128 threads
         const uint32_t chains = n_steps ? (n_steps - 1 + 2 * h) / kOuterFlush + 1 : 0;
         float sum[kRanks] = {};
+        // Where x or dy has an infinity or NaN, the upper part's sum is what the product is: the lower parts may be 0
+        // or of the other sign there, and give NaN for an infinity. From the first such sum of the warp on,
+        // the upper part goes first, and what it has made infinite takes no more. (Columns past the width are
+        // whatever shared memory held.)
+        const bool within = h * 128 + (warp & 3u) * 32 + lane < cols;
+        constexpr float kInf = __builtin_huge_valf();
+        bool special = false;
         for (uint32_t c = 0; c < chains; ++c) {
             const uint32_t acc = kHalves == 2 ? h : c % kAccs, use = kHalves == 2 ? c : c / kAccs;
             if (!bar_wait(bar_d + 8 * acc, use & 1u, abort_flag)) break;
             fence_after();
 #pragma unroll
-            for (uint32_t j = 0; j < kRanks; j += 16)
+            for (uint32_t j = 0; j < kRanks; j += 16) {
+                const uint32_t at = tmem + ((warp & 3u) * 32 << 16) + acc * kWide + j0 + j;
+                uint32_t d[16];
+                if (!special) {
 #pragma unroll
-                for (int part = 2; part >= 0; --part) { // small parts first
-                    uint32_t d[16];
-                    tmem_ld16(d, tmem + ((warp & 3u) * 32 << 16) + acc * kWide + part * R + j0 + j);
+                    for (int part = 2; part >= 0; --part) { // small parts first
+                        tmem_ld16(d, at + part * R);
 #pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
+                        for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
+                    }
+                    float most = 0.f;
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) most = max_abs_nan(most, __uint_as_float(d[i]));
+                    if (!__any_sync(0xFFFFFFFFu, within && !(most < kInf))) continue;
+                    special = true;
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i)
+                        if (!(fabsf(__uint_as_float(d[i])) < kInf)) sum[j + i] = __uint_as_float(d[i]); // what it was is finite
+                } else {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        tmem_ld16(d, at + part * R);
+#pragma unroll
+                        for (uint32_t i = 0; i < 16; ++i)
+                            if (part == 0 || fabsf(sum[j + i]) < kInf) sum[j + i] += __uint_as_float(d[i]);
+                    }
                 }
+            }
             fence_before();
             bar_arrive(bar_free + 8 * acc);
         }
@@ -943,7 +971,7 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     // columns part * cols / split ..: the parts of all CTAs added up, 4 ranks of a column at a time
-    const uint32_t each = kOuterCols / p.split, quads = rm / 4;
+    const uint32_t each = kOuterCols / p.split, quads = rm / 4, rank = s_rank;
     for (uint32_t i = tid; i < each * quads; i += kOuterThreads) {
         // neighbouring threads have neighbouring columns (dA), or neighbouring ranks of a column (dB)
         const uint32_t c = part * each + (job.transposed ? i / quads : i % each), j = 4 * (job.transposed ? i % quads : i / each);
@@ -954,6 +982,8 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
             const float4 u = *reinterpret_cast<const float4*>(cluster.map_shared_rank(red, q) + c * (R + 4) + j);
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
         }
+        // past the adapter's rank 0, whatever stood in x and dy (the parts are 0 there, but 0 times infinity is not)
+        v = make_float4(j < rank ? v.x : 0.f, j + 1 < rank ? v.y : 0.f, j + 2 < rank ? v.z : 0.f, j + 3 < rank ? v.w : 0.f);
         if (job.transposed) {
             float4* d = reinterpret_cast<float4*>(out + uint64_t(c0 + c) * rm + j);
             if (p.accumulate) { const float4 u = *d; v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w); }
