@@ -21,8 +21,8 @@
 // the next product as three BF16 numbers each (24 bits, see split3): three small matrix
 // instructions in place of one lossy one, on a side where the tensor cores wait for memory.
 // The tensor cores' accumulation rounds towards zero, so chains of matrix instructions are kept
-// to 16 (shrink, outer) or 24 (expand, for each projection that adds to a dx) links and their sums
-// added in FP32 outside.
+// to 16 (shrink, outer) or 28 (expand: links at the size of the sum; 56 at rank 128) and their sums added in
+// FP32 outside.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -438,6 +438,13 @@ constexpr uint32_t expand_bufs = R > 64 ? 2 : 4;
 // Sources that stand beside each other in an operand's 64 (or 128) ranks.
 template <int R>
 constexpr uint32_t group_of = R >= 64 ? 1 : 64 / R;
+// Groups whose products are one chain of matrix instructions. The links of the lower parts come first in a group, so
+// in the first one only those of the upper part (4, at rank 128 8) are rounded at the size of the sum; each group
+// behind it has 12 (24). So a chain has 28 such links at most (rank 128: 56), and q, k and v are one. A dx of more
+// sources is several chains, each a turn of the buffers, added up in tensor memory by the warps that write
+// (MANY). q, k and v at rank 128, 8192 tokens, in BF16: 333 us in one chain, 366 us in two.
+template <int R>
+constexpr uint32_t chain_of = 3 * group_of<R>; // its sources
 // Shared memory: h's parts (tokens x ranks, K-major), two buffers of weights, then those of base.
 template <int R, bool BF16>
 __host__ __device__ constexpr uint32_t expand_w() { return expand_cols<BF16> * 128 * atoms_of<R>; }
@@ -463,14 +470,15 @@ struct ExpandAt {
 // BF16: base and out are BF16. h enters as all of its three parts (24 bits) here too: with the upper two
 // an output could be off by 2^-17 of the products' magnitudes, which is more than its own rounding
 // where the products cancel.
-template <int R, bool WT, bool BF16>
+// MANY: some dx has more sources than a chain holds.
+template <int R, bool WT, bool BF16, bool MANY>
 __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_bar[4 + 3 * expand_bufs<R>];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     constexpr uint32_t kParts = 3, kCols = expand_cols<BF16>, es = BF16 ? 2 : 4, kPart = 16384 * atoms_of<R>;
-    constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kTmem = kBufs * kCols;
+    constexpr uint32_t kBufs = expand_bufs<R>, kGroup = group_of<R>, kChain = chain_of<R>, kTmem = kBufs * kCols;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sH = s0, sW = sH + kParts * kPart, sRow = sW + 2 * expand_w<R, BF16>();
@@ -554,10 +562,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 }
             }
             const uint32_t n0 = at.block * kCols, N = job.width, count = tl.z, sources = rank ? job.n_src : 0u;
-            if (!left_out(job, rank)) {
+            auto take_turn = [&](bool last) { // base goes with a unit's last chain
                 const uint32_t buf = turn % kBufs, n = n0 + piece * (16 / es);
-                if (turn >= kBufs && !bar_wait(bar_free + 8 * buf, (turn / kBufs - 1) & 1u, abort_flag)) break;
-                if (job.base && n < N) {
+                if (turn >= kBufs && !bar_wait(bar_free + 8 * buf, (turn / kBufs - 1) & 1u, abort_flag)) return false;
+                if (last && job.base && n < N) {
                     const uint32_t dst = sRow + (buf * kTile + (t0 >> 4)) * kRowBytes + row_piece(t0 >> 4, piece);
 #pragma unroll
                     for (uint32_t i = 0; i < 16; ++i)
@@ -565,8 +573,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 }
                 bar_arrive_copies(bar_base + 8 * buf);
                 ++turn;
-            }
+                return true;
+            };
+            if (!left_out(job, rank) && !take_turn(!MANY || sources <= kChain)) break;
             for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) { // a group of sources at a time
+                if (MANY && g0 > 0 && g0 % kChain == 0 && !take_turn(g0 + kChain >= sources)) { ok = false; break; }
                 const uint32_t wb = step & 1u, sb = sW + wb * expand_w<R, BF16>(), g1 = min(g0 + kGroup, sources);
                 if (step >= 2 && !bar_wait(bar_empty + 8 * wb, (step / 2 - 1) & 1u, abort_flag)) { ok = false; break; }
                 if (!parts_in) { // once what stood there has been read
@@ -618,24 +629,38 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             const ExpandJob& job = p.job[at.job];
             if (fresh) rank = rank_at(tile_of[at.tile]);
             if (!left_out(job, rank)) {
-                const uint32_t db = turn % kBufs, kn = (rank + 15) / 16, sources = rank ? job.n_src : 0u;
+                const uint32_t kn = (rank + 15) / 16, sources = rank ? job.n_src : 0u;
+                uint32_t db = turn % kBufs;
                 if (turn >= kBufs && !bar_wait(bar_free + 8 * db, (turn / kBufs - 1) & 1u, abort_flag)) break;
                 for (uint32_t g0 = 0; g0 < sources; g0 += kGroup, ++step) {
+                    const bool begins = g0 == 0 || (MANY && g0 % kChain == 0);
+                    if (MANY && begins && g0 > 0) { // the next chain
+                        commit_tc(bar_d + 8 * db);
+                        db = ++turn % kBufs;
+                        if (turn >= kBufs && !bar_wait(bar_free + 8 * db, (turn / kBufs - 1) & 1u, abort_flag)) { ok = false; break; }
+                    }
                     const uint32_t wb = step & 1u, w = sW + wb * expand_w<R, BF16>();
                     if (!bar_wait(bar_full + 8 * wb, (step / 2) & 1u, abort_flag)) { ok = false; break; }
                     fence_operands(); // the copies, before the tensor cores read them
                     fence_after();
-                    for (uint32_t g = g0; g < min(g0 + kGroup, sources); ++g)
-                        for (uint32_t k1 = 0; k1 < kn; ++k1) {
-                            const uint32_t kk = (g - g0) * (R / 16) + k1;
-                            const uint64_t bd = WT ? mn_major(w + kk * 2048, kGroup * R * 128) : k_major(w + (kk >> 2) * (kCols * 128) + (kk & 3u) * 32);
+                    // the descriptors' address field counts 16 bytes, and no sum carries out of it
+                    const uint64_t wd = WT ? mn_major(w, kGroup * R * 128) : k_major(w), hd = k_major(sH);
+                    const uint32_t in_group = min(sources - g0, kGroup);
+                    uint32_t more = !begins;
 #pragma unroll
-                            for (int t = kParts - 1; t >= 0; --t) // small parts first
-                                mma_tc(tmem + db * kCols, k_major(sH + t * kPart + (kk >> 2) * 16384 + (kk & 3u) * 32), bd, idesc,
-                                       !(g == 0 && k1 == 0 && t == static_cast<int>(kParts) - 1));
-                        }
+                    for (int t = kParts - 1; t >= 0; --t) // small parts first
+                        for (uint32_t g = 0; g < in_group; ++g)
+#pragma unroll
+                            for (uint32_t k1 = 0; k1 < R / 16; ++k1) {
+                                if (k1 >= kn) break;
+                                const uint32_t kk = g * (R / 16) + k1;
+                                mma_tc(tmem + db * kCols, hd + ((t * kPart + (kk >> 2) * 16384 + (kk & 3u) * 32) >> 4),
+                                       wd + ((WT ? kk * 2048 : (kk >> 2) * (kCols * 128) + (kk & 3u) * 32) >> 4), idesc, more);
+                                more = 1;
+                            }
                     commit_tc(bar_empty + 8 * wb);
                 }
+                if (!ok) break;
                 if (rank) commit_tc(bar_d + 8 * db);
                 else bar_arrive(bar_d + 8 * db);
                 ++turn;
@@ -653,6 +678,27 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         uint64_t row[8] = {}; // of the rows r0 + lane / 8 + 4 i
         bool fresh = true;
         ExpandAt at = start;
+        auto chain_done = [&](uint32_t t) { // of turn t, and its base has landed
+            const uint32_t buf = t % kBufs, parity = (t / kBufs) & 1u;
+            if (!bar_wait(bar_base + 8 * buf, parity, abort_flag) || !bar_wait(bar_d + 8 * buf, parity, abort_flag)) return false;
+            fence_after();
+            return true;
+        };
+        auto join = [&](uint32_t t) { // the sum of turn t - 1 joins that of turn t
+            const uint32_t mine = tmem + (r0 << 16) + half * kHalf, to = mine + t % kBufs * kCols, from = mine + (t - 1) % kBufs * kCols;
+#pragma unroll 1
+            for (uint32_t k = 0; k < kHalf; k += 16) {
+                uint32_t d[16], e[16];
+                tmem_ld16(d, to + k);
+                tmem_ld16(e, from + k);
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) + __uint_as_float(e[i]));
+                tmem_st16(to + k, d);
+            }
+            fence_before();
+            bar_arrive(bar_free + 8 * ((t - 1) % kBufs));
+            return true;
+        };
         for (uint32_t u = 0; u < n_units; ++u) {
             const ExpandJob& job = p.job[at.job];
             if (fresh) {
@@ -665,11 +711,18 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 }
             }
             if (!left_out(job, rank)) {
+                if (MANY) { // the chains before the last: each joins the sum of those before it, in its own buffer
+                    bool ok = true;
+                    const uint32_t sources = rank ? job.n_src : 0u;
+                    for (uint32_t g = kChain; g < sources; g += kChain, ++turn) {
+                        ok = chain_done(turn) && (g == kChain || join(turn));
+                        if (!ok) break;
+                    }
+                    if (!ok || (sources > kChain && !(chain_done(turn) && join(turn)))) break;
+                }
                 const uint32_t buf = turn % kBufs, n = at.block * kCols + half * kHalf + (lane & 7u) * (16 / es);
                 uint8_t* mine = rows + (buf * kTile + r0) * kRowBytes; // the warp's rows
-                if (!bar_wait(bar_base + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
-                if (!bar_wait(bar_d + 8 * buf, (turn / kBufs) & 1u, abort_flag)) break;
-                fence_after();
+                if (!chain_done(turn)) break;
                 if (rank || !job.base)
 #pragma unroll
                     for (uint32_t c = 0; c < kHalf; c += 16) {
@@ -1094,6 +1147,14 @@ bs_status launch_shrink(ShrinkParams& p, uint32_t jobs, uint32_t R, const Gpu& g
     default: return launch<lora_shrink_kernel<128, WT>, shrink_threads<128>>(grid, shrink_smem<128, WT>(), p.split, gpu, p);
     }
 }
+template <int R, bool WT, bool BF16>
+bs_status launch_expand_rank(const ExpandParams& p, dim3 grid, const Gpu& gpu) {
+    constexpr uint32_t smem = expand_smem<R, BF16>();
+    if constexpr (WT) // forward has one source
+        for (uint32_t k = 0; k < p.n_jobs; ++k)
+            if (p.job[k].n_src > chain_of<R>) return launch<lora_expand_kernel<R, WT, BF16, true>, kExpandThreads>(grid, smem, 1, gpu, p);
+    return launch<lora_expand_kernel<R, WT, BF16, false>, kExpandThreads>(grid, smem, 1, gpu, p);
+}
 template <bool WT, bool BF16>
 bs_status launch_expand_of(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     p.n_jobs = jobs;
@@ -1102,10 +1163,10 @@ bs_status launch_expand_of(ExpandParams& p, uint32_t jobs, uint32_t R, const Gpu
         units += uint64_t(tile_cap(p.b.tokens, p.b.n, kTile)) * ((p.job[k].width + expand_cols<BF16> - 1) / expand_cols<BF16>);
     const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(units, gpu.sms)));
     switch (R) {
-    case 16: return launch<lora_expand_kernel<16, WT, BF16>, kExpandThreads>(grid, expand_smem<16, BF16>(), 1, gpu, p);
-    case 32: return launch<lora_expand_kernel<32, WT, BF16>, kExpandThreads>(grid, expand_smem<32, BF16>(), 1, gpu, p);
-    case 64: return launch<lora_expand_kernel<64, WT, BF16>, kExpandThreads>(grid, expand_smem<64, BF16>(), 1, gpu, p);
-    default: return launch<lora_expand_kernel<128, WT, BF16>, kExpandThreads>(grid, expand_smem<128, BF16>(), 1, gpu, p);
+    case 16: return launch_expand_rank<16, WT, BF16>(p, grid, gpu);
+    case 32: return launch_expand_rank<32, WT, BF16>(p, grid, gpu);
+    case 64: return launch_expand_rank<64, WT, BF16>(p, grid, gpu);
+    default: return launch_expand_rank<128, WT, BF16>(p, grid, gpu);
     }
 }
 // The jobs of a call may be of both types: those of each go together.
