@@ -211,8 +211,7 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
                 BRows<R>& cur = ring[r];
                 float d[4] = {};
 #pragma unroll
-                for (int m = 0; m < W / WS; ++m) {
-                    if (static_cast<uint32_t>(m) >= steps) break;
+                for (int m = 0; m < W / WS; ++m)
                     if (static_cast<uint32_t>(m) + 1 == steps) {
 #pragma unroll
                         for (int i = 0; i < WS; ++i) {
@@ -221,12 +220,16 @@ __global__ void __launch_bounds__(kFewThreads, R == 16 ? 4 : R <= 64 ? 3 : 2) lo
                         }
                     }
 #pragma unroll
-                    for (int w = m * WS; w < (m + 1) * WS; w += 2) {
-                        const uint32_t af[4] = {cur.lo[w], cur.hi[w], cur.lo[w + 1], cur.hi[w + 1]};
+                for (int t = 2; t >= 0; --t) // small parts first: the sum is rounded at its size R / 16 times, not three times as often
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) mma16816(d, af, hf[w][t], hf[w + 1][t]);
+                    for (int m = 0; m < W / WS; ++m) {
+                        if (static_cast<uint32_t>(m) >= steps) break;
+#pragma unroll
+                        for (int w = m * WS; w < (m + 1) * WS; w += 2) {
+                            const uint32_t af[4] = {cur.lo[w], cur.hi[w], cur.lo[w + 1], cur.hi[w + 1]};
+                            mma16816(d, af, hf[w][t], hf[w + 1][t]);
+                        }
                     }
-                }
                 if (n0 + kAhead<R> * row_deal < rows_end) load(cur, n0 + kAhead<R> * row_deal);
                 float* y = s_y + 2 * q * kHoldRows + (held + r) * 128 + warp * 16 + g;
                 if (2 * q < count) { y[0] = d[0]; y[8] = d[2]; }

@@ -81,3 +81,25 @@ def test_sources_by_the_dozen_are_all_there(tokens, r, dt, sources):
         s.backward(plan, xs, [_dev(v) for v in dys], state, das, dbs, dxs=[dx] * sources, dx_bases=[bd] * sources)
         assert torch.equal(dx.cpu(), want), in_place
     assert int(plan.err) == 0
+
+
+@pytest.mark.parametrize("tokens", [1, 40, 300])
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+def test_lower_parts_are_added_up_before_they_meet_a_large_sum(tokens, r):
+    # h_0 = 2^24, then pairs of 1024 + 15/64 and -1024, whose upper parts cancel: y is 2^24 + (r/2 - 1) 15/64. 8 pairs
+    # are a matrix instruction, 1.875 of the lower parts together: at the size of 2^24 each of them would be lost. Added
+    # up first they are exact, and one rounding towards zero, by less than 2, is left
+    n, rows, cols = 2, 72, 136
+    x = np.zeros((tokens, cols))
+    x[:, 0], x[:, 60], x[:, 130] = 2.0 ** 24, 1024, 15 / 64
+    a = np.zeros((n, r, cols))
+    a[:, 0, 0] = 1
+    a[:, 2::2, 60], a[:, 2::2, 130] = 1, 1
+    a[:, 3::2, 60] = -1
+    b = np.ones((n, rows, r))
+    s = bs.LoraAdapters([_dev(a)], [_dev(b)])
+    plan = bs.LoraPlan(tokens, n).update((torch.arange(tokens, device="cuda") % n).int())
+    y = torch.full((tokens, rows), -2.0 ** 24, device="cuda")
+    s.forward(plan, [_dev(x)], [y])
+    assert int(plan.err) == 0
+    assert float((y.double() - (r // 2 - 1) * 15 / 64).abs().max()) < 2
