@@ -1079,10 +1079,12 @@ class AdamW:
         """One step, enqueued on the stream; with max_norm, grad_norm(max_norm) first. into: a twin
         that receives the results, while this handle's tensors stay as they are. number: the step's
         number (from 1), instead of one more than the last one's."""
-        if max_norm is not None:
-            self.grad_norm(max_norm, stream)
         if into is not None and into.ctl is not self.ctl:
             raise BsError(E_ARG, "adamw", "into: a twin of this handle")
+        if not 0 <= number < 2 ** 31:
+            raise BsError(E_ARG, "adamw", "number: 1 .. 2^31 - 1, or 0")
+        if max_norm is not None:
+            self.grad_norm(max_norm, stream)
         self._prm.step = number
         _on(self._index, "adamw", lib.bs_adamw, self._n, self._items, into._items if into is not None else None,
             ctypes.byref(self._prm), self._at[0], stream=stream)

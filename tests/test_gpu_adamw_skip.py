@@ -166,3 +166,15 @@ def test_a_twin_shares_the_norm_and_the_factor():
     twin.step(into=a)
     b.step()
     assert _same(_held(a), _held(b)) and float(a.clip) == float(twin.clip) == 0.5
+
+
+def test_a_step_that_is_refused_takes_no_norm_and_no_other_number():
+    a, other = _make((300, 5), 32, F32, False), _make((300, 5), 32, F32, False)
+    before = [t.clone() for t in _held(a)] + [a.ctl.clone()]
+    for kw in (dict(into=other), dict(number=-1), dict(number=2 ** 31), dict(number=2 ** 32), dict(number=2 ** 32 + 5), dict(number=-2 ** 32 + 5)):
+        with pytest.raises(bs.BsError) as e:
+            a.step(max_norm=0.01, **kw)
+        assert e.value.code == bs.E_ARG
+    assert _same(before, _held(a) + [a.ctl])
+    a.step(number=2 ** 31 - 1)
+    assert int(a.steps) == 2 ** 31 - 1
