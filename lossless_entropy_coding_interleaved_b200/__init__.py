@@ -1008,8 +1008,8 @@ class AdamW:
         # updated in place, but not overlap otherwise
         self._spans, self._family = spans, _family if _family is not None else weakref.WeakSet()
         for other in self._family:
-            both = sorted({*spans, *other._spans})
-            if any(a[1] > b[0] for a, b in zip(both, both[1:])):
+            both = sorted(spans + other._spans)  # two runs in order: a merge
+            if any(a[1] > b[0] and a != b for a, b in zip(both, both[1:])):
                 raise BsError(E_ARG, "adamw", "a twin's parameters, masters and moments must not overlap its handle's")
         for g in self.grads:  # a gradient may be read by several items, but not written by any
             lo, hi = g.data_ptr(), g.data_ptr() + g.numel() * g.element_size()
