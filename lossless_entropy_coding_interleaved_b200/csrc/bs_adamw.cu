@@ -559,10 +559,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) adamw_kernel(cons
     if (!p.last) return;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    const uint32_t once = __ldcg(&p.ctl->once); // again: it would take a register all the way
+    // again, beside the arrival: kept from above they would take registers all the way
+    const uint32_t once = __ldcg(&p.ctl->once);
+    const float own_clip = __ldcg(&p.ctl->own_clip);
     if (atomicInc(&p.ctl->arrived, gridDim.x - 1) != gridDim.x - 1) return;
     if (!skip) p.ctl->step = p.step ? static_cast<int32_t>(p.step) : p.ctl->step + 1;
-    if (once == 1) p.ctl->clip = p.ctl->own_clip;
+    if (once == 1) p.ctl->clip = own_clip;
     if (once == 3) { // this was the norm's step
         p.ctl->skip = 0;
         p.ctl->once = 1;
@@ -661,6 +663,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     __syncthreads();
     if (!s_last) return;
     __threadfence();
+    const uint32_t once = threadIdx.x == 0 ? __ldcg(&p.ctl->once) : 0;
     double x = 0;
     for (uint32_t i = threadIdx.x; i < p.partial_at + gridDim.x; i += kThreads) x += __ldcg(p.partial + i);
     x = cta_sum(x);
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         const float norm = static_cast<float>(sqrt(x));
         const bool finite = norm < __uint_as_float(0x7F800000u);
         p.ctl->norm = norm;
-        if (p.ctl->once) p.ctl->once = 3;
+        if (once) p.ctl->once = 3;
         p.ctl->skip = finite ? 0u : 1u;
         p.ctl->clip = finite ? static_cast<float>(fmin(1.0, static_cast<double>(p.max_norm) / (sqrt(x) + 1e-6))) : 0.f;
     }
