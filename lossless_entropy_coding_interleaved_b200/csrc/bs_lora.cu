@@ -982,33 +982,39 @@ __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_ke
             const uint32_t acc = kHalves == 2 ? h : c % kAccs, use = kHalves == 2 ? c : c / kAccs;
             if (!bar_wait(bar_d + 8 * acc, use & 1u, abort_flag)) break;
             fence_after();
+            const uint32_t at = tmem + ((warp & 3u) * 32 << 16) + acc * kWide + j0;
+            float odd[2] = {};
 #pragma unroll
             for (uint32_t j = 0; j < kRanks; j += 16) {
-                const uint32_t at = tmem + ((warp & 3u) * 32 << 16) + acc * kWide + j0 + j;
                 uint32_t d[16];
                 if (!special) {
 #pragma unroll
                     for (int part = 2; part >= 0; --part) { // small parts first
-                        tmem_ld16(d, at + part * R);
+                        tmem_ld16(d, at + part * R + j);
 #pragma unroll
                         for (uint32_t i = 0; i < 16; ++i) sum[j + i] += __uint_as_float(d[i]);
                     }
-                    float most = 0.f;
 #pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i) most = max_abs_nan(most, __uint_as_float(d[i]));
-                    if (!__any_sync(0xFFFFFFFFu, within && !(most < kInf))) continue;
-                    special = true;
-#pragma unroll
-                    for (uint32_t i = 0; i < 16; ++i)
-                        if (!(fabsf(__uint_as_float(d[i])) < kInf)) sum[j + i] = __uint_as_float(d[i]); // what it was is finite
+                    for (uint32_t i = 0; i < 16; ++i) odd[i & 1u] = fmaf(__uint_as_float(d[i]), 0.f, odd[i & 1u]); // NaN from the first such number on
                 } else {
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
-                        tmem_ld16(d, at + part * R);
+                        tmem_ld16(d, at + part * R + j);
 #pragma unroll
                         for (uint32_t i = 0; i < 16; ++i)
                             if (part == 0 || fabsf(sum[j + i]) < kInf) sum[j + i] += __uint_as_float(d[i]);
                     }
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, within && odd[0] + odd[1] != 0.f)) { // what such a sum was before is finite
+                special = true;
+#pragma unroll
+                for (uint32_t j = 0; j < kRanks; j += 16) {
+                    uint32_t d[16];
+                    tmem_ld16(d, at + j);
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i)
+                        if (!(fabsf(__uint_as_float(d[i])) < kInf)) sum[j + i] = __uint_as_float(d[i]);
                 }
             }
             fence_before();

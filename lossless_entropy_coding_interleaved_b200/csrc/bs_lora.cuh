@@ -122,11 +122,6 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float max_abs_nan(float a, float b) { // the larger of a and |b|, NaN if either is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-    return r;
-}
 // The three BF16 numbers whose sum is f: each takes 8 bits of what the ones before it left, 24 in
 // all, so a rank-wide FP32 intermediate goes through the BF16 tensor cores without loss. What an
 // infinity or NaN leaves is taken as 0, not as the NaN of inf - inf.
