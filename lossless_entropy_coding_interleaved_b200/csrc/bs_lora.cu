@@ -462,7 +462,7 @@ struct ExpandAt {
 // evenly, in the order job, tile, block, so that a CTA keeps a tile's h for its run of blocks. base's
 // rows are copied to shared memory some blocks ahead, the matrix instructions' sums (128 tokens x the
 // block's columns, in tensor memory) are added to them there, and they leave in lines of 128 bytes.
-// 8192 tokens x 14336 columns, BF16, rank 64: 91 us. Before: 209 us by mma.sync with the sums
+// 8192 tokens x 14336 columns, BF16, rank 64: 94 us (91 with two parts of h). Before: 209 us by mma.sync with the sums
 // going to memory from its registers, 243 us from tensor memory number by number (20 to 33
 // instructions for each 32 of them), 143 us with a bulk copy for each row's 256 or 128 bytes, which
 // the copy engine takes 14 cycles each for.
@@ -800,8 +800,8 @@ constexpr uint32_t outer_load = R > 32 ? 256 : 128;
 constexpr uint32_t kOuterTok = 64;
 // Up to rank 32 a CTA is small and an adapter's tokens are often few, so that its start and end are what
 // it costs: 4 CTAs of 2 stages an SM (3 at rank 32, with one sum in tensor memory). 1003 tokens of 36
-// adapters, gate and up projections: 113 us at rank 16, 220 at rank 32; with 2 CTAs of 3 stages 182
-// and 283. 8192 tokens of 2 adapters, gate: 53 and 68 us, against 59 and 78.
+// adapters, gate and up projections: 131 us at rank 16, 205 at rank 32; with 2 CTAs of 3 stages 182
+// and 283. 8192 tokens of 2 adapters, gate: 56 and 68 us, against 59 and 78.
 template <int R>
 constexpr uint32_t outer_stages = R <= 32 ? 2 : 3;
 constexpr uint32_t outer_ctas(uint32_t R) { return R <= 16 ? 4 : R <= 32 ? 3 : 1; }
@@ -814,7 +814,7 @@ constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(outer_stages<
 constexpr uint32_t kOuterFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
 // Sums in tensor memory: 128 columns x the 3 parts' ranks, beside each other (one matrix instruction
 // reads the columns once for all parts; one for each part read them three times, and 8192 tokens at
-// rank 64 took 135 us, bound by shared memory, against 86 to 93). At rank 16 two of them take turns;
+// rank 64 took 135 us, bound by shared memory, against 94). At rank 16 two of them take turns;
 // rank 64 has one for each 128 of its 256 columns, which are added up two stages apart, so that one
 // half's matrix instructions go on meanwhile; ranks 32 and 128 have one.
 template <int R>
@@ -1128,7 +1128,8 @@ bs_status launch(dim3 grid, uint32_t smem, uint32_t cluster, const Gpu& gpu, con
 // 128, but they pass through tiles that are mostly empty (2 to 2.4 us an adapter). 64 tokens of one
 // adapter: 27 and 33 us here, 22 and 25 us tiled (18 and 22 us at 3584 x 4096, rank 64); 256 tokens of 8:
 // 31 and 39 us, tiled 35 and 41; 512 of 32: 55 and 82, tiled 78 and 92; 1024 of 256: 121 and 223,
-// tiled 514 and 618.
+// tiled 514 and 618. n is the pool's size, all that the host knows: where few adapters of a large pool are in use
+// the rule is off (1000 tokens of one adapter: 32 us tiled, in a pool of up to 8, and 48 us here, in one of 64).
 bool few_tokens(uint32_t tokens, uint32_t n) { return tokens <= kFewTokens && tokens <= 16 * n + 48; }
 
 // CTAs of a cluster that share a sum: the most of 1, 2, 4, 8 that leave each CTA 4 steps and fit into
@@ -1189,6 +1190,8 @@ bs_status launch_expand(const ExpandParams& all, uint32_t jobs, uint32_t R, cons
     }
     return BS_OK;
 }
+// An adapter's tokens are taken to be tokens / n, the pool's share: the plan alone knows better (4096 tokens of one
+// adapter, gradients: 83 us in a pool of 1, 120 us in one of 64).
 bs_status launch_outer(OuterParams& p, uint32_t jobs, uint32_t R, const Gpu& gpu) {
     const uint32_t cols = R == 64 ? outer_cols<64> : outer_cols<128>;
     uint32_t ctas = 0;

@@ -15,9 +15,9 @@
 // is indexed to match. Nothing is staged in shared memory but h. h enters the second product as three
 // BF16 numbers (24 bits).
 //
-// On one B200: one token, q, k and v at rank 16: 9 us with the plan's launch, all of it latency. 37
-// tokens of 24 adapters of rank up to 64, gate and up (14336 x 3584 each): 31 us with the plan's, 88 MB
-// at 2.8 TB/s; with h through memory between two kernels 53 us.
+// On one B200: one token, q, k and v at rank 16: 9.5 us with the plan's launch, all of it latency. 37
+// tokens of 24 adapters of rank up to 64, gate and up (14336 x 3584 each): 32 us with the plan's, 88 MB
+// at 2.7 TB/s; with h through memory between two kernels 53 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
