@@ -28,6 +28,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <iterator>
 
 #include "bs_lora.cuh"
 #include "bs_lora_tc.cuh"
@@ -243,6 +244,8 @@ template <int R, bool WT>
 constexpr uint32_t shrink_smem() {
     return 1024 + std::max<uint32_t>(kShrinkStages * shrink_stage<R, WT>(), kTile * (R + 4) * 4);
 }
+template <int R>
+constexpr uint32_t shrink_tmem = R <= 16 ? 32 : 2 * R; // columns
 constexpr uint32_t kFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
 
 // WT: the weights' rank index is the contiguous one (B), else the summed index is (A).
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(shrink_threads<R>, R <= 64 ? 2 : 1) lora_shrin
     __shared__ __align__(8) uint64_t s_bar[2 * kShrinkStages + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    constexpr uint32_t kTmem = R <= 16 ? 32 : 2 * R, S = kShrinkStages, kShrinkOut = shrink_out<R>, kRanks = R > 64 ? 64 : R;
+    constexpr uint32_t kTmem = shrink_tmem<R>, S = kShrinkStages, kShrinkOut = shrink_out<R>, kRanks = R > 64 ? 64 : R;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     const uint32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;
     const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -810,7 +813,10 @@ constexpr uint32_t outer_threads = outer_out<R> + outer_load<R> + 32;
 template <int R>
 __host__ __device__ constexpr uint32_t outer_stage() { return outer_cols<R> * 128 + 8192 * ((3 * R + 63) / 64); }
 template <int R>
-constexpr uint32_t outer_smem() { return 1024 + std::max<uint32_t>(outer_stages<R> * outer_stage<R>(), outer_cols<R> * (R + 4) * 4); }
+constexpr uint32_t outer_smem() {
+    // rank 64: 9 KB more than it uses, so that no CTA of rank 16 fits beside one (see kClustered)
+    return std::max<uint32_t>(R == 64 ? 178 * 1024 : 0, 1024 + std::max<uint32_t>(outer_stages<R> * outer_stage<R>(), outer_cols<R> * (R + 4) * 4));
+}
 constexpr uint32_t kOuterFlush = 4; // stages whose sums stay in tensor memory: chains of 16 matrix instructions
 // Sums in tensor memory: 128 columns x the 3 parts' ranks, beside each other (one matrix instruction
 // reads the columns once for all parts; one for each part read them three times, and 8192 tokens at
@@ -819,12 +825,40 @@ constexpr uint32_t kOuterFlush = 4; // stages whose sums stay in tensor memory: 
 // half's matrix instructions go on meanwhile; ranks 32 and 128 have one.
 template <int R>
 constexpr uint32_t outer_accs = R == 16 || R == 64 ? 2 : 1;
+template <int R>
+constexpr uint32_t outer_tmem = R <= 32 ? 128 : 512; // columns, a power of two
+
+// Two of these kernels may run at a time, on two streams. The CTAs of a cluster wait for each other, so if tensor
+// memory ran out, a CTA could wait for that of another kernel's cluster, which waits for a peer that waits
+// for this cluster's, for good. Shared memory has to keep CTAs apart that take more than the SM's 512
+// columns together: whatever of them it holds at a time must find its columns.
+struct Takes {
+    uint32_t tmem, smem;
+};
+constexpr uint32_t kSmShared = 228 * 1024, kCtaShared = 1024; // of an SM, and what a CTA takes of it besides its own
+constexpr Takes kClustered[] = {
+    {shrink_tmem<16>, shrink_smem<16, false>()}, {shrink_tmem<16>, shrink_smem<16, true>()}, {shrink_tmem<32>, shrink_smem<32, false>()},
+    {shrink_tmem<32>, shrink_smem<32, true>()}, {shrink_tmem<64>, shrink_smem<64, false>()}, {shrink_tmem<64>, shrink_smem<64, true>()},
+    {shrink_tmem<128>, shrink_smem<128, false>()}, {shrink_tmem<128>, shrink_smem<128, true>()}, {outer_tmem<16>, outer_smem<16>()},
+    {outer_tmem<32>, outer_smem<32>()}, {outer_tmem<64>, outer_smem<64>()}, {outer_tmem<128>, outer_smem<128>()}};
+constexpr uint32_t most_columns(uint32_t from, uint32_t smem_left) { // of kinds `from` and later, that fit
+    uint32_t most = 0;
+    for (uint32_t k = from; k < std::size(kClustered); ++k) {
+        const uint32_t need = kClustered[k].smem + kCtaShared;
+        if (need > smem_left) continue;
+        const uint32_t all = kClustered[k].tmem + most_columns(k, smem_left - need);
+        most = all > most ? all : most;
+    }
+    return most;
+}
+static_assert(most_columns(0, kSmShared) <= 512, "CTAs that fit beside each other take more tensor memory than there is");
 
 template <int R>
 __global__ void __launch_bounds__(outer_threads<R>, outer_ctas(R)) lora_outer_kernel(const __grid_constant__ OuterParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr uint32_t S = outer_stages<R>, kOuterCols = outer_cols<R>, kHalves = kOuterCols / 128, kAccs = outer_accs<R>, kWide = 3 * R;
-    constexpr uint32_t kTmem = R <= 32 ? 128 : 512; // at least kAccs * kWide, a power of two
+    constexpr uint32_t kTmem = outer_tmem<R>;
+    static_assert(kTmem >= kAccs * kWide);
     constexpr uint32_t kStage = outer_stage<R>(), kRanks = R > 64 ? 64 : R, kOuterOut = outer_out<R>, kOuterThreads = outer_threads<R>;
     constexpr uint32_t kOuterLoad = outer_load<R>;
     __shared__ __align__(8) uint64_t s_bar[2 * S + 4];

@@ -185,3 +185,19 @@ def test_the_check_answers_what_the_call_would():
         assert check([_item(**kw)]) == _forward([_item(**kw)]) == bs.E_ARG, kw
     assert check([_item()], _batch(rank_max=12)) == bs.E_ARG and check([_item(), _item()]) == bs.E_ARG
     assert L.bs_lora_forward_check(-1, None, ctypes.byref(_batch())) == bs.E_ARG and L.bs_lora_forward_check(1, None, None) == bs.E_ARG
+
+
+def test_what_an_sm_holds_of_clustered_kernels_finds_its_tensor_memory():
+    # checked when the library is compiled; here: that it still is, of every kernel that is launched as a cluster and
+    # takes tensor memory, by the sizes that the launches use
+    src = _source("bs_lora.cu")
+    assert "static_assert(most_columns(0, kSmShared) <= 512" in src
+    table = src[src.index("kClustered[] = {"):src.index("constexpr uint32_t most_columns")]
+    for r in (16, 32, 64, 128):
+        for wt in ("false", "true"):
+            assert f"{{shrink_tmem<{r}>, shrink_smem<{r}, {wt}>()}}" in table
+        assert f"{{outer_tmem<{r}>, outer_smem<{r}>()}}" in table
+        assert f"launch<lora_shrink_kernel<{r}, WT>, shrink_threads<{r}>>(grid, shrink_smem<{r}, WT>(), p.split" in src
+        assert f"launch<lora_outer_kernel<{r}>, outer_threads<{r}>>(grid, outer_smem<{r}>(), p.split" in src
+    assert src.count("constexpr uint32_t kTmem = shrink_tmem<R>") == src.count("constexpr uint32_t kTmem = outer_tmem<R>") == 1
+    assert re.findall(r"lora_expand_kernel<[^;]*>\(grid, smem, (\d)", src) == ["1", "1"]  # no cluster
