@@ -141,3 +141,30 @@ def test_calls_whose_x_the_call_before_wrote(tokens):
         product([(fw, info, width, width, bufs[2], out)], err)
         assert all(torch.equal(a, b) for a, b in zip(bufs, want)) and torch.equal(out, got)
     assert int(err) == 0 and int(plan.err) == 0
+
+
+@pytest.mark.parametrize("pairs", [((16, 300), (64, 300)), ((64, 1500), (8, 1500)), ((128, 300), (16, 900)), ((32, 700), (32, 40)), ((64, 400), (64, 400))])
+def test_two_batches_at_once_on_two_streams(pairs):
+    made, streams = [], [torch.cuda.Stream() for _ in pairs]
+    for seed, (r, tokens) in enumerate(pairs):
+        m = Made(tokens, r, [(1024, 512), (512, 512)], n=5, seed=seed)
+        m.x, m.dy = [_dev(m.whole(tokens, 512))] * 2, [_dev(m.whole(tokens, rows, most=1)) for rows, _ in m.projs]
+        m.state, m.work = m.set.state(tokens), m.set.state(tokens)
+
+        def go(m=m, stream=None):
+            o = dict(ys=[torch.zeros(m.tokens, rows, device="cuda") for rows, _ in m.projs], das=[torch.zeros(v.shape, device="cuda") for v in m.a],
+                     dbs=[torch.zeros(v.shape, device="cuda") for v in m.b], dx=[torch.zeros(m.tokens, 512, device="cuda")])
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            for _ in range(30):
+                m.set.forward(m.plan, m.x, o["ys"], [None] * 2, state=m.state, stream=stream)
+                m.set.backward(m.plan, m.x, m.dy, m.state, o["das"], o["dbs"], o["dx"] * 2, work=m.work, stream=stream)
+            return o
+        made.append(go)
+    alone = [go() for go in made]
+    torch.cuda.synchronize()
+    together = [go(stream=s) for go, s in zip(made, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, together):
+        for k in a:
+            assert all(torch.equal(u, v) for u, v in zip(a[k], b[k])), k
