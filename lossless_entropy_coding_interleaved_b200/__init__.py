@@ -1026,7 +1026,7 @@ class AdamW:
             it.n, it.param_type, it.grad_type = sizes[k], _TYPES[self.params[k].dtype], _TYPES[self.grads[k].dtype]
             it.weight_decay = decay[k]
         self._n, self._sizes, self._index = n, sizes, self.params[0].get_device()
-        self._prm = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
+        self._prm = self._numbered = AdamWParams(betas[0], betas[1], eps, bits, 0, seed & (2 ** 64 - 1))
         self.ctl = torch.zeros(8, dtype=torch.int32, device=dev) if _ctl is None else _ctl
         f = self.ctl.view(torch.float32)
         self._lr, self._clip, self.norm, self.steps = f[0], f[1], f[4], self.ctl[2]
@@ -1085,9 +1085,12 @@ class AdamW:
             raise BsError(E_ARG, "adamw", "number: 1 .. 2^31 - 1, or 0")
         if max_norm is not None:
             self.grad_norm(max_norm, stream)
-        self._prm.step = number
+        numbered = self._numbered  # never changed once made: another thread's call may be reading it
+        if numbered.step != number:
+            p = self._prm
+            self._numbered = numbered = AdamWParams(p.beta1, p.beta2, p.eps, p.bits, number, p.seed)
         _on(self._index, "adamw", lib.bs_adamw, self._n, self._items, into._items if into is not None else None,
-            ctypes.byref(self._prm), self._at[0], stream=stream)
+            ctypes.byref(numbered), self._at[0], stream=stream)
 
     def read_states(self, ms=None, vs=None, stream=None):
         """The moments as float32 lists, (exp_avgs, exp_avg_sqs). 32-bit moments are returned as they

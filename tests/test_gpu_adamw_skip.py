@@ -178,3 +178,20 @@ def test_a_step_that_is_refused_takes_no_norm_and_no_other_number():
     assert _same(before, _held(a) + [a.ctl])
     a.step(number=2 ** 31 - 1)
     assert int(a.steps) == 2 ** 31 - 1
+
+
+def test_a_step_keeps_its_number_whatever_other_threads_step(monkeypatch):
+    # another thread's step between a call's own preparation and its launch
+    a, b = (_make((300, 5), 8, F32, False) for _ in range(2))
+    launch, others = bs._on, [9, 0, 7]
+
+    def on(index, what, fn, *args, **kw):
+        if others:
+            a.step(number=others.pop())
+        return launch(index, what, fn, *args, **kw)
+    monkeypatch.setattr(bs, "_on", on)
+    a.step(number=5)
+    monkeypatch.setattr(bs, "_on", launch)
+    for number in (9, 0, 7, 5):  # the innermost is launched first
+        b.step(number=number)
+    assert int(a.steps) == 5 and _same(_held(a), _held(b))
